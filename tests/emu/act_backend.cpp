@@ -1,0 +1,404 @@
+// Host stand-in for the device side of the activation operators (tests only):
+// every launch is carried out lane by lane on host memory with the kernels'
+// own index functions (ua2a_act_geometry.h), the arithmetic written plainly.
+// Each access is checked against the size of the buffer it belongs to, and
+// each output byte may be written once; a violation sets an error that the
+// test reads.  The exchange's own launches are not part of this library.
+#include <immintrin.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <vector>
+
+#include "ua2a_act_internal.h"
+
+using namespace ua2a;
+
+namespace {
+
+int g_error = 0;              // first violation: 1 read, 2 write, 3 written twice
+int g_launches = 0;
+ActLaunch g_last;
+
+void flag(int e)
+{
+    if (!g_error) g_error = e;
+}
+
+struct Buf {
+    uint8_t* p;
+    int64_t bytes;
+    std::vector<uint8_t> hits;
+    Buf(const void* q, int64_t n) : p(static_cast<uint8_t*>(const_cast<void*>(q))), bytes(q ? n : 0) {}
+    bool in(int64_t at, int64_t n) const { return at >= 0 && at + n <= bytes; }
+    bool write(int64_t at, int64_t n)
+    {
+        if (!in(at, n)) {
+            flag(2);
+            return false;
+        }
+        if (hits.empty()) hits.assign(static_cast<size_t>(bytes), 0);
+        for (int64_t k = at; k < at + n; ++k)
+            if (hits[static_cast<size_t>(k)]++) flag(3);
+        return true;
+    }
+};
+
+float bits_f(uint32_t u)
+{
+    float f;
+    memcpy(&f, &u, 4);
+    return f;
+}
+uint32_t f_bits(float f)
+{
+    uint32_t u;
+    memcpy(&u, &f, 4);
+    return u;
+}
+
+// one value of the type at element `at`
+float get(const Buf& b, int64_t at, int32_t type)
+{
+    const int64_t e = type == UA2A_TYPE_FP32 ? 4 : 2;
+    if (!b.in(at * e, e)) {
+        flag(1);
+        return 0.f;
+    }
+    if (type == UA2A_TYPE_FP32) {
+        float f;
+        memcpy(&f, b.p + at * 4, 4);
+        return f;
+    }
+    uint16_t u;
+    memcpy(&u, b.p + at * 2, 2);
+    if (type == UA2A_TYPE_BF16) return bits_f(uint32_t(u) << 16);
+    return _cvtsh_ss(u);
+}
+
+float round_to(float f, int32_t type)
+{
+    if (type == UA2A_TYPE_FP32) return f;
+    if (type == UA2A_TYPE_FP16) return _cvtsh_ss(_cvtss_sh(f, 0));
+    if (f != f) return f;
+    uint32_t u = f_bits(f);
+    u += 0x7fffu + ((u >> 16) & 1);
+    return bits_f(u & 0xffff0000u);
+}
+
+void put(Buf& b, int64_t at, float f, int32_t type)
+{
+    const int64_t e = type == UA2A_TYPE_FP32 ? 4 : 2;
+    if (!b.write(at * e, e)) return;
+    if (type == UA2A_TYPE_FP32) {
+        memcpy(b.p + at * 4, &f, 4);
+        return;
+    }
+    uint16_t u;
+    if (type == UA2A_TYPE_BF16) {
+        u = static_cast<uint16_t>(f_bits(round_to(f, type)) >> 16);
+    } else {
+        u = _cvtss_sh(f, 0);
+    }
+    memcpy(b.p + at * 2, &u, 2);
+}
+
+void put8(Buf& b, int64_t at, uint8_t v)
+{
+    if (b.write(at, 1)) b.p[at] = v;
+}
+uint8_t get8(const Buf& b, int64_t at)
+{
+    if (b.in(at, 1)) return b.p[at];
+    flag(1);
+    return 0;
+}
+
+struct Format {
+    int mantissa, bias;
+    uint8_t nan, inf;
+    double most;
+};
+Format format_of(int32_t f)
+{
+    if (f == UA2A_FORMAT_E4M3) return {3, 7, 0x7f, 0x7f, 448.0};
+    return {2, 15, 0x7f, 0x7c, 57344.0};
+}
+
+double code_value(uint8_t c, int32_t f)
+{
+    const Format q = format_of(f);
+    const int mag = c & 0x7f, e = mag >> q.mantissa, m = mag & ((1 << q.mantissa) - 1);
+    double v;
+    if (f == UA2A_FORMAT_E4M3 ? mag == 0x7f : mag > 0x7c)
+        v = NAN;
+    else if (f == UA2A_FORMAT_E5M2 && mag == 0x7c)
+        v = INFINITY;
+    else if (e == 0)
+        v = ldexp(m, 1 - q.bias - q.mantissa);
+    else
+        v = ldexp((1 << q.mantissa) + m, e - q.bias - q.mantissa);
+    return (c & 0x80) ? -v : v;
+}
+
+uint8_t code_of(double x, int32_t f)
+{
+    const Format q = format_of(f);
+    const uint8_t sign = signbit(x) ? 0x80 : 0;
+    if (x != x) return sign | q.nan;
+    if (isinf(x)) return sign | q.inf;
+    const double a = fabs(x);
+    if (a == 0) return sign;
+    int e;
+    frexp(a, &e);
+    e -= 1;
+    if (e < 1 - q.bias) e = 1 - q.bias;
+    double n = nearbyint(ldexp(a, q.mantissa - e));            // steps of the value's size
+    if (n >= (2 << q.mantissa)) {
+        n /= 2;
+        e += 1;
+    }
+    if (n < (1 << q.mantissa)) return sign | static_cast<uint8_t>(n);   // subnormal
+    return sign | static_cast<uint8_t>(((e + q.bias) << q.mantissa) + (static_cast<int>(n) - (1 << q.mantissa)));
+}
+
+// scale exponent of a block's values, by search
+int scale_exponent(const std::vector<float>& v, int32_t f)
+{
+    double m = 0;
+    for (float x : v)
+        if (isfinite(x) && fabs(x) > m) m = fabs(x);
+    int k = -127;
+    while (k < 127 && m > ldexp(format_of(f).most, k)) ++k;
+    return k;
+}
+
+// quantises a head (D values) and stores codes and scales
+void put_head(Buf& codes, Buf& scales, int64_t at, int64_t scale0, const std::vector<float>& v, int32_t f)
+{
+    for (size_t lo = 0; lo < v.size(); lo += kBlockValues) {
+        const size_t hi = lo + kBlockValues < v.size() ? lo + kBlockValues : v.size();
+        const int k = scale_exponent(std::vector<float>(v.begin() + lo, v.begin() + hi), f);
+        for (size_t i = lo; i < hi; ++i) put8(codes, at + i, code_of(ldexp(static_cast<double>(v[i]), -k), f));
+        put8(scales, scale0 + lo / kBlockValues, static_cast<uint8_t>(k + 127));
+    }
+}
+
+// Every lane slot of a norm launch: fn(segment, slot), in the kernel's order.
+template <class F>
+void norm_lanes(const ActLaunch& L, const NormGeom& g, F fn)
+{
+    for (uint32_t wg = 0; wg < L.grid_x; ++wg)
+        for (uint32_t group = wg; group < g.groups; group += L.grid_x)
+            for (uint32_t tid = 0; tid < L.block; ++tid) {
+                const Segment s = segment_of(g, group, tid, L.block);
+                if (!s.live) continue;
+                const uint32_t lane = tid & ((1u << g.lanes_log) - 1);
+                for (int32_t it = 0; it < L.items; ++it) {
+                    const Slot sl = slot_of(g, lane + (static_cast<uint32_t>(it) << g.lanes_log),
+                                            static_cast<uint32_t>(L.V));
+                    if (sl.ok) fn(s, sl);
+                }
+            }
+}
+
+int64_t scales_of(const NormGeom& g) { return int64_t(g.segs) * (g.per_head ? 1 : g.sh.H) * g.sh.nb; }
+int64_t values_of(const NormGeom& g) { return int64_t(g.segs) * g.len; }
+
+void norm(const ActLaunch& L)
+{
+    const NormArgs& a = L.norm;
+    const NormGeom& g = a.g;
+    const int64_t n = values_of(g), e = L.type == UA2A_TYPE_FP32 ? 4 : 2;
+    Buf x(a.x, n * e), res(a.residual, n * e), w(a.weight, int64_t(g.len) * (a.weight_f32 ? 4 : e));
+    Buf out(a.out, a.out_format ? n : n * e), osc(a.out_scales, scales_of(g)), sum(a.sum, n * e), saved(a.saved, n),
+        ssc(a.saved_scales, scales_of(g)), rstd(a.rstd, int64_t(g.segs) * 4);
+    std::vector<double> ss(g.segs, 0.0);
+    std::vector<float> h(static_cast<size_t>(n)), y(static_cast<size_t>(n));   // P order
+    norm_lanes(L, g, [&](const Segment& s, const Slot& sl) {
+        for (int32_t i = 0; i < L.V; ++i) {
+            const int64_t p = value_at(g, s, sl, false) + i;
+            float v = get(x, value_at(g, s, sl, L.mode) + i, L.type);
+            if (res.p) {
+                v = round_to(v + get(res, p, L.type), L.type);
+                put(sum, p, v, L.type);
+            }
+            h[static_cast<size_t>(p)] = v;
+            ss[s.seg] += double(v) * v;
+        }
+    });
+    norm_lanes(L, g, [&](const Segment& s, const Slot& sl) {
+        const double r = 1.0 / sqrt(ss[s.seg] / g.len + a.eps);
+        for (int32_t i = 0; i < L.V; ++i) {
+            const int64_t p = value_at(g, s, sl, false) + i;
+            const float wt = w.p ? get(w, int64_t(sl.hh) * g.sh.D + sl.d + i, a.weight_f32 ? UA2A_TYPE_FP32 : L.type) : 1.f;
+            y[static_cast<size_t>(p)] = static_cast<float>(h[static_cast<size_t>(p)] * r * wt);
+            if (!a.out_format) put(out, value_at(g, s, sl, !L.mode) + i, y[static_cast<size_t>(p)], L.type);
+        }
+        if (rstd.p && sl.hh == 0 && sl.d == 0) put(rstd, s.seg, static_cast<float>(r), UA2A_TYPE_FP32);
+        if (sl.d == 0) {                                        // a head's first slot: the whole head's 8 bits
+            const int64_t p = value_at(g, s, sl, false);
+            const auto head = [&](const std::vector<float>& v) {
+                return std::vector<float>(v.begin() + p, v.begin() + p + g.sh.D);
+            };
+            if (a.saved_format)
+                put_head(saved, ssc, p, scale_at(g, s, sl, false), head(h), a.saved_format);
+        }
+    });
+    if (a.out_format)
+        norm_lanes(L, g, [&](const Segment& s, const Slot& sl) {
+            if (sl.d != 0) return;
+            const int64_t p = value_at(g, s, sl, false);
+            put_head(out, osc, value_at(g, s, sl, !L.mode), scale_at(g, s, sl, !L.mode),
+                     std::vector<float>(y.begin() + p, y.begin() + p + g.sh.D), a.out_format);
+        });
+}
+
+void norm_grad(const ActLaunch& L)
+{
+    const NormGradArgs& a = L.grad;
+    const NormGeom& g = a.g;
+    const int64_t n = values_of(g), e = L.type == UA2A_TYPE_FP32 ? 4 : 2;
+    Buf dy(a.dy, n * e), dsum(a.dsum, n * e), saved(a.saved, a.saved_format ? n : n * e), ssc(a.saved_scales, scales_of(g)),
+        w(a.weight, int64_t(g.len) * (a.weight_f32 ? 4 : e)), rstd(a.rstd, int64_t(g.segs) * 4);
+    Buf dx(a.dx, n * e), dres(a.dresidual, n * e), partial(a.partial, int64_t(L.grid_x) * g.len * 4);
+    std::vector<double> dot(g.segs, 0.0), dw(g.len, 0.0);
+    const auto each = [&](const Segment& s, const Slot& sl, int32_t i, double* gy, double* nh, double* d) {
+        *d = get(dy, value_at(g, s, sl, !L.mode) + i, L.type);
+        double h;
+        if (a.saved_format)
+            h = code_value(get8(saved, value_at(g, s, sl, false) + i), a.saved_format) *
+                ldexp(1.0, get8(ssc, scale_at(g, s, sl, false)) - 127);
+        else
+            h = get(saved, value_at(g, s, sl, a.saved_gathered) + i, L.type);
+        const float wt = w.p ? get(w, int64_t(sl.hh) * g.sh.D + sl.d + i, a.weight_f32 ? UA2A_TYPE_FP32 : L.type) : 1.f;
+        *nh = h * get(rstd, s.seg, UA2A_TYPE_FP32);
+        *gy = *d * wt;
+    };
+    norm_lanes(L, g, [&](const Segment& s, const Slot& sl) {
+        for (int32_t i = 0; i < L.V; ++i) {
+            double gy, nh, d;
+            each(s, sl, i, &gy, &nh, &d);
+            dot[s.seg] += gy * nh;
+            dw[sl.hh * g.sh.D + sl.d + i] += d * nh;
+        }
+    });
+    norm_lanes(L, g, [&](const Segment& s, const Slot& sl) {
+        for (int32_t i = 0; i < L.V; ++i) {
+            double gy, nh, d;
+            each(s, sl, i, &gy, &nh, &d);
+            const int64_t p = value_at(g, s, sl, false) + i;
+            double r = get(rstd, s.seg, UA2A_TYPE_FP32) * (gy - nh * dot[s.seg] / g.len);
+            if (dsum.p) r += get(dsum, p, L.type);
+            put(dx, L.mode ? value_at(g, s, sl, true) + i : p, static_cast<float>(r), L.type);
+            if (dres.p) put(dres, p, static_cast<float>(r), L.type);
+        }
+    });
+    if (partial.p)                                              // everything in the first workgroup's row
+        for (int64_t k = 0; k < int64_t(L.grid_x) * g.len; ++k)
+            put(partial, k, k < g.len ? static_cast<float>(dw[static_cast<size_t>(k)]) : 0.f, UA2A_TYPE_FP32);
+}
+
+void columns(const ActLaunch& L)
+{
+    const ColumnArgs& a = L.columns;
+    Buf in(a.partial, int64_t(a.rows) * a.cols * 4), out(a.out, int64_t(a.cols) * 4);
+    for (uint32_t c = 0; c < L.grid_x * 32; ++c) {
+        if (c >= a.cols) continue;
+        float t = 0.f;
+        for (uint32_t r = 0; r < a.rows; ++r) t += get(in, int64_t(r) * a.cols + c, UA2A_TYPE_FP32);
+        put(out, c, t, UA2A_TYPE_FP32);
+    }
+}
+
+void cache(const ActLaunch& L, bool write)
+{
+    const CacheArgs& a = L.cache;
+    const CacheGeom& g = a.g;
+    const int64_t e = L.type == UA2A_TYPE_FP32 ? 4 : 2, nval = int64_t(g.rows) * (write ? g.sh.H : g.sh.hl) * g.sh.D;
+    Buf codes(a.codes, 2 * g.part), scales(a.scales, 2 * g.part_scales);
+    for (uint32_t y = 0; y < L.grid_y; ++y) {
+        Buf val(write ? (y ? a.v : a.k) : (y ? a.v_out : a.k_out), nval * e);
+        if (!val.p) continue;
+        for (uint64_t id = 0; id < uint64_t(L.grid_x) * L.block; ++id) {
+            if (id >= uint64_t(g.rows) * g.slots) continue;
+            const CacheSlot s = cache_slot(g, static_cast<uint32_t>(id), static_cast<uint32_t>(L.V), write);
+            if (s.i >= g.seqs) {
+                flag(1);
+                continue;
+            }
+            const int64_t row = cache_row(g, s, a.starts, a.counts);
+            if (row < 0 || s.d >= g.sh.D) continue;
+            if (write) {
+                const int64_t head = row * g.sh.hl + (s.h - s.r * g.sh.hl);
+                if (s.d != 0) continue;                         // a head's first slot does the head
+                std::vector<float> v;
+                for (uint32_t i = 0; i < g.sh.D; ++i)
+                    v.push_back(get(val, (int64_t(s.row) * g.sh.H + s.h) * g.sh.D + i, L.type));
+                put_head(codes, scales, (y ? g.part : 0) + head * g.sh.D, (y ? g.part_scales : 0) + head * g.sh.nb, v,
+                         a.format);
+            } else {
+                const int64_t head = row * g.sh.hl + s.h;
+                for (int32_t i = 0; i < L.V; ++i) {
+                    double f = code_value(get8(codes, (y ? g.part : 0) + head * g.sh.D + s.d + i), a.format) *
+                               ldexp(1.0, get8(scales, (y ? g.part_scales : 0) + head * g.sh.nb + s.blk) - 127);
+                    const double most = L.type == UA2A_TYPE_FP16 ? 65504.0
+                                        : bits_f(L.type == UA2A_TYPE_FP32 ? 0x7f7fffffu : 0x7f7f0000u);
+                    if (isfinite(f) && fabs(f) > most) f = f < 0 ? -most : most;
+                    put(val, (int64_t(s.row) * g.sh.hl + s.h) * g.sh.D + s.d + i, static_cast<float>(f), L.type);
+                }
+            }
+        }
+    }
+}
+
+}  // namespace
+
+namespace ua2a {
+
+int act_launch(const ActLaunch& L, void*)
+{
+    ++g_launches;
+    g_last = L;
+    switch (L.kernel) {
+    case ActKernel::Norm: norm(L); break;
+    case ActKernel::NormGrad: norm_grad(L); break;
+    case ActKernel::Columns: columns(L); break;
+    case ActKernel::CacheWrite: cache(L, true); break;
+    case ActKernel::CacheRead: cache(L, false); break;
+    }
+    return 0;
+}
+
+int backend_current_device(int32_t* device)
+{
+    *device = 0;
+    return 0;
+}
+int backend_launch(const Launch&, void*) { return -1; }
+const char* backend_error_name(int) { return "emulated"; }
+int backend_scratch_window(int32_t, uint8_t**) { return -1; }
+
+}  // namespace ua2a
+
+extern "C" {
+int ua2a_act_emu_error() { return g_error; }
+int ua2a_act_emu_launches() { return g_launches; }
+void ua2a_act_emu_reset()
+{
+    g_error = 0;
+    g_launches = 0;
+}
+int ua2a_act_emu_last(int what)   // 0 V, 1 items, 2 block, 3 grid, 4 lanes
+{
+    const NormGeom& g = g_last.kernel == ActKernel::NormGrad ? g_last.grad.g : g_last.norm.g;
+    switch (what) {
+    case 0: return g_last.V;
+    case 1: return g_last.items;
+    case 2: return static_cast<int>(g_last.block);
+    case 3: return static_cast<int>(g_last.grid_x);
+    default: return 1 << g.lanes_log;
+    }
+}
+}

@@ -21,7 +21,9 @@ heads and gathers the sequence, mode 1 is its inverse, chunked runs the same
 exchange one batch plane at a time through a window sized for one plane.)
 ``Plan.exchange_ranks`` runs it between per-rank tensors (one allocation
 each, the ranks' shapes without the leading w), optionally only for the runs
-a range of ranks sends.
+a range of ranks sends.  The operators of include/ua2a_act.h (RMS norms joined
+with the exchange, 8-bit checkpoints, the 8-bit key/value cache) are methods
+of ``Plan`` too; see ``activations.py``.
 """
 from __future__ import annotations
 
@@ -99,7 +101,7 @@ def load_library() -> ctypes.CDLL:
         raise RuntimeError(
             f"{LIBRARY} is missing: build it with `python -m ulysses_all_re_amd.build` "
             "(the exchange has no non-HIP implementation)")
-    _lib = declare_signatures(ctypes.CDLL(LIBRARY))
+    _lib = declare_activation_signatures(declare_signatures(ctypes.CDLL(LIBRARY)))
     return _lib
 
 
@@ -277,6 +279,11 @@ def ua2a_describe(plan: int, mode: int, chunked: int, inp: int, out: int) -> dic
     return {name: getattr(info, name) for name, _ in ua2a_launch_info_t._fields_}
 
 
+# the operators of include/ua2a_act.h: norms joined with the exchange, the 8-bit cache
+from .activations import (  # noqa: E402  (uses the names above)
+    ActivationCalls, Cache, NormExchange, NormGradients, declare_activation_signatures)
+
+
 # ------------------------------------------------------------- torch wrapper
 
 def _current_raw_stream(device) -> int:
@@ -289,7 +296,7 @@ def _current_raw_stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-class Plan:
+class Plan(ActivationCalls):
     """A ua2a plan bound to torch tensors on one device.
 
     ``window``: optional device tensor used as the one-plane window of

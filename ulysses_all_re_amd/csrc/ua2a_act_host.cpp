@@ -1,0 +1,438 @@
+// Host side of the activation operators' C ABI (ua2a_act.h): argument checks,
+// launch shapes and launches.  Like the exchange's calls, each validates every
+// pointer and range before it launches, judges overlap by byte ranges, and
+// disables the plan for good when a launch fails.
+#include <math.h>
+#include <stdio.h>
+#include <string.h>
+
+#include "ua2a_act_internal.h"
+
+using namespace ua2a;
+
+namespace {
+
+constexpr int64_t kMaxSegments = int64_t(1) << 31;
+constexpr int64_t kMaxSlots = int64_t(kMaxGridWorkItems) - kActBlock;    // lane slots of a cache call
+constexpr int64_t kMaxCacheValues = int64_t(1) << 38;
+constexpr uint32_t kNormGrid = 4096;       // most workgroups of a forward launch
+constexpr uint32_t kGradGrid = 1024;       // ... of a backward launch, each with a row of partial sums
+
+struct Range {
+    const void* p;
+    int64_t bytes;
+};
+
+bool overlap(const Range& a, const Range& b)
+{
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+    return a.p != nullptr && b.p != nullptr && a.bytes > 0 && b.bytes > 0 &&
+           pa < pb + static_cast<uintptr_t>(b.bytes) && pb < pa + static_cast<uintptr_t>(a.bytes);
+}
+
+// Whether an output overlaps another output or an input.
+bool aliased(const Range* outs, int nouts, const Range* ins, int nins)
+{
+    for (int i = 0; i < nouts; ++i) {
+        for (int k = i + 1; k < nouts; ++k)
+            if (overlap(outs[i], outs[k])) return true;
+        for (int k = 0; k < nins; ++k)
+            if (overlap(outs[i], ins[k])) return true;
+    }
+    return false;
+}
+
+bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+int32_t type_bytes(int32_t type)
+{
+    return type == UA2A_TYPE_FP32 ? 4 : type == UA2A_TYPE_BF16 || type == UA2A_TYPE_FP16 ? 2 : 0;
+}
+
+bool good_format(int32_t f) { return f == UA2A_FORMAT_E4M3 || f == UA2A_FORMAT_E5M2; }
+
+int fail(ua2a_plan_t plan, const char* what, int err)
+{
+    plan->disabled = 1;
+    snprintf(plan->reason, sizeof plan->reason, "%s failed: %s", what, backend_error_name(err));
+    return UA2A_ERR_HIP;
+}
+
+int check_device(ua2a_plan_t plan)
+{
+    int32_t dev = -1;
+    const int err = backend_current_device(&dev);
+    if (err != 0) return fail(plan, "querying the current device", err);
+    return dev == plan->device ? UA2A_OK : UA2A_ERR_DEVICE;
+}
+
+int64_t tokens_of(const ua2a_plan_s* p) { return p->layout.tensor_elems / (p->H * p->D); }
+
+ActShape shape_of(const ua2a_plan_s* p)
+{
+    ActShape g;
+    g.H = static_cast<uint32_t>(p->H);
+    g.D = static_cast<uint32_t>(p->D);
+    g.nb = static_cast<uint32_t>((p->D + kBlockValues - 1) / kBlockValues);
+    g.hl = static_cast<uint32_t>(p->H / p->w);
+    g.S = static_cast<uint32_t>(p->S_local);
+    g.B = static_cast<uint32_t>(p->B);
+    g.SG = static_cast<uint32_t>(p->S_local * p->w);           // < 2^32 by the plan's limits
+    g.d_hl = make_div32(g.hl);
+    g.d_S = make_div32(g.S);
+    g.d_B = make_div32(g.B);
+    const int64_t rows = p->B * p->S_local * p->w;             // of one A rank
+    g.a_rank = rows * g.hl * g.D;
+    g.a_rank_scales = rows * g.hl * g.nb;
+    return g;
+}
+
+uint32_t log2_of(uint32_t pow2)
+{
+    uint32_t l = 0;
+    while ((1u << l) < pow2) ++l;
+    return l;
+}
+
+// Segments, lanes and slots of a norm with V values per slot.  A segment of
+// up to 64 slots gets a lane for each (the next power of two); a longer one
+// the fewest of 64, 128 or 256 lanes with at most kActItems slots each, so
+// that up to four segments share a workgroup and few of its waves wait for
+// one another; still longer ones a workgroup of kActBigBlock lanes.
+int norm_geometry(const ua2a_plan_s* p, int32_t per_head, int32_t V, NormGeom* g, int32_t* items, uint32_t* block)
+{
+    g->sh = shape_of(p);
+    g->per_head = per_head ? 1u : 0u;
+    const int64_t heads = per_head ? 1 : p->H;
+    const uint32_t q = kBlockValues / static_cast<uint32_t>(V);
+    const int64_t slots = heads * ((p->D + kBlockValues - 1) / kBlockValues) * q;
+    if (slots > int64_t(kActBigBlock) * kActBigItems) return UA2A_ERR_SHAPE;
+    const int64_t segs = tokens_of(p) * (per_head ? p->H : 1);
+    if (segs >= kMaxSegments) return UA2A_ERR_SHAPE;
+    uint32_t lanes = 1;
+    *block = kActBlock;
+    if (slots <= 64) {
+        while (lanes < slots) lanes *= 2;
+    } else if (slots <= int64_t(kActBlock) * kActItems) {
+        lanes = 64;
+        while (lanes * kActItems < slots) lanes *= 2;
+    } else {
+        lanes = *block = kActBigBlock;
+    }
+    int32_t n = static_cast<int32_t>((slots + lanes - 1) / lanes);
+    if (*block == kActBigBlock)
+        n = V == 1 ? 8 : n <= 2 ? 2 : n <= 4 ? 4 : 8;          // the compiled counts
+    else if (V == 1 && n > 1)
+        n = 5;
+    *items = n;
+    g->len = static_cast<uint32_t>(heads * p->D);
+    g->slots = static_cast<uint32_t>(slots);
+    g->q_log = log2_of(q);
+    g->lanes_log = log2_of(lanes);
+    g->segs = static_cast<uint32_t>(segs);
+    const uint32_t per = *block / lanes;
+    g->groups = (g->segs + per - 1) / per;
+    g->d_nb = make_div32(g->sh.nb);
+    g->d_H = make_div32(g->sh.H);
+    return UA2A_OK;
+}
+
+uint32_t least(uint32_t a, uint32_t b) { return a < b ? a : b; }
+
+// What every call checks first.
+int check_plan(ua2a_plan_t plan, int32_t type)
+{
+    if (plan == nullptr) return UA2A_ERR_INVALID_ARG;
+    if (plan->disabled) return UA2A_ERR_DISABLED;
+    if (type_bytes(type) == 0 || type_bytes(type) != plan->elem_bytes) return UA2A_ERR_INVALID_ARG;
+    return UA2A_OK;
+}
+
+int check_cache(ua2a_plan_t plan, const ua2a_cache_t* c, int64_t* values, int64_t* scales)
+{
+    if (c == nullptr || c->codes == nullptr || c->scales == nullptr || !good_format(c->format))
+        return UA2A_ERR_INVALID_ARG;
+    if (c->sequences < 1 || c->capacity < 1 || c->capacity > INT32_MAX || c->sequences > INT32_MAX)
+        return UA2A_ERR_SHAPE;
+    const int64_t row = plan->H * plan->D;                     // one position on all ranks
+    if (c->sequences > kMaxCacheValues / c->capacity || c->sequences * c->capacity > kMaxCacheValues / (2 * row))
+        return UA2A_ERR_SHAPE;
+    const int64_t nb = (plan->D + kBlockValues - 1) / kBlockValues;
+    *values = 2 * c->sequences * c->capacity * row;
+    *scales = 2 * c->sequences * c->capacity * plan->H * nb;
+    return UA2A_OK;
+}
+
+void cache_geometry(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t V, int64_t each, CacheGeom* g)
+{
+    g->sh = shape_of(plan);
+    g->w = static_cast<uint32_t>(plan->w);
+    g->seqs = static_cast<uint32_t>(c->sequences);
+    g->each = static_cast<uint32_t>(each);
+    g->cap = c->capacity;
+    g->q_log = log2_of(kBlockValues / static_cast<uint32_t>(V));
+    g->part = c->sequences * c->capacity * plan->H * plan->D;
+    g->part_scales = c->sequences * c->capacity * plan->H * g->sh.nb;
+    g->d_nb = make_div32(g->sh.nb);
+    g->d_each = make_div32(g->each);
+    g->d_seqs = make_div32(g->seqs);
+}
+
+}  // namespace
+
+extern "C" {
+
+int ua2a_norm_exchange(ua2a_plan_t plan, int32_t mode, const ua2a_norm_t* n, void* stream)
+{
+    if (n == nullptr) return UA2A_ERR_INVALID_ARG;
+    int rc = check_plan(plan, n->type);
+    if (rc != UA2A_OK) return rc;
+    if ((mode != 0 && mode != 1) || (n->per_head != 0 && n->per_head != 1)) return UA2A_ERR_INVALID_ARG;
+    if (n->x == nullptr || n->out == nullptr || (n->residual == nullptr) != (n->sum == nullptr))
+        return UA2A_ERR_INVALID_ARG;
+    if (!(n->eps > 0.f) || isinf(n->eps)) return UA2A_ERR_INVALID_ARG;
+    if (n->weight != nullptr && n->weight_type != n->type && n->weight_type != UA2A_TYPE_FP32)
+        return UA2A_ERR_INVALID_ARG;
+    if (n->out_format != UA2A_FORMAT_NONE && !good_format(n->out_format)) return UA2A_ERR_INVALID_ARG;
+    if (n->saved_format != UA2A_FORMAT_NONE && !good_format(n->saved_format)) return UA2A_ERR_INVALID_ARG;
+    if ((n->out_format != UA2A_FORMAT_NONE) != (n->out_scales != nullptr)) return UA2A_ERR_INVALID_ARG;
+    if ((n->saved_format != UA2A_FORMAT_NONE) != (n->saved != nullptr) || (n->saved == nullptr) != (n->saved_scales == nullptr))
+        return UA2A_ERR_INVALID_ARG;
+
+    const uintptr_t e = static_cast<uintptr_t>(plan->elem_bytes);
+    const int32_t wbytes = type_bytes(n->weight_type);
+    if (misaligned(n->x, e) || misaligned(n->residual, e) || misaligned(n->sum, e) ||
+        (!n->out_format && misaligned(n->out, e)) ||
+        (n->weight != nullptr && misaligned(n->weight, static_cast<uintptr_t>(wbytes))) || misaligned(n->rstd, 4))
+        return UA2A_ERR_ALIGN;
+    const bool wide = (plan->D * plan->elem_bytes) % 16 == 0 && !misaligned(n->x, 16) && !misaligned(n->residual, 16) &&
+                      !misaligned(n->sum, 16) && !misaligned(n->weight, 16) && !misaligned(n->saved, 8) &&
+                      !misaligned(n->out, n->out_format ? 8 : 16);
+    ActLaunch L;
+    memset(&L, 0, sizeof L);
+    L.kernel = ActKernel::Norm;
+    L.type = n->type;
+    L.V = wide ? 16 / plan->elem_bytes : 1;
+    L.mode = mode;
+    NormArgs& a = L.norm;
+    rc = norm_geometry(plan, n->per_head, L.V, &a.g, &L.items, &L.block);
+    if (rc != UA2A_OK) return rc;
+
+    const int64_t values = plan->layout.tensor_elems, bytes = plan->layout.tensor_bytes;
+    const int64_t nscales = tokens_of(plan) * plan->H * a.g.sh.nb;
+    const Range ins[] = {{n->x, bytes}, {n->residual, bytes},
+                         {n->weight, n->weight != nullptr ? int64_t(a.g.len) * wbytes : 0}};
+    const Range outs[] = {{n->out, n->out_format ? values : bytes}, {n->out_scales, nscales}, {n->sum, bytes},
+                          {n->saved, values}, {n->saved_scales, nscales}, {n->rstd, int64_t(a.g.segs) * 4}};
+    if (aliased(outs, 6, ins, 3)) return UA2A_ERR_ALIAS;
+    rc = check_device(plan);
+    if (rc != UA2A_OK) return rc;
+
+    a.x = n->x;
+    a.residual = n->residual;
+    a.weight = n->weight;
+    a.out = n->out;
+    a.out_scales = static_cast<uint8_t*>(n->out_scales);
+    a.sum = n->sum;
+    a.saved = static_cast<uint8_t*>(n->saved);
+    a.saved_scales = static_cast<uint8_t*>(n->saved_scales);
+    a.rstd = n->rstd;
+    a.eps = n->eps;
+    a.inv_len = 1.f / static_cast<float>(a.g.len);
+    a.weight_f32 = n->weight_type == UA2A_TYPE_FP32 ? 1 : 0;
+    a.out_format = n->out_format;
+    a.saved_format = n->saved_format;
+    L.grid_x = least(a.g.groups, kNormGrid);
+    L.grid_y = 1;
+    const int err = act_launch(L, stream);
+    return err == 0 ? UA2A_OK : fail(plan, "launching the norm kernel", err);
+}
+
+int ua2a_norm_workspace(ua2a_plan_t plan, int32_t per_head, int64_t* bytes)
+{
+    if (plan == nullptr || bytes == nullptr || (per_head != 0 && per_head != 1)) return UA2A_ERR_INVALID_ARG;
+    const int64_t len = per_head ? plan->D : plan->H * plan->D;
+    const int64_t segs = tokens_of(plan) * (per_head ? plan->H : 1);
+    if (len > int64_t(kActBigBlock) * kActBigItems * 8 || segs >= kMaxSegments) return UA2A_ERR_SHAPE;
+    *bytes = (segs < kGradGrid ? segs : kGradGrid) * len * 4;
+    return UA2A_OK;
+}
+
+int ua2a_norm_exchange_backward(ua2a_plan_t plan, int32_t mode, const ua2a_norm_grad_t* n, void* stream)
+{
+    if (n == nullptr) return UA2A_ERR_INVALID_ARG;
+    int rc = check_plan(plan, n->type);
+    if (rc != UA2A_OK) return rc;
+    if ((mode != 0 && mode != 1) || (n->per_head != 0 && n->per_head != 1)) return UA2A_ERR_INVALID_ARG;
+    if (n->dy == nullptr || n->saved == nullptr || n->rstd == nullptr || n->dx == nullptr) return UA2A_ERR_INVALID_ARG;
+    if (n->weight != nullptr && n->weight_type != n->type && n->weight_type != UA2A_TYPE_FP32)
+        return UA2A_ERR_INVALID_ARG;
+    if (n->saved_format != UA2A_FORMAT_NONE && !good_format(n->saved_format)) return UA2A_ERR_INVALID_ARG;
+    if ((n->saved_format != UA2A_FORMAT_NONE) != (n->saved_scales != nullptr)) return UA2A_ERR_INVALID_ARG;
+    if (n->saved_gathered != 0 && (n->saved_gathered != 1 || mode != 1 || n->saved_format != UA2A_FORMAT_NONE))
+        return UA2A_ERR_INVALID_ARG;
+    if ((n->dresidual != nullptr && mode != 1) || (n->dweight != nullptr && n->workspace == nullptr) ||
+        n->workspace_bytes < 0)
+        return UA2A_ERR_INVALID_ARG;
+
+    const uintptr_t e = static_cast<uintptr_t>(plan->elem_bytes);
+    const int32_t wbytes = type_bytes(n->weight_type);
+    if (misaligned(n->dy, e) || misaligned(n->dsum, e) || misaligned(n->dx, e) || misaligned(n->dresidual, e) ||
+        (!n->saved_format && misaligned(n->saved, e)) ||
+        (n->weight != nullptr && misaligned(n->weight, static_cast<uintptr_t>(wbytes))) || misaligned(n->rstd, 4) ||
+        misaligned(n->dweight, 4) || misaligned(n->workspace, 16))
+        return UA2A_ERR_ALIGN;
+    const bool wide = (plan->D * plan->elem_bytes) % 16 == 0 && !misaligned(n->dy, 16) && !misaligned(n->dsum, 16) &&
+                      !misaligned(n->dx, 16) && !misaligned(n->dresidual, 16) && !misaligned(n->weight, 16) &&
+                      !misaligned(n->saved, n->saved_format ? 8 : 16);
+    ActLaunch L;
+    memset(&L, 0, sizeof L);
+    L.kernel = ActKernel::NormGrad;
+    L.type = n->type;
+    L.V = wide ? 16 / plan->elem_bytes : 1;
+    L.mode = mode;
+    NormGradArgs& a = L.grad;
+    rc = norm_geometry(plan, n->per_head, L.V, &a.g, &L.items, &L.block);
+    if (rc != UA2A_OK) return rc;
+    L.grid_x = least(a.g.groups, kGradGrid);
+    L.grid_y = 1;
+
+    const int64_t values = plan->layout.tensor_elems, bytes = plan->layout.tensor_bytes;
+    const int64_t nscales = tokens_of(plan) * plan->H * a.g.sh.nb;
+    const int64_t wspace = n->dweight != nullptr ? int64_t(L.grid_x) * a.g.len * 4 : 0;
+    if (n->workspace_bytes < wspace) return UA2A_ERR_CAPACITY;
+    const Range ins[] = {{n->dy, bytes}, {n->dsum, bytes}, {n->saved, n->saved_format ? values : bytes},
+                         {n->saved_scales, nscales}, {n->rstd, int64_t(a.g.segs) * 4},
+                         {n->weight, n->weight != nullptr ? int64_t(a.g.len) * wbytes : 0}};
+    const Range outs[] = {{n->dx, bytes}, {n->dresidual, bytes}, {n->dweight, int64_t(a.g.len) * 4},
+                          {n->workspace, wspace}};
+    if (aliased(outs, 4, ins, 6)) return UA2A_ERR_ALIAS;
+    rc = check_device(plan);
+    if (rc != UA2A_OK) return rc;
+
+    a.dy = n->dy;
+    a.dsum = n->dsum;
+    a.saved = n->saved;
+    a.saved_scales = static_cast<const uint8_t*>(n->saved_scales);
+    a.weight = n->weight;
+    a.rstd = n->rstd;
+    a.dx = n->dx;
+    a.dresidual = n->dresidual;
+    a.partial = n->dweight != nullptr ? static_cast<float*>(n->workspace) : nullptr;
+    a.inv_len = 1.f / static_cast<float>(a.g.len);
+    a.weight_f32 = n->weight_type == UA2A_TYPE_FP32 ? 1 : 0;
+    a.saved_format = n->saved_format;
+    a.saved_gathered = n->saved_gathered;
+    int err = act_launch(L, stream);
+    if (err != 0) return fail(plan, "launching the norm's backward kernel", err);
+    if (n->dweight == nullptr) return UA2A_OK;
+    const uint32_t rows = L.grid_x, cols = a.g.len;
+    L.kernel = ActKernel::Columns;
+    L.columns.partial = static_cast<const float*>(n->workspace);
+    L.columns.out = n->dweight;
+    L.columns.rows = rows;
+    L.columns.cols = cols;
+    L.block = 1024;
+    L.grid_x = (cols + 31) / 32;
+    err = act_launch(L, stream);
+    return err == 0 ? UA2A_OK : fail(plan, "launching the weight gradient's sum", err);
+}
+
+int ua2a_cache_write(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t type, const void* k, const void* v,
+                     const int32_t* starts, const int32_t* counts, void* stream)
+{
+    int rc = check_plan(plan, type);
+    if (rc != UA2A_OK) return rc;
+    int64_t values, nscales;
+    rc = check_cache(plan, c, &values, &nscales);
+    if (rc != UA2A_OK) return rc;
+    if ((k == nullptr && v == nullptr) || starts == nullptr) return UA2A_ERR_INVALID_ARG;
+    const int64_t gathered = plan->B * plan->S_local * plan->w;
+    if (gathered % c->sequences != 0) return UA2A_ERR_SHAPE;
+    const uintptr_t e = static_cast<uintptr_t>(plan->elem_bytes);
+    if (misaligned(k, e) || misaligned(v, e) || misaligned(starts, 4) || misaligned(counts, 4)) return UA2A_ERR_ALIGN;
+    const bool wide = (plan->D * plan->elem_bytes) % 16 == 0 && !misaligned(k, 16) && !misaligned(v, 16) &&
+                      !misaligned(c->codes, 8);
+    ActLaunch L;
+    memset(&L, 0, sizeof L);
+    L.kernel = ActKernel::CacheWrite;
+    L.type = type;
+    L.V = wide ? 16 / plan->elem_bytes : 1;
+    CacheArgs& a = L.cache;
+    cache_geometry(plan, c, L.V, gathered / c->sequences, &a.g);
+    const int64_t row = plan->H * a.g.sh.nb * (kBlockValues / L.V);
+    if (row > kMaxSlots / gathered) return UA2A_ERR_SHAPE;
+    a.g.slots = static_cast<uint32_t>(row);
+    a.g.rows = static_cast<uint32_t>(gathered);
+    a.g.d_slots = make_div32(a.g.slots);
+    const int64_t bytes = plan->layout.tensor_bytes;
+    const Range ins[] = {{k, bytes}, {v, bytes}, {starts, c->sequences * 4}, {counts, c->sequences * 4}};
+    const Range outs[] = {{c->codes, values}, {c->scales, nscales}};
+    if (aliased(outs, 2, ins, 4)) return UA2A_ERR_ALIAS;
+    rc = check_device(plan);
+    if (rc != UA2A_OK) return rc;
+    a.k = k;
+    a.v = v;
+    a.codes = static_cast<uint8_t*>(c->codes);
+    a.scales = static_cast<uint8_t*>(c->scales);
+    a.starts = starts;
+    a.counts = counts;
+    a.format = c->format;
+    L.block = kActBlock;
+    L.grid_x = static_cast<uint32_t>((row * gathered + kActBlock - 1) / kActBlock);
+    L.grid_y = 2;
+    const int err = act_launch(L, stream);
+    return err == 0 ? UA2A_OK : fail(plan, "launching the cache write", err);
+}
+
+int ua2a_cache_read(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t type, int64_t n, const int32_t* starts,
+                    const int32_t* counts, void* k_out, void* v_out, void* stream)
+{
+    int rc = check_plan(plan, type);
+    if (rc != UA2A_OK) return rc;
+    int64_t values, nscales;
+    rc = check_cache(plan, c, &values, &nscales);
+    if (rc != UA2A_OK) return rc;
+    if (k_out == nullptr && v_out == nullptr) return UA2A_ERR_INVALID_ARG;
+    if (n < 1 || n > INT32_MAX) return UA2A_ERR_SHAPE;
+    const uintptr_t e = static_cast<uintptr_t>(plan->elem_bytes);
+    if (misaligned(k_out, e) || misaligned(v_out, e) || misaligned(starts, 4) || misaligned(counts, 4))
+        return UA2A_ERR_ALIGN;
+    const bool wide = (plan->D * plan->elem_bytes) % 16 == 0 && !misaligned(k_out, 16) && !misaligned(v_out, 16) &&
+                      !misaligned(c->codes, 8);
+    ActLaunch L;
+    memset(&L, 0, sizeof L);
+    L.kernel = ActKernel::CacheRead;
+    L.type = type;
+    L.V = wide ? 16 / plan->elem_bytes : 1;
+    CacheArgs& a = L.cache;
+    cache_geometry(plan, c, L.V, n, &a.g);
+    const int64_t row = int64_t(a.g.sh.hl) * a.g.sh.nb * (kBlockValues / L.V);
+    if (c->sequences > kMaxSlots / plan->w || c->sequences * plan->w > kMaxSlots / n) return UA2A_ERR_SHAPE;
+    const int64_t rows = c->sequences * plan->w * n;
+    if (row > kMaxSlots / rows) return UA2A_ERR_SHAPE;
+    a.g.slots = static_cast<uint32_t>(row);
+    a.g.rows = static_cast<uint32_t>(rows);
+    a.g.d_slots = make_div32(a.g.slots);
+    const int64_t bytes = rows * a.g.sh.hl * plan->D * plan->elem_bytes;
+    const Range ins[] = {{c->codes, values}, {c->scales, nscales}, {starts, c->sequences * 4},
+                         {counts, c->sequences * 4}};
+    const Range outs[] = {{k_out, bytes}, {v_out, bytes}};
+    if (aliased(outs, 2, ins, 4)) return UA2A_ERR_ALIAS;
+    rc = check_device(plan);
+    if (rc != UA2A_OK) return rc;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.codes = static_cast<uint8_t*>(c->codes);
+    a.scales = static_cast<uint8_t*>(c->scales);
+    a.starts = starts;
+    a.counts = counts;
+    a.format = c->format;
+    L.block = kActBlock;
+    L.grid_x = static_cast<uint32_t>((row * rows + kActBlock - 1) / kActBlock);
+    L.grid_y = 2;
+    const int err = act_launch(L, stream);
+    return err == 0 ? UA2A_OK : fail(plan, "launching the cache read", err);
+}
+
+}  // extern "C"
