@@ -203,18 +203,26 @@ void norm_lanes(const ActLaunch& L, const NormGeom& g, F fn)
             }
 }
 
-int64_t scales_of(const NormGeom& g) { return int64_t(g.segs) * (g.per_head ? 1 : g.sh.H) * g.sh.nb; }
-int64_t values_of(const NormGeom& g) { return int64_t(g.segs) * g.len; }
+int64_t scales_of(const NormGeom& g) { return int64_t(g.segs) * g.heads * g.sh.nb; }
+int64_t values_of(const NormGeom& g) { return int64_t(g.segs) * g.heads * g.sh.D; }
+// the norm that a slot belongs to, counted over all, and its number
+bool per_head(const NormGeom& g) { return g.cols == g.sh.D; }
+int64_t stats_of(const NormGeom& g) { return int64_t(g.segs) * (per_head(g) ? g.heads : 1); }
+size_t stat(const NormGeom& g, const Segment& s, const Slot& sl)
+{
+    return per_head(g) ? static_cast<size_t>(s.at.p) * g.sh.H + s.h0 + sl.hh : s.at.p;
+}
+int64_t weight_at(const NormGeom& g, const Slot& sl) { return (per_head(g) ? 0 : int64_t(sl.hh) * g.sh.D) + sl.d; }
 
 void norm(const ActLaunch& L)
 {
     const NormArgs& a = L.norm;
     const NormGeom& g = a.g;
     const int64_t n = values_of(g), e = L.type == UA2A_TYPE_FP32 ? 4 : 2;
-    Buf x(a.x, n * e), res(a.residual, n * e), w(a.weight, int64_t(g.len) * (a.weight_f32 ? 4 : e));
+    Buf x(a.x, n * e), res(a.residual, n * e), w(a.weight, int64_t(g.cols) * (a.weight_f32 ? 4 : e));
     Buf out(a.out, a.out_format ? n : n * e), osc(a.out_scales, scales_of(g)), sum(a.sum, n * e), saved(a.saved, n),
-        ssc(a.saved_scales, scales_of(g)), rstd(a.rstd, int64_t(g.segs) * 4);
-    std::vector<double> ss(g.segs, 0.0);
+        ssc(a.saved_scales, scales_of(g)), rstd(a.rstd, stats_of(g) * 4);
+    std::vector<double> ss(static_cast<size_t>(stats_of(g)), 0.0);
     std::vector<float> h(static_cast<size_t>(n)), y(static_cast<size_t>(n));   // P order
     norm_lanes(L, g, [&](const Segment& s, const Slot& sl) {
         for (int32_t i = 0; i < L.V; ++i) {
@@ -225,18 +233,18 @@ void norm(const ActLaunch& L)
                 put(sum, p, v, L.type);
             }
             h[static_cast<size_t>(p)] = v;
-            ss[s.seg] += double(v) * v;
+            ss[stat(g, s, sl)] += double(v) * v;
         }
     });
     norm_lanes(L, g, [&](const Segment& s, const Slot& sl) {
-        const double r = 1.0 / sqrt(ss[s.seg] / g.len + a.eps);
+        const double r = 1.0 / sqrt(ss[stat(g, s, sl)] * a.inv_len + a.eps);
         for (int32_t i = 0; i < L.V; ++i) {
             const int64_t p = value_at(g, s, sl, false) + i;
-            const float wt = w.p ? get(w, int64_t(sl.hh) * g.sh.D + sl.d + i, a.weight_f32 ? UA2A_TYPE_FP32 : L.type) : 1.f;
+            const float wt = w.p ? get(w, weight_at(g, sl) + i, a.weight_f32 ? UA2A_TYPE_FP32 : L.type) : 1.f;
             y[static_cast<size_t>(p)] = static_cast<float>(h[static_cast<size_t>(p)] * r * wt);
             if (!a.out_format) put(out, value_at(g, s, sl, !L.mode) + i, y[static_cast<size_t>(p)], L.type);
         }
-        if (rstd.p && sl.hh == 0 && sl.d == 0) put(rstd, s.seg, static_cast<float>(r), UA2A_TYPE_FP32);
+        if (rstd.p && (per_head(g) || sl.hh == 0) && sl.d == 0) put(rstd, static_cast<int64_t>(stat(g, s, sl)), static_cast<float>(r), UA2A_TYPE_FP32);
         if (sl.d == 0) {                                        // a head's first slot: the whole head's 8 bits
             const int64_t p = value_at(g, s, sl, false);
             const auto head = [&](const std::vector<float>& v) {
@@ -261,9 +269,9 @@ void norm_grad(const ActLaunch& L)
     const NormGeom& g = a.g;
     const int64_t n = values_of(g), e = L.type == UA2A_TYPE_FP32 ? 4 : 2;
     Buf dy(a.dy, n * e), dsum(a.dsum, n * e), saved(a.saved, a.saved_format ? n : n * e), ssc(a.saved_scales, scales_of(g)),
-        w(a.weight, int64_t(g.len) * (a.weight_f32 ? 4 : e)), rstd(a.rstd, int64_t(g.segs) * 4);
-    Buf dx(a.dx, n * e), dres(a.dresidual, n * e), partial(a.partial, int64_t(L.grid_x) * g.len * 4);
-    std::vector<double> dot(g.segs, 0.0), dw(g.len, 0.0);
+        w(a.weight, int64_t(g.cols) * (a.weight_f32 ? 4 : e)), rstd(a.rstd, stats_of(g) * 4);
+    Buf dx(a.dx, n * e), dres(a.dresidual, n * e), partial(a.partial, int64_t(L.grid_x) * g.cols * 4);
+    std::vector<double> dot(static_cast<size_t>(stats_of(g)), 0.0), dw(g.cols, 0.0);
     const auto each = [&](const Segment& s, const Slot& sl, int32_t i, double* gy, double* nh, double* d) {
         *d = get(dy, value_at(g, s, sl, !L.mode) + i, L.type);
         double h;
@@ -272,16 +280,16 @@ void norm_grad(const ActLaunch& L)
                 ldexp(1.0, get8(ssc, scale_at(g, s, sl, false)) - 127);
         else
             h = get(saved, value_at(g, s, sl, a.saved_gathered) + i, L.type);
-        const float wt = w.p ? get(w, int64_t(sl.hh) * g.sh.D + sl.d + i, a.weight_f32 ? UA2A_TYPE_FP32 : L.type) : 1.f;
-        *nh = h * get(rstd, s.seg, UA2A_TYPE_FP32);
+        const float wt = w.p ? get(w, weight_at(g, sl) + i, a.weight_f32 ? UA2A_TYPE_FP32 : L.type) : 1.f;
+        *nh = h * get(rstd, static_cast<int64_t>(stat(g, s, sl)), UA2A_TYPE_FP32);
         *gy = *d * wt;
     };
     norm_lanes(L, g, [&](const Segment& s, const Slot& sl) {
         for (int32_t i = 0; i < L.V; ++i) {
             double gy, nh, d;
             each(s, sl, i, &gy, &nh, &d);
-            dot[s.seg] += gy * nh;
-            dw[sl.hh * g.sh.D + sl.d + i] += d * nh;
+            dot[stat(g, s, sl)] += gy * nh;
+            dw[static_cast<size_t>(weight_at(g, sl) + i)] += d * nh;
         }
     });
     norm_lanes(L, g, [&](const Segment& s, const Slot& sl) {
@@ -289,15 +297,15 @@ void norm_grad(const ActLaunch& L)
             double gy, nh, d;
             each(s, sl, i, &gy, &nh, &d);
             const int64_t p = value_at(g, s, sl, false) + i;
-            double r = get(rstd, s.seg, UA2A_TYPE_FP32) * (gy - nh * dot[s.seg] / g.len);
+            double r = get(rstd, static_cast<int64_t>(stat(g, s, sl)), UA2A_TYPE_FP32) * (gy - nh * dot[stat(g, s, sl)] * a.inv_len);
             if (dsum.p) r += get(dsum, p, L.type);
             put(dx, L.mode ? value_at(g, s, sl, true) + i : p, static_cast<float>(r), L.type);
             if (dres.p) put(dres, p, static_cast<float>(r), L.type);
         }
     });
     if (partial.p)                                              // everything in the first workgroup's row
-        for (int64_t k = 0; k < int64_t(L.grid_x) * g.len; ++k)
-            put(partial, k, k < g.len ? static_cast<float>(dw[static_cast<size_t>(k)]) : 0.f, UA2A_TYPE_FP32);
+        for (int64_t k = 0; k < int64_t(L.grid_x) * g.cols; ++k)
+            put(partial, k, k < g.cols ? static_cast<float>(dw[static_cast<size_t>(k)]) : 0.f, UA2A_TYPE_FP32);
 }
 
 void columns(const ActLaunch& L)

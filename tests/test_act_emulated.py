@@ -84,7 +84,7 @@ def run_norm(lib, plan, x, weight, mode, residual=None, per_head=False, out_fmt=
 
 # (w, B, S, H, D): one lane to several workgroups' worth of slots, heads that
 # are no multiple of a block or of 16 bytes, one token, long norms
-SHAPES = [(1, 1, 1, 1, 8), (2, 1, 8, 4, 16), (3, 2, 5, 6, 40), (2, 1, 3, 4, 7), (5, 1, 4, 10, 2), (1, 2, 3, 5, 33),
+SHAPES = [(1, 1, 1, 1, 8), (2, 1, 5, 8, 128), (5, 1, 9, 5, 32), (1, 1, 7, 10, 128), (2, 1, 8, 4, 16), (3, 2, 5, 6, 40), (2, 1, 3, 4, 7), (5, 1, 4, 10, 2), (1, 2, 3, 5, 33),
           (4, 2, 7, 8, 80), (2, 1, 3, 6, 128), (2, 1, 2, 12, 128), (2, 1, 2, 32, 128), (8, 1, 3, 40, 128),
           (1, 1, 2, 96, 128), (1, 1, 2, 256, 128), (2, 1, 1, 60, 7)]
 

@@ -52,21 +52,26 @@ UA2A_HD int64_t a_offset(const ActShape& g, uint32_t arow, uint32_t h, uint32_t 
 }
 
 // --------------------------------------------------------------------- norms
-// A segment is what one norm covers: a token's H*D values, or one head's D.
-// 2^lanes_log lanes work on a segment; the unit of a lane is a slot of V
-// consecutive values of one head.  A block of 32 values is 32/V slots, so
-// with heads padded to whole blocks a block's slots are consecutive lanes,
-// aligned to 32/V: its largest value is found by exchanging lanes in a group.
+// A segment is what 2^lanes_log lanes work on together: a token's H heads
+// where one norm covers them all, or a head that is a norm by itself; or a
+// bundle of heads with a norm each, 2^head_log lanes apiece.  The unit of a
+// lane is a slot of V consecutive values of one head.  A block of 32 values is
+// 32/V slots, and heads are padded to whole blocks (in bundles to 2^head_log
+// slots), so a block's slots are consecutive lanes, aligned to 32/V: its
+// largest value is found by exchanging lanes in a group.
 struct NormGeom {
     ActShape sh;
-    uint32_t len;                // values of a segment
-    uint32_t per_head;           // 1: segments are heads
-    uint32_t slots;              // slots of a segment, padding of short blocks included
+    uint32_t cols;               // values of the weight: H*D, with a norm per head D
+    uint32_t heads;              // heads of a segment
+    uint32_t per_token;          // segments of a token
+    uint32_t slots;              // slots of a segment, padding included
     uint32_t q_log;              // slots of a block = 2^q_log
+    uint32_t head_log;           // bundles: slots of a head = 2^head_log; else 0
+    uint32_t padded;             // 1: some lanes' slots are padding
     uint32_t lanes_log;
     uint32_t segs;               // segments in all
     uint32_t groups;             // workgroups' worth of segments
-    Div32 d_nb, d_H;
+    Div32 d_nb, d_per;
 };
 
 struct Slot {
@@ -78,11 +83,17 @@ struct Slot {
 
 UA2A_HD Slot slot_of(const NormGeom& g, uint32_t slot, uint32_t V)
 {
-    const uint32_t b = slot >> g.q_log;
+    const uint32_t within = slot & ((1u << g.q_log) - 1);
     Slot s;
-    s.hh = fdiv(b, g.d_nb);
-    s.blk = b - s.hh * g.sh.nb;
-    s.d = s.blk * kBlockValues + (slot & ((1u << g.q_log) - 1)) * V;
+    if (g.head_log) {
+        s.hh = slot >> g.head_log;
+        s.blk = (slot & ((1u << g.head_log) - 1)) >> g.q_log;
+    } else {
+        const uint32_t b = slot >> g.q_log;
+        s.hh = fdiv(b, g.d_nb);
+        s.blk = b - s.hh * g.sh.nb;
+    }
+    s.d = s.blk * kBlockValues + within * V;
     s.ok = (slot < g.slots && s.d < g.sh.D) ? 1u : 0u;
     return s;
 }
@@ -103,8 +114,8 @@ UA2A_HD Segment segment_of(const NormGeom& g, uint32_t group, uint32_t tid, uint
     Segment s;
     s.live = seg < g.segs ? 1u : 0u;
     s.seg = s.live ? seg : 0u;
-    const uint32_t token = g.per_head ? fdiv(s.seg, g.d_H) : s.seg;
-    s.h0 = g.per_head ? s.seg - token * g.sh.H : 0u;
+    const uint32_t token = fdiv(s.seg, g.d_per);
+    s.h0 = (s.seg - token * g.per_token) * g.heads;
     s.at = token_place(g.sh, token);
     return s;
 }

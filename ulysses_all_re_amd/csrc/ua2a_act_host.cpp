@@ -15,8 +15,7 @@ namespace {
 constexpr int64_t kMaxSegments = int64_t(1) << 31;
 constexpr int64_t kMaxSlots = int64_t(kMaxGridWorkItems) - kActBlock;    // lane slots of a cache call
 constexpr int64_t kMaxCacheValues = int64_t(1) << 38;
-constexpr uint32_t kNormGrid = 4096;       // most workgroups of a forward launch
-constexpr uint32_t kGradGrid = 1024;       // ... of a backward launch, each with a row of partial sums
+constexpr uint32_t kNormGrid = 1u << 20;   // most workgroups of a forward launch
 
 struct Range {
     const void* p;
@@ -94,47 +93,80 @@ uint32_t log2_of(uint32_t pow2)
     return l;
 }
 
-// Segments, lanes and slots of a norm with V values per slot.  A segment of
-// up to 64 slots gets a lane for each (the next power of two); a longer one
-// the fewest of 64, 128 or 256 lanes with at most kActItems slots each, so
-// that up to four segments share a workgroup and few of its waves wait for
-// one another; still longer ones a workgroup of kActBigBlock lanes.
-int norm_geometry(const ua2a_plan_s* p, int32_t per_head, int32_t V, NormGeom* g, int32_t* items, uint32_t* block)
+// Segments, lanes and slots of a norm with V values per slot.
+//
+// One norm per segment: up to 64 slots get a lane each (the next power of
+// two); more the fewest of 64, 128 or 256 lanes with at most kActItems slots
+// each, so that up to four segments share a workgroup and few of its waves
+// wait for one another; still more a workgroup of kActBigBlock lanes.
+//
+// A norm per head of up to 64 slots (the next power of two): heads in bundles,
+// which keeps as many loads in flight per lane and leaves all sums within a
+// wave.  A bundle's lanes are the most of 64 whose heads divide H, its slots
+// per lane the most that divide the rest.
+int norm_geometry(const ua2a_plan_s* p, int32_t per_head, int32_t V, NormGeom* g, ActLaunch* L)
 {
     g->sh = shape_of(p);
-    g->per_head = per_head ? 1u : 0u;
-    const int64_t heads = per_head ? 1 : p->H;
     const uint32_t q = kBlockValues / static_cast<uint32_t>(V);
-    const int64_t slots = heads * ((p->D + kBlockValues - 1) / kBlockValues) * q;
-    if (slots > int64_t(kActBigBlock) * kActBigItems) return UA2A_ERR_SHAPE;
-    const int64_t segs = tokens_of(p) * (per_head ? p->H : 1);
-    if (segs >= kMaxSegments) return UA2A_ERR_SHAPE;
-    uint32_t lanes = 1;
-    *block = kActBlock;
-    if (slots <= 64) {
-        while (lanes < slots) lanes *= 2;
-    } else if (slots <= int64_t(kActBlock) * kActItems) {
+    const int64_t head_slots = int64_t(g->sh.nb) * q;
+    uint32_t lanes = 1, n = 1;
+    int64_t slots = (per_head ? 1 : p->H) * head_slots;
+    L->block = kActBlock;
+    L->span = 0;
+    g->heads = per_head ? 1u : g->sh.H;
+    g->head_log = 0;
+    if (per_head && head_slots <= 64 && V > 1) {
+        uint32_t hq = 1;
+        while (hq < head_slots) hq *= 2;
         lanes = 64;
-        while (lanes * kActItems < slots) lanes *= 2;
+        while (g->sh.H % (lanes / hq) != 0) lanes /= 2;        // lanes == hq divides at the latest
+        n = kActItems;                                          // with fewer lanes than 64 what is left is odd
+        while ((g->sh.H / (lanes / hq)) % n != 0) --n;
+        L->span = lanes == 64 ? 1 : 2;
+        g->heads = lanes / hq * n;
+        g->head_log = log2_of(hq);
+        slots = int64_t(g->heads) * hq;
+        g->padded = (p->D % kBlockValues != 0 || hq != head_slots) ? 1u : 0u;
     } else {
-        lanes = *block = kActBigBlock;
+        if (slots > int64_t(kActBigBlock) * kActBigItems) return UA2A_ERR_SHAPE;
+        if (slots <= 64) {
+            while (lanes < slots) lanes *= 2;
+        } else if (slots <= int64_t(kActBlock) * kActItems) {
+            lanes = 64;
+            while (lanes * kActItems < slots) lanes *= 2;
+        } else {
+            lanes = L->block = kActBigBlock;
+        }
+        n = static_cast<uint32_t>((slots + lanes - 1) / lanes);
+        if (L->block == kActBigBlock)
+            n = V == 1 ? 8 : n <= 2 ? 2 : n <= 4 ? 4 : 8;      // the compiled counts
+        else if (V == 1 && n > 1)
+            n = 5;
+        g->padded = (p->D % kBlockValues != 0 || int64_t(lanes) * n != slots) ? 1u : 0u;
     }
-    int32_t n = static_cast<int32_t>((slots + lanes - 1) / lanes);
-    if (*block == kActBigBlock)
-        n = V == 1 ? 8 : n <= 2 ? 2 : n <= 4 ? 4 : 8;          // the compiled counts
-    else if (V == 1 && n > 1)
-        n = 5;
-    *items = n;
-    g->len = static_cast<uint32_t>(heads * p->D);
+    g->per_token = g->sh.H / g->heads;
+    const int64_t segs = tokens_of(p) * g->per_token;
+    if (tokens_of(p) * (per_head ? p->H : 1) >= kMaxSegments) return UA2A_ERR_SHAPE;
+    L->items = static_cast<int32_t>(n);
+    g->cols = static_cast<uint32_t>((per_head ? 1 : p->H) * p->D);
     g->slots = static_cast<uint32_t>(slots);
     g->q_log = log2_of(q);
     g->lanes_log = log2_of(lanes);
     g->segs = static_cast<uint32_t>(segs);
-    const uint32_t per = *block / lanes;
+    const uint32_t per = L->block / lanes;
     g->groups = (g->segs + per - 1) / per;
     g->d_nb = make_div32(g->sh.nb);
-    g->d_H = make_div32(g->sh.H);
+    g->d_per = make_div32(g->per_token);
     return UA2A_OK;
+}
+
+// Most workgroups of a backward launch: as many as the device holds at once
+// (its kernels keep their sums in registers, so fewer of them fit as the
+// slots per lane grow), each walking over segments.
+uint32_t grad_grid(uint32_t block, int32_t items)
+{
+    if (block == kActBigBlock) return 256;
+    return items >= 4 ? 512 : items == 3 ? 768 : 1024;
 }
 
 uint32_t least(uint32_t a, uint32_t b) { return a < b ? a : b; }
@@ -215,15 +247,16 @@ int ua2a_norm_exchange(ua2a_plan_t plan, int32_t mode, const ua2a_norm_t* n, voi
     L.V = wide ? 16 / plan->elem_bytes : 1;
     L.mode = mode;
     NormArgs& a = L.norm;
-    rc = norm_geometry(plan, n->per_head, L.V, &a.g, &L.items, &L.block);
+    rc = norm_geometry(plan, n->per_head, L.V, &a.g, &L);
     if (rc != UA2A_OK) return rc;
 
     const int64_t values = plan->layout.tensor_elems, bytes = plan->layout.tensor_bytes;
     const int64_t nscales = tokens_of(plan) * plan->H * a.g.sh.nb;
+    const int64_t nstats = tokens_of(plan) * (n->per_head ? plan->H : 1);
     const Range ins[] = {{n->x, bytes}, {n->residual, bytes},
-                         {n->weight, n->weight != nullptr ? int64_t(a.g.len) * wbytes : 0}};
+                         {n->weight, n->weight != nullptr ? int64_t(a.g.cols) * wbytes : 0}};
     const Range outs[] = {{n->out, n->out_format ? values : bytes}, {n->out_scales, nscales}, {n->sum, bytes},
-                          {n->saved, values}, {n->saved_scales, nscales}, {n->rstd, int64_t(a.g.segs) * 4}};
+                          {n->saved, values}, {n->saved_scales, nscales}, {n->rstd, nstats * 4}};
     if (aliased(outs, 6, ins, 3)) return UA2A_ERR_ALIAS;
     rc = check_device(plan);
     if (rc != UA2A_OK) return rc;
@@ -238,7 +271,7 @@ int ua2a_norm_exchange(ua2a_plan_t plan, int32_t mode, const ua2a_norm_t* n, voi
     a.saved_scales = static_cast<uint8_t*>(n->saved_scales);
     a.rstd = n->rstd;
     a.eps = n->eps;
-    a.inv_len = 1.f / static_cast<float>(a.g.len);
+    a.inv_len = 1.f / static_cast<float>(a.g.cols);
     a.weight_f32 = n->weight_type == UA2A_TYPE_FP32 ? 1 : 0;
     a.out_format = n->out_format;
     a.saved_format = n->saved_format;
@@ -251,11 +284,18 @@ int ua2a_norm_exchange(ua2a_plan_t plan, int32_t mode, const ua2a_norm_t* n, voi
 int ua2a_norm_workspace(ua2a_plan_t plan, int32_t per_head, int64_t* bytes)
 {
     if (plan == nullptr || bytes == nullptr || (per_head != 0 && per_head != 1)) return UA2A_ERR_INVALID_ARG;
-    const int64_t len = per_head ? plan->D : plan->H * plan->D;
-    const int64_t segs = tokens_of(plan) * (per_head ? plan->H : 1);
-    if (len > int64_t(kActBigBlock) * kActBigItems * 8 || segs >= kMaxSegments) return UA2A_ERR_SHAPE;
-    *bytes = (segs < kGradGrid ? segs : kGradGrid) * len * 4;
-    return UA2A_OK;
+    // the wide vectors and single values lie differently on the lanes: room for either
+    *bytes = 0;
+    int found = UA2A_ERR_SHAPE;
+    for (const int32_t V : {16 / plan->elem_bytes, 1}) {
+        NormGeom g;
+        ActLaunch L;
+        if (V > 16 / 2 || norm_geometry(plan, per_head, V, &g, &L) != UA2A_OK) continue;
+        const int64_t need = int64_t(least(g.groups, grad_grid(L.block, L.items))) * g.cols * 4;
+        if (need > *bytes) *bytes = need;
+        found = UA2A_OK;
+    }
+    return found;
 }
 
 int ua2a_norm_exchange_backward(ua2a_plan_t plan, int32_t mode, const ua2a_norm_grad_t* n, void* stream)
@@ -292,19 +332,20 @@ int ua2a_norm_exchange_backward(ua2a_plan_t plan, int32_t mode, const ua2a_norm_
     L.V = wide ? 16 / plan->elem_bytes : 1;
     L.mode = mode;
     NormGradArgs& a = L.grad;
-    rc = norm_geometry(plan, n->per_head, L.V, &a.g, &L.items, &L.block);
+    rc = norm_geometry(plan, n->per_head, L.V, &a.g, &L);
     if (rc != UA2A_OK) return rc;
-    L.grid_x = least(a.g.groups, kGradGrid);
+    L.grid_x = least(a.g.groups, grad_grid(L.block, L.items));
     L.grid_y = 1;
 
     const int64_t values = plan->layout.tensor_elems, bytes = plan->layout.tensor_bytes;
     const int64_t nscales = tokens_of(plan) * plan->H * a.g.sh.nb;
-    const int64_t wspace = n->dweight != nullptr ? int64_t(L.grid_x) * a.g.len * 4 : 0;
+    const int64_t nstats = tokens_of(plan) * (n->per_head ? plan->H : 1);
+    const int64_t wspace = n->dweight != nullptr ? int64_t(L.grid_x) * a.g.cols * 4 : 0;
     if (n->workspace_bytes < wspace) return UA2A_ERR_CAPACITY;
     const Range ins[] = {{n->dy, bytes}, {n->dsum, bytes}, {n->saved, n->saved_format ? values : bytes},
-                         {n->saved_scales, nscales}, {n->rstd, int64_t(a.g.segs) * 4},
-                         {n->weight, n->weight != nullptr ? int64_t(a.g.len) * wbytes : 0}};
-    const Range outs[] = {{n->dx, bytes}, {n->dresidual, bytes}, {n->dweight, int64_t(a.g.len) * 4},
+                         {n->saved_scales, nscales}, {n->rstd, nstats * 4},
+                         {n->weight, n->weight != nullptr ? int64_t(a.g.cols) * wbytes : 0}};
+    const Range outs[] = {{n->dx, bytes}, {n->dresidual, bytes}, {n->dweight, int64_t(a.g.cols) * 4},
                           {n->workspace, wspace}};
     if (aliased(outs, 4, ins, 6)) return UA2A_ERR_ALIAS;
     rc = check_device(plan);
@@ -319,14 +360,14 @@ int ua2a_norm_exchange_backward(ua2a_plan_t plan, int32_t mode, const ua2a_norm_
     a.dx = n->dx;
     a.dresidual = n->dresidual;
     a.partial = n->dweight != nullptr ? static_cast<float*>(n->workspace) : nullptr;
-    a.inv_len = 1.f / static_cast<float>(a.g.len);
+    a.inv_len = 1.f / static_cast<float>(a.g.cols);
     a.weight_f32 = n->weight_type == UA2A_TYPE_FP32 ? 1 : 0;
     a.saved_format = n->saved_format;
     a.saved_gathered = n->saved_gathered;
     int err = act_launch(L, stream);
     if (err != 0) return fail(plan, "launching the norm's backward kernel", err);
     if (n->dweight == nullptr) return UA2A_OK;
-    const uint32_t rows = L.grid_x, cols = a.g.len;
+    const uint32_t rows = L.grid_x, cols = a.g.cols;
     L.kernel = ActKernel::Columns;
     L.columns.partial = static_cast<const float*>(n->workspace);
     L.columns.out = n->dweight;

@@ -25,7 +25,7 @@ struct NormArgs {
     uint8_t* saved_scales;
     float* rstd;
     float eps;
-    float inv_len;               // 1 / g.len
+    float inv_len;               // 1 / values of a norm
     int32_t weight_f32;
     int32_t out_format;
     int32_t saved_format;
@@ -41,7 +41,7 @@ struct NormGradArgs {
     const float* rstd;
     void* dx;
     void* dresidual;
-    float* partial;              // [grid][len], or null without dweight
+    float* partial;              // [grid][cols], or null without dweight
     float inv_len;
     int32_t weight_f32;
     int32_t saved_format;
@@ -74,6 +74,7 @@ struct ActLaunch {
     int32_t type;                // UA2A_TYPE_*
     int32_t V;                   // values per lane slot: 16 / elem_bytes, or 1
     int32_t items;               // norms: slots per lane (a compiled count)
+    int32_t span;                // norms: how segments lie on lanes (Span of ua2a_act_norm.h)
     int32_t mode;
     uint32_t block, grid_x, grid_y;
     NormArgs norm;
