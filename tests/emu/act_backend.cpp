@@ -189,15 +189,17 @@ void put_head(Buf& codes, Buf& scales, int64_t at, int64_t scale0, const std::ve
 template <class F>
 void norm_lanes(const ActLaunch& L, const NormGeom& g, F fn)
 {
-    for (uint32_t wg = 0; wg < L.grid_x; ++wg)
-        for (uint32_t group = wg; group < g.groups; group += L.grid_x)
+    const uint32_t wgs = L.grid_x * L.grid_y;
+    for (uint32_t wg = 0; wg < wgs; ++wg)
+        for (uint32_t group = wg; group < g.groups; group += wgs)
             for (uint32_t tid = 0; tid < L.block; ++tid) {
-                const Segment s = segment_of(g, group, tid, L.block);
+                const Segment s = segment_of(g, group, tid / g.lanes);
                 if (!s.live) continue;
-                const uint32_t lane = tid & ((1u << g.lanes_log) - 1);
+                const uint32_t lane = tid % g.lanes;
                 for (int32_t it = 0; it < L.items; ++it) {
-                    const Slot sl = slot_of(g, lane + (static_cast<uint32_t>(it) << g.lanes_log),
-                                            static_cast<uint32_t>(L.V));
+                    const uint32_t slot = lane + static_cast<uint32_t>(it) * g.lanes;
+                    const Slot sl = g.head_log ? bundle_slot(g, slot, static_cast<uint32_t>(L.V))
+                                           : norm_slot(g, slot, static_cast<uint32_t>(L.V));
                     if (sl.ok) fn(s, sl);
                 }
             }
@@ -217,18 +219,22 @@ int64_t weight_at(const NormGeom& g, const Slot& sl) { return (per_head(g) ? 0 :
 void norm(const ActLaunch& L)
 {
     const NormArgs& a = L.norm;
+    const bool mode1 = a.flags & kNormMode1;
+    const int32_t out_format = !(a.flags & kNormOut8) ? 0 : a.flags & kNormOutE5M2 ? UA2A_FORMAT_E5M2 : UA2A_FORMAT_E4M3;
+    const int32_t saved_format =
+        !(a.flags & kNormSaved8) ? 0 : a.flags & kNormSavedE5M2 ? UA2A_FORMAT_E5M2 : UA2A_FORMAT_E4M3;
     const NormGeom& g = a.g;
     const int64_t n = values_of(g), e = L.type == UA2A_TYPE_FP32 ? 4 : 2;
-    Buf x(a.x, n * e), res(a.residual, n * e), w(a.weight, int64_t(g.cols) * (a.weight_f32 ? 4 : e));
-    Buf out(a.out, a.out_format ? n : n * e), osc(a.out_scales, scales_of(g)), sum(a.sum, n * e), saved(a.saved, n),
-        ssc(a.saved_scales, scales_of(g)), rstd(a.rstd, stats_of(g) * 4);
+    Buf x(a.x, n * e), res(a.residual, n * e), w(a.flags & kNormWeight ? a.weight : nullptr, int64_t(g.cols) * (a.weight_f32 ? 4 : e));
+    Buf out(a.out, out_format ? n : n * e), osc(a.out_scales, scales_of(g)), sum(a.sum, n * e), saved(a.saved, n),
+        ssc(a.saved_scales, scales_of(g)), rstd(a.flags & kNormRstd ? a.rstd : nullptr, stats_of(g) * 4);
     std::vector<double> ss(static_cast<size_t>(stats_of(g)), 0.0);
     std::vector<float> h(static_cast<size_t>(n)), y(static_cast<size_t>(n));   // P order
     norm_lanes(L, g, [&](const Segment& s, const Slot& sl) {
         for (int32_t i = 0; i < L.V; ++i) {
             const int64_t p = value_at(g, s, sl, false) + i;
-            float v = get(x, value_at(g, s, sl, L.mode) + i, L.type);
-            if (res.p) {
+            float v = get(x, value_at(g, s, sl, mode1) + i, L.type);
+            if (a.flags & kNormResidual) {
                 v = round_to(v + get(res, p, L.type), L.type);
                 put(sum, p, v, L.type);
             }
@@ -242,7 +248,7 @@ void norm(const ActLaunch& L)
             const int64_t p = value_at(g, s, sl, false) + i;
             const float wt = w.p ? get(w, weight_at(g, sl) + i, a.weight_f32 ? UA2A_TYPE_FP32 : L.type) : 1.f;
             y[static_cast<size_t>(p)] = static_cast<float>(h[static_cast<size_t>(p)] * r * wt);
-            if (!a.out_format) put(out, value_at(g, s, sl, !L.mode) + i, y[static_cast<size_t>(p)], L.type);
+            if (!out_format) put(out, value_at(g, s, sl, !mode1) + i, y[static_cast<size_t>(p)], L.type);
         }
         if (rstd.p && (per_head(g) || sl.hh == 0) && sl.d == 0) put(rstd, static_cast<int64_t>(stat(g, s, sl)), static_cast<float>(r), UA2A_TYPE_FP32);
         if (sl.d == 0) {                                        // a head's first slot: the whole head's 8 bits
@@ -250,36 +256,37 @@ void norm(const ActLaunch& L)
             const auto head = [&](const std::vector<float>& v) {
                 return std::vector<float>(v.begin() + p, v.begin() + p + g.sh.D);
             };
-            if (a.saved_format)
-                put_head(saved, ssc, p, scale_at(g, s, sl, false), head(h), a.saved_format);
+            if (saved_format)
+                put_head(saved, ssc, p, scale_at(g, s, sl, false), head(h), saved_format);
         }
     });
-    if (a.out_format)
+    if (out_format)
         norm_lanes(L, g, [&](const Segment& s, const Slot& sl) {
             if (sl.d != 0) return;
             const int64_t p = value_at(g, s, sl, false);
-            put_head(out, osc, value_at(g, s, sl, !L.mode), scale_at(g, s, sl, !L.mode),
-                     std::vector<float>(y.begin() + p, y.begin() + p + g.sh.D), a.out_format);
+            put_head(out, osc, value_at(g, s, sl, !mode1), scale_at(g, s, sl, !mode1),
+                     std::vector<float>(y.begin() + p, y.begin() + p + g.sh.D), out_format);
         });
 }
 
 void norm_grad(const ActLaunch& L)
 {
     const NormGradArgs& a = L.grad;
+    const bool mode1 = a.flags & kNormMode1;
     const NormGeom& g = a.g;
     const int64_t n = values_of(g), e = L.type == UA2A_TYPE_FP32 ? 4 : 2;
-    Buf dy(a.dy, n * e), dsum(a.dsum, n * e), saved(a.saved, a.saved_format ? n : n * e), ssc(a.saved_scales, scales_of(g)),
-        w(a.weight, int64_t(g.cols) * (a.weight_f32 ? 4 : e)), rstd(a.rstd, stats_of(g) * 4);
-    Buf dx(a.dx, n * e), dres(a.dresidual, n * e), partial(a.partial, int64_t(L.grid_x) * g.cols * 4);
+    Buf dy(a.dy, n * e), dsum(a.flags & kNormResidual ? a.dsum : nullptr, n * e), saved(a.saved, a.saved_format ? n : n * e), ssc(a.saved_scales, scales_of(g)),
+        w(a.flags & kNormWeight ? a.weight : nullptr, int64_t(g.cols) * (a.weight_f32 ? 4 : e)), rstd(a.rstd, stats_of(g) * 4);
+    Buf dx(a.dx, n * e), dres(a.flags & kNormApart ? a.dresidual : nullptr, n * e), partial(a.flags & kNormPartial ? a.partial : nullptr, int64_t(L.grid_x) * g.cols * 4);
     std::vector<double> dot(static_cast<size_t>(stats_of(g)), 0.0), dw(g.cols, 0.0);
     const auto each = [&](const Segment& s, const Slot& sl, int32_t i, double* gy, double* nh, double* d) {
-        *d = get(dy, value_at(g, s, sl, !L.mode) + i, L.type);
+        *d = get(dy, value_at(g, s, sl, !mode1) + i, L.type);
         double h;
         if (a.saved_format)
             h = code_value(get8(saved, value_at(g, s, sl, false) + i), a.saved_format) *
                 ldexp(1.0, get8(ssc, scale_at(g, s, sl, false)) - 127);
         else
-            h = get(saved, value_at(g, s, sl, a.saved_gathered) + i, L.type);
+            h = get(saved, value_at(g, s, sl, (a.flags & kNormGathered) != 0) + i, L.type);
         const float wt = w.p ? get(w, weight_at(g, sl) + i, a.weight_f32 ? UA2A_TYPE_FP32 : L.type) : 1.f;
         *nh = h * get(rstd, static_cast<int64_t>(stat(g, s, sl)), UA2A_TYPE_FP32);
         *gy = *d * wt;
@@ -299,7 +306,7 @@ void norm_grad(const ActLaunch& L)
             const int64_t p = value_at(g, s, sl, false) + i;
             double r = get(rstd, static_cast<int64_t>(stat(g, s, sl)), UA2A_TYPE_FP32) * (gy - nh * dot[stat(g, s, sl)] * a.inv_len);
             if (dsum.p) r += get(dsum, p, L.type);
-            put(dx, L.mode ? value_at(g, s, sl, true) + i : p, static_cast<float>(r), L.type);
+            put(dx, mode1 ? value_at(g, s, sl, true) + i : p, static_cast<float>(r), L.type);
             if (dres.p) put(dres, p, static_cast<float>(r), L.type);
         }
     });
@@ -406,7 +413,7 @@ int ua2a_act_emu_last(int what)   // 0 V, 1 items, 2 block, 3 grid, 4 lanes
     case 1: return g_last.items;
     case 2: return static_cast<int>(g_last.block);
     case 3: return static_cast<int>(g_last.grid_x);
-    default: return 1 << g.lanes_log;
+    default: return static_cast<int>(g.lanes);
     }
 }
 }

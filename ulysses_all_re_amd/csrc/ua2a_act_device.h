@@ -131,35 +131,15 @@ __device__ __forceinline__ float dpp_add(float x)
     return x + __uint_as_float(dpp<CTRL>(__float_as_uint(x)));
 }
 
-// Sum over aligned groups of 2^log lanes of a wave (log is uniform).
-__device__ __forceinline__ float group_sum(float x, uint32_t log)
+// Sum over aligned groups of `lanes` lanes of a wave, a power of two (uniform).
+__device__ __forceinline__ float group_sum(float x, uint32_t lanes)
 {
-    if (log >= 1) x = dpp_add<kDppXor1>(x);
-    if (log >= 2) x = dpp_add<kDppXor2>(x);
-    if (log >= 3) x = dpp_add<kDppHalfMirror>(x);
-    if (log >= 4) x = dpp_add<kDppMirror>(x);
-    if (log >= 5) x += __shfl_xor(x, 16);
-    if (log >= 6) x += __shfl_xor(x, 32);
-    return x;
-}
-
-// Sum over the 2^log lanes of a segment, in every lane of it; segments wider
-// than a wave join their waves' sums through LDS, in the waves' order.  `red`
-// holds one sum per wave, for two rounds in turn: a wave writes round n + 2
-// only after the barrier of round n + 1, which every wave reaches with round
-// n read.
-__device__ __forceinline__ float segment_sum(float x, uint32_t log, float (*red)[16], uint32_t round)
-{
-    x = group_sum(x, log);
-    if (log <= 6) return x;
-    const uint32_t wave = threadIdx.x >> 6;
-    const uint32_t waves = 1u << (log - 6);
-    float* r = red[round & 1];
-    if ((threadIdx.x & 63) == 0) r[wave] = x;
-    __syncthreads();
-    const uint32_t first = wave & ~(waves - 1);
-    x = 0.f;
-    for (uint32_t k = 0; k < waves; ++k) x += r[first + k];
+    if (lanes > 1) x = dpp_add<kDppXor1>(x);
+    if (lanes > 2) x = dpp_add<kDppXor2>(x);
+    if (lanes > 4) x = dpp_add<kDppHalfMirror>(x);
+    if (lanes > 8) x = dpp_add<kDppMirror>(x);
+    if (lanes > 16) x += __shfl_xor(x, 16);
+    if (lanes > 32) x += __shfl_xor(x, 32);
     return x;
 }
 

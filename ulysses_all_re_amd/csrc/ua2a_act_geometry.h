@@ -21,7 +21,8 @@ constexpr uint32_t kBlockValues = 32;    // values that share a scale
 struct ActShape {
     uint32_t H, D, nb, hl;
     uint32_t S, B, SG;           // SG = S * w
-    Div32 d_hl, d_S, d_B;
+    Div32 d_hl, d_S, d_B, d_run;
+    uint32_t run;                // hl * D: values of a token on one A rank
     int64_t a_rank;              // A: values from one rank to the next
     int64_t a_rank_scales;       // ... and scales
 };
@@ -51,10 +52,18 @@ UA2A_HD int64_t a_offset(const ActShape& g, uint32_t arow, uint32_t h, uint32_t 
     return static_cast<int64_t>(r) * rank + (static_cast<int64_t>(arow) * g.hl + k) * per + d;
 }
 
+// The A offset of value e of a token's H * D.
+UA2A_HD int64_t a_offset_of_value(const ActShape& g, uint32_t e)
+{
+    const uint32_t r = fdiv(e, g.d_run);
+    return static_cast<int64_t>(r) * g.a_rank + (e - r * g.run);
+}
+
 // --------------------------------------------------------------------- norms
-// A segment is what 2^lanes_log lanes work on together: a token's H heads
-// where one norm covers them all, or a head that is a norm by itself; or a
-// bundle of heads with a norm each, 2^head_log lanes apiece.  The unit of a
+// A segment is what `lanes` lanes work on together: a token's H heads where
+// one norm covers them all, or a head that is a norm by itself; or a bundle of
+// heads with a norm each, 2^head_log lanes apiece.  Its lanes are a power of
+// two, or a workgroup of whole waves.  The unit of a
 // lane is a slot of V consecutive values of one head.  A block of 32 values is
 // 32/V slots, and heads are padded to whole blocks (in bundles to 2^head_log
 // slots), so a block's slots are consecutive lanes, aligned to 32/V: its
@@ -68,7 +77,9 @@ struct NormGeom {
     uint32_t q_log;              // slots of a block = 2^q_log
     uint32_t head_log;           // bundles: slots of a head = 2^head_log; else 0
     uint32_t padded;             // 1: some lanes' slots are padding
-    uint32_t lanes_log;
+    uint32_t dense;              // 1: heads are whole blocks, so slot k holds values k*V .. of the segment
+    uint32_t lanes;
+    uint32_t per_log;            // segments of a workgroup = 2^per_log
     uint32_t segs;               // segments in all
     uint32_t groups;             // workgroups' worth of segments
     Div32 d_nb, d_per;
@@ -81,21 +92,26 @@ struct Slot {
     uint32_t ok;                 // 0: padding
 };
 
-UA2A_HD Slot slot_of(const NormGeom& g, uint32_t slot, uint32_t V)
+UA2A_HD Slot slot_at(const NormGeom& g, uint32_t slot, uint32_t hh, uint32_t blk, uint32_t V)
 {
-    const uint32_t within = slot & ((1u << g.q_log) - 1);
     Slot s;
-    if (g.head_log) {
-        s.hh = slot >> g.head_log;
-        s.blk = (slot & ((1u << g.head_log) - 1)) >> g.q_log;
-    } else {
-        const uint32_t b = slot >> g.q_log;
-        s.hh = fdiv(b, g.d_nb);
-        s.blk = b - s.hh * g.sh.nb;
-    }
-    s.d = s.blk * kBlockValues + within * V;
+    s.hh = hh;
+    s.blk = blk;
+    s.d = blk * kBlockValues + (slot & ((1u << g.q_log) - 1)) * V;
     s.ok = (slot < g.slots && s.d < g.sh.D) ? 1u : 0u;
     return s;
+}
+
+UA2A_HD Slot bundle_slot(const NormGeom& g, uint32_t slot, uint32_t V)
+{
+    return slot_at(g, slot, slot >> g.head_log, (slot & ((1u << g.head_log) - 1)) >> g.q_log, V);
+}
+
+UA2A_HD Slot norm_slot(const NormGeom& g, uint32_t slot, uint32_t V)
+{
+    const uint32_t b = slot >> g.q_log;
+    const uint32_t hh = fdiv(b, g.d_nb);
+    return slot_at(g, slot, hh, b - hh * g.sh.nb, V);
 }
 
 // What a lane needs of one segment: the token's places, its first head, and
@@ -107,10 +123,9 @@ struct Segment {
     uint32_t live;
 };
 
-UA2A_HD Segment segment_of(const NormGeom& g, uint32_t group, uint32_t tid, uint32_t block)
+UA2A_HD Segment segment_of(const NormGeom& g, uint32_t group, uint32_t within)
 {
-    const uint32_t per = block >> g.lanes_log;                  // segments per workgroup
-    const uint32_t seg = group * per + (tid >> g.lanes_log);
+    const uint32_t seg = (group << g.per_log) + within;         // within: segment of the workgroup
     Segment s;
     s.live = seg < g.segs ? 1u : 0u;
     s.seg = s.live ? seg : 0u;

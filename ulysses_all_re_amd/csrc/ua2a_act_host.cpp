@@ -15,7 +15,6 @@ namespace {
 constexpr int64_t kMaxSegments = int64_t(1) << 31;
 constexpr int64_t kMaxSlots = int64_t(kMaxGridWorkItems) - kActBlock;    // lane slots of a cache call
 constexpr int64_t kMaxCacheValues = int64_t(1) << 38;
-constexpr uint32_t kNormGrid = 1u << 20;   // most workgroups of a forward launch
 
 struct Range {
     const void* p;
@@ -80,6 +79,8 @@ ActShape shape_of(const ua2a_plan_s* p)
     g.d_hl = make_div32(g.hl);
     g.d_S = make_div32(g.S);
     g.d_B = make_div32(g.B);
+    g.run = static_cast<uint32_t>(p->H / p->w * p->D);         // < 2^31 by the plan's limits
+    g.d_run = make_div32(g.run);
     const int64_t rows = p->B * p->S_local * p->w;             // of one A rank
     g.a_rank = rows * g.hl * g.D;
     g.a_rank_scales = rows * g.hl * g.nb;
@@ -96,15 +97,18 @@ uint32_t log2_of(uint32_t pow2)
 // Segments, lanes and slots of a norm with V values per slot.
 //
 // One norm per segment: up to 64 slots get a lane each (the next power of
-// two); more the fewest of 64, 128 or 256 lanes with at most kActItems slots
-// each, so that up to four segments share a workgroup and few of its waves
-// wait for one another; still more a workgroup of kActBigBlock lanes.
+// two).  More: forward a workgroup to itself, of no more whole waves than it
+// needs with one, two or four slots per lane, up to kActBlock lanes (measured:
+// single precision, 288 slots, 82 us against 88 with 512 lanes; 640 slots 341
+// against 339, and 489 with 640 lanes); backward the fewest of one, two or four
+// waves with at most kActItems slots each.  Beyond them up to kActBigBlock lanes.
 //
-// A norm per head of up to 64 slots (the next power of two): heads in bundles,
-// which keeps as many loads in flight per lane and leaves all sums within a
-// wave.  A bundle's lanes are the most of 64 whose heads divide H, its slots
-// per lane the most that divide the rest.
-int norm_geometry(const ua2a_plan_s* p, int32_t per_head, int32_t V, NormGeom* g, ActLaunch* L)
+// A norm per head of up to 64 slots (the next power of two): heads in
+// bundles, which leaves all sums within a wave.  A bundle's lanes are the most
+// of 64 whose heads divide H; its slots per lane one forward (video-DiT heads
+// with a checkpoint: 313 us, with five 341), backward two where they divide the
+// rest (360 us; one 365, five 390).
+int norm_geometry(const ua2a_plan_s* p, int32_t per_head, int32_t V, bool backward, NormGeom* g, ActLaunch* L)
 {
     g->sh = shape_of(p);
     const uint32_t q = kBlockValues / static_cast<uint32_t>(V);
@@ -112,7 +116,6 @@ int norm_geometry(const ua2a_plan_s* p, int32_t per_head, int32_t V, NormGeom* g
     uint32_t lanes = 1, n = 1;
     int64_t slots = (per_head ? 1 : p->H) * head_slots;
     L->block = kActBlock;
-    L->span = 0;
     g->heads = per_head ? 1u : g->sh.H;
     g->head_log = 0;
     if (per_head && head_slots <= 64 && V > 1) {
@@ -120,9 +123,8 @@ int norm_geometry(const ua2a_plan_s* p, int32_t per_head, int32_t V, NormGeom* g
         while (hq < head_slots) hq *= 2;
         lanes = 64;
         while (g->sh.H % (lanes / hq) != 0) lanes /= 2;        // lanes == hq divides at the latest
-        n = kActItems;                                          // with fewer lanes than 64 what is left is odd
-        while ((g->sh.H / (lanes / hq)) % n != 0) --n;
-        L->span = lanes == 64 ? 1 : 2;
+        n = backward && (g->sh.H / (lanes / hq)) % 2 == 0 ? 2 : 1;     // lanes < 64 leave an odd number
+        L->span = lanes == 64 ? kSpanBundle : kSpanBundles;
         g->heads = lanes / hq * n;
         g->head_log = log2_of(hq);
         slots = int64_t(g->heads) * hq;
@@ -131,19 +133,22 @@ int norm_geometry(const ua2a_plan_s* p, int32_t per_head, int32_t V, NormGeom* g
         if (slots > int64_t(kActBigBlock) * kActBigItems) return UA2A_ERR_SHAPE;
         if (slots <= 64) {
             while (lanes < slots) lanes *= 2;
-        } else if (slots <= int64_t(kActBlock) * kActItems) {
+            L->span = kSpanPart;
+        } else if (backward && V > 1 && slots <= int64_t(kActBlock) * kActItems) {
             lanes = 64;
             while (lanes * kActItems < slots) lanes *= 2;
+            n = static_cast<uint32_t>((slots + lanes - 1) / lanes);
+            L->span = kSpanWaves;
         } else {
-            lanes = L->block = kActBigBlock;
+            while (kActBlock * n < slots && n < 4) n *= 2;
+            while (kActBigBlock * n < slots) n *= 2;            // 1, 2, 4 or 8
+            lanes = static_cast<uint32_t>((slots + n - 1) / n + 63) / 64 * 64;
+            L->block = lanes;
+            L->span = kSpanWide;
         }
-        n = static_cast<uint32_t>((slots + lanes - 1) / lanes);
-        if (L->block == kActBigBlock)
-            n = V == 1 ? 8 : n <= 2 ? 2 : n <= 4 ? 4 : 8;      // the compiled counts
-        else if (V == 1 && n > 1)
-            n = 5;
         g->padded = (p->D % kBlockValues != 0 || int64_t(lanes) * n != slots) ? 1u : 0u;
     }
+    g->dense = (p->D % kBlockValues == 0 && g->head_log == 0) ? 1u : 0u;
     g->per_token = g->sh.H / g->heads;
     const int64_t segs = tokens_of(p) * g->per_token;
     if (tokens_of(p) * (per_head ? p->H : 1) >= kMaxSegments) return UA2A_ERR_SHAPE;
@@ -151,21 +156,23 @@ int norm_geometry(const ua2a_plan_s* p, int32_t per_head, int32_t V, NormGeom* g
     g->cols = static_cast<uint32_t>((per_head ? 1 : p->H) * p->D);
     g->slots = static_cast<uint32_t>(slots);
     g->q_log = log2_of(q);
-    g->lanes_log = log2_of(lanes);
+    g->lanes = lanes;
+    g->per_log = log2_of(L->block / lanes);
     g->segs = static_cast<uint32_t>(segs);
-    const uint32_t per = L->block / lanes;
-    g->groups = (g->segs + per - 1) / per;
+    g->groups = static_cast<uint32_t>((segs + (int64_t(1) << g->per_log) - 1) >> g->per_log);
     g->d_nb = make_div32(g->sh.nb);
     g->d_per = make_div32(g->per_token);
     return UA2A_OK;
 }
 
-// Most workgroups of a backward launch: as many as the device holds at once
-// (its kernels keep their sums in registers, so fewer of them fit as the
-// slots per lane grow), each walking over segments.
-uint32_t grad_grid(uint32_t block, int32_t items)
+// Most workgroups of a backward launch: as many as the device holds at once,
+// each walking over segments (its kernels keep sums in registers, so fewer fit
+// as the slots per lane grow).  A grid that is no multiple of what is resident
+// leaves part of the device idle at the end: video-DiT with five slots per
+// lane 354 us with 512 workgroups, 451 with 768, 377 with 1024.
+uint32_t grad_grid(int32_t span, int32_t items)
 {
-    if (block == kActBigBlock) return 256;
+    if (span == kSpanWide) return 512;
     return items >= 4 ? 512 : items == 3 ? 768 : 1024;
 }
 
@@ -245,9 +252,8 @@ int ua2a_norm_exchange(ua2a_plan_t plan, int32_t mode, const ua2a_norm_t* n, voi
     L.kernel = ActKernel::Norm;
     L.type = n->type;
     L.V = wide ? 16 / plan->elem_bytes : 1;
-    L.mode = mode;
     NormArgs& a = L.norm;
-    rc = norm_geometry(plan, n->per_head, L.V, &a.g, &L);
+    rc = norm_geometry(plan, n->per_head, L.V, false, &a.g, &L);
     if (rc != UA2A_OK) return rc;
 
     const int64_t values = plan->layout.tensor_elems, bytes = plan->layout.tensor_bytes;
@@ -273,10 +279,13 @@ int ua2a_norm_exchange(ua2a_plan_t plan, int32_t mode, const ua2a_norm_t* n, voi
     a.eps = n->eps;
     a.inv_len = 1.f / static_cast<float>(a.g.cols);
     a.weight_f32 = n->weight_type == UA2A_TYPE_FP32 ? 1 : 0;
-    a.out_format = n->out_format;
-    a.saved_format = n->saved_format;
-    L.grid_x = least(a.g.groups, kNormGrid);
-    L.grid_y = 1;
+    a.flags = (mode == 1 ? kNormMode1 : 0) | (n->weight != nullptr ? kNormWeight : 0) |
+              (n->residual != nullptr ? kNormResidual : 0) | (n->rstd != nullptr ? kNormRstd : 0) |
+              (n->out_format ? kNormOut8 : 0) | (n->out_format == UA2A_FORMAT_E5M2 ? kNormOutE5M2 : 0) |
+              (n->saved_format ? kNormSaved8 : 0) | (n->saved_format == UA2A_FORMAT_E5M2 ? kNormSavedE5M2 : 0);
+    // one workgroup per group of segments, within what a dispatch counts along x
+    L.grid_x = least(a.g.groups, static_cast<uint32_t>(kMaxGridWorkItems / L.block));
+    L.grid_y = (a.g.groups + L.grid_x - 1) / L.grid_x;
     const int err = act_launch(L, stream);
     return err == 0 ? UA2A_OK : fail(plan, "launching the norm kernel", err);
 }
@@ -290,8 +299,8 @@ int ua2a_norm_workspace(ua2a_plan_t plan, int32_t per_head, int64_t* bytes)
     for (const int32_t V : {16 / plan->elem_bytes, 1}) {
         NormGeom g;
         ActLaunch L;
-        if (V > 16 / 2 || norm_geometry(plan, per_head, V, &g, &L) != UA2A_OK) continue;
-        const int64_t need = int64_t(least(g.groups, grad_grid(L.block, L.items))) * g.cols * 4;
+        if (V > 16 / 2 || norm_geometry(plan, per_head, V, true, &g, &L) != UA2A_OK) continue;
+        const int64_t need = int64_t(least(g.groups, grad_grid(L.span, L.items))) * g.cols * 4;
         if (need > *bytes) *bytes = need;
         found = UA2A_OK;
     }
@@ -330,11 +339,10 @@ int ua2a_norm_exchange_backward(ua2a_plan_t plan, int32_t mode, const ua2a_norm_
     L.kernel = ActKernel::NormGrad;
     L.type = n->type;
     L.V = wide ? 16 / plan->elem_bytes : 1;
-    L.mode = mode;
     NormGradArgs& a = L.grad;
-    rc = norm_geometry(plan, n->per_head, L.V, &a.g, &L);
+    rc = norm_geometry(plan, n->per_head, L.V, true, &a.g, &L);
     if (rc != UA2A_OK) return rc;
-    L.grid_x = least(a.g.groups, grad_grid(L.block, L.items));
+    L.grid_x = least(a.g.groups, grad_grid(L.span, L.items));
     L.grid_y = 1;
 
     const int64_t values = plan->layout.tensor_elems, bytes = plan->layout.tensor_bytes;
@@ -363,7 +371,9 @@ int ua2a_norm_exchange_backward(ua2a_plan_t plan, int32_t mode, const ua2a_norm_
     a.inv_len = 1.f / static_cast<float>(a.g.cols);
     a.weight_f32 = n->weight_type == UA2A_TYPE_FP32 ? 1 : 0;
     a.saved_format = n->saved_format;
-    a.saved_gathered = n->saved_gathered;
+    a.flags = (mode == 1 ? kNormMode1 : 0) | (n->weight != nullptr ? kNormWeight : 0) |
+              (n->dsum != nullptr ? kNormResidual : 0) | (n->dweight != nullptr ? kNormPartial : 0) |
+              (n->dresidual != nullptr ? kNormApart : 0) | (n->saved_gathered ? kNormGathered : 0);
     int err = act_launch(L, stream);
     if (err != 0) return fail(plan, "launching the norm's backward kernel", err);
     if (n->dweight == nullptr) return UA2A_OK;

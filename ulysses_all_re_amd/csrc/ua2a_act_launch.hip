@@ -14,8 +14,7 @@ const void* cache_kernel(const ActLaunch& L);
 int act_launch(const ActLaunch& L, void* stream)
 {
     const void* fn = nullptr;
-    int32_t mode = L.mode;
-    void* args[2] = {nullptr, &mode};
+    void* args[1] = {nullptr};
     switch (L.kernel) {
     case ActKernel::Norm:
         fn = norm_kernel(L);

@@ -7,12 +7,24 @@
 namespace ua2a {
 namespace {
 
-// How a segment lies on its lanes (see NormGeom).
-enum Span {
-    kOne,         // one norm; several slots per lane only where a wave has one segment
-    kBundle,      // a bundle of heads on a whole wave
-    kBundles,     // several bundles share a wave
-};
+enum Span { kPart = kSpanPart, kWide = kSpanWide, kWaves = kSpanWaves, kBundle = kSpanBundle, kBundles = kSpanBundles };
+constexpr bool one_norm(Span s) { return s == kPart || s == kWide || s == kWaves; }
+
+// The lane of the segment, and the segment of the workgroup.  A segment of
+// whole waves is the same in every lane, so what follows from it is scalar.
+template <Span SPAN>
+__device__ __forceinline__ uint32_t segment_lane(const NormGeom& g)
+{
+    return SPAN == kWide ? threadIdx.x : threadIdx.x & (g.lanes - 1);
+}
+template <Span SPAN>
+__device__ __forceinline__ uint32_t segment_within(const NormGeom& g)
+{
+    if constexpr (SPAN == kWide) return 0;
+    uint32_t tid = threadIdx.x;
+    if constexpr (SPAN == kWaves || SPAN == kBundle) tid = __builtin_amdgcn_readfirstlane(tid);
+    return tid >> (31 - __builtin_clz(g.lanes));
+}
 
 // What a lane needs to know of its slots, whatever the segment: offsets from
 // the segment's first value on either side, and which slots are no padding
@@ -26,16 +38,34 @@ struct LaneSlots {
     uint32_t ok;                 // bit per slot
 };
 
+template <Span SPAN, int V>
+__device__ __forceinline__ Slot slot_of(const NormGeom& g, uint32_t lane, int it)
+{
+    const uint32_t slot = lane + static_cast<uint32_t>(it) * g.lanes;
+    return one_norm(SPAN) ? norm_slot(g, slot, V) : bundle_slot(g, slot, V);
+}
+
 template <Span SPAN, int V, int ITEMS>
 __device__ __forceinline__ LaneSlots<ITEMS> lane_slots(const NormGeom& g, uint32_t lane)
 {
     LaneSlots<ITEMS> l;
     l.ok = 0;
+    if (one_norm(SPAN) && g.dense) {
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+            const uint32_t slot = lane + static_cast<uint32_t>(it) * g.lanes;
+            const bool ok = slot < g.slots;
+            l.p[it] = ok ? slot * V : 0;
+            l.a[it] = a_offset_of_value(g.sh, l.p[it]);
+            l.ok |= (ok ? 1u : 0u) << it;
+        }
+        return l;
+    }
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
-        const Slot s = slot_of(g, lane + (static_cast<uint32_t>(it) << g.lanes_log), V);
+        const Slot s = slot_of<SPAN, V>(g, lane, it);
         l.p[it] = s.ok ? s.hh * g.sh.D + s.d : 0;
-        l.a[it] = s.ok && SPAN == kOne ? a_offset(g.sh, 0, s.hh, g.sh.D, g.sh.a_rank, s.d) : 0;
+        l.a[it] = s.ok && one_norm(SPAN) ? a_offset(g.sh, 0, s.hh, g.sh.D, g.sh.a_rank, s.d) : 0;
         l.ok |= s.ok << it;
     }
     return l;
@@ -45,8 +75,8 @@ __device__ __forceinline__ LaneSlots<ITEMS> lane_slots(const NormGeom& g, uint32
 template <Span SPAN, int V, int ITEMS>
 __device__ __forceinline__ uint32_t weight_offset(const NormGeom& g, const LaneSlots<ITEMS>& l, uint32_t lane, int it)
 {
-    if constexpr (SPAN == kOne) return l.p[it];
-    return l.ok & 1 ? slot_of(g, lane, V).d : 0;
+    if constexpr (one_norm(SPAN)) return l.p[it];
+    return l.ok & 1 ? slot_of<SPAN, V>(g, lane, 0).d : 0;
 }
 
 // A segment's first value (and scale) on either side; for bundles the A side
@@ -59,18 +89,15 @@ struct SegmentBase {
     bool live;
 };
 
-template <Span SPAN, int BLOCK, int ITEMS>
+template <Span SPAN>
 __device__ __forceinline__ SegmentBase segment_base(const NormGeom& g, uint32_t group)
 {
-    uint32_t tid = threadIdx.x;
-    // a segment of whole waves: the same in every lane, so it is scalar work
-    if constexpr (SPAN == kBundle || (SPAN == kOne && ITEMS > 1)) tid = __builtin_amdgcn_readfirstlane(tid);
-    const Segment s = segment_of(g, group, tid, BLOCK);
+    const Segment s = segment_of(g, group, segment_within<SPAN>(g));
     const Slot first = {0, 0, 0, 1};
     SegmentBase b;
     b.p = value_at(g, s, first, false);
     b.ps = scale_at(g, s, first, false);
-    if constexpr (SPAN == kOne) {
+    if constexpr (one_norm(SPAN)) {
         b.a = value_at(g, s, first, true);
         b.as = scale_at(g, s, first, true);
     } else {
@@ -107,30 +134,33 @@ struct Places {
     }
     __device__ __forceinline__ Slot slot(int it) const
     {
-        return slot_of(g, lane + (static_cast<uint32_t>(it) << g.lanes_log), V);
+        return slot_of<SPAN, V>(g, lane, it);
     }
     __device__ __forceinline__ bool ok(int it) const { return l.ok >> it & 1; }
     __device__ __forceinline__ uint32_t p(int it) const { return l.p[it]; }
     __device__ __forceinline__ int64_t a(int it) const
     {
-        if constexpr (SPAN == kOne) return l.a[it];
+        if constexpr (one_norm(SPAN)) return l.a[it];
         const Slot sl = slot(it);
         return sl.ok ? a_offset(g.sh, 0, s.h0 + sl.hh, g.sh.D, g.sh.a_rank, sl.d) : 0;
     }
     __device__ __forceinline__ uint32_t scale_p(int it) const
     {
+        if (!ok(it)) return 0;
+        // one norm: blocks in the order of the slots
+        if constexpr (one_norm(SPAN)) return (lane + static_cast<uint32_t>(it) * g.lanes) / (kBlockValues / V);
         const Slot sl = slot(it);
         return sl.hh * g.sh.nb + sl.blk;
     }
     __device__ __forceinline__ int64_t scale_a(int it) const
     {
         const Slot sl = slot(it);
-        return a_offset(g.sh, 0, (SPAN == kOne ? 0 : s.h0) + sl.hh, g.sh.nb, g.sh.a_rank_scales, sl.blk);
+        return a_offset(g.sh, 0, (one_norm(SPAN) ? 0 : s.h0) + sl.hh, g.sh.nb, g.sh.a_rank_scales, sl.blk);
     }
     // index of the slot's rstd
     __device__ __forceinline__ uint32_t stat(int it) const
     {
-        if constexpr (SPAN == kOne) return s.seg;
+        if constexpr (one_norm(SPAN)) return s.seg;
         return s.token * g.sh.H + s.h0 + (ok(it) ? slot(it).hh : 0);
     }
 };
@@ -162,60 +192,74 @@ struct Weights {
     }
 };
 
+// Sum over the lanes of a segment, in every lane of it; segments wider than a
+// wave join their waves' sums through LDS, in the waves' order.  `red` holds
+// one sum per wave, for two rounds in turn: a wave writes round n + 2 only
+// after the barrier of round n + 1, which every wave reaches with round n
+// read.
+template <Span SPAN>
+__device__ __forceinline__ float segment_sum(float x, uint32_t lanes, float (*red)[16], uint32_t round)
+{
+    if constexpr (SPAN == kPart) return group_sum(x, lanes);
+    x = group_sum(x, 64);
+    if (lanes <= 64) return x;
+    const uint32_t wave = threadIdx.x >> 6;
+    const uint32_t waves = lanes >> 6;
+    float* r = red[round & 1];
+    if ((threadIdx.x & 63) == 0) r[wave] = x;
+    __syncthreads();
+    const uint32_t first = SPAN == kWide ? 0 : wave & ~(waves - 1);
+    x = 0.f;
+    for (uint32_t k = 0; k < waves; ++k) x += r[first + k];
+    return x;
+}
+
 // Sums over a slot's norm: bundles sum each slot over its head's lanes,
 // others all slots over the segment's.
 template <Span SPAN, int ITEMS>
 __device__ __forceinline__ void norm_sums(const NormGeom& g, float (&x)[ITEMS], float (*red)[16], uint32_t round)
 {
-    if constexpr (SPAN == kOne) {
+    if constexpr (one_norm(SPAN)) {
         float t = x[0];
 #pragma unroll
         for (int it = 1; it < ITEMS; ++it) t += x[it];
-        t = segment_sum(t, g.lanes_log, red, round);
+        t = segment_sum<SPAN>(t, g.lanes, red, round);
 #pragma unroll
         for (int it = 0; it < ITEMS; ++it) x[it] = t;
     } else {
 #pragma unroll
-        for (int it = 0; it < ITEMS; ++it) x[it] = group_sum(x[it], g.head_log);
+        for (int it = 0; it < ITEMS; ++it) x[it] = group_sum(x[it], 1u << g.head_log);
     }
 }
 
 }  // namespace
 
+// K<T, W, V, span, slots per lane, most lanes of a workgroup>::fn() for a
+// launch.  The forward kernels have one slot per lane wherever a workgroup
+// holds the norm; the backward ones keep sums per slot, so several.
 template <class T, class W, int V, template <class, class, int, Span, int, int> class K>
 const void* norm_pick(const ActLaunch& L)
 {
-    if constexpr (V == 1) {
-        if (L.block == kActBlock && L.items == 1) return K<T, W, 1, kOne, 1, kActBlock>::fn();
-        if (L.block == kActBlock && L.items == 5) return K<T, W, 1, kOne, 5, kActBlock>::fn();
-        if (L.block == kActBigBlock && L.items == 8) return K<T, W, 1, kOne, 8, kActBigBlock>::fn();
-    } else if (L.span == kBundle) {
+    if (L.span == kPart) return K<T, W, V, kPart, 1, kActBlock>::fn();
+    if (L.span == kWide) {
         switch (L.items) {
-        case 1: return K<T, W, V, kBundle, 1, kActBlock>::fn();
-        case 2: return K<T, W, V, kBundle, 2, kActBlock>::fn();
-        case 3: return K<T, W, V, kBundle, 3, kActBlock>::fn();
-        case 4: return K<T, W, V, kBundle, 4, kActBlock>::fn();
-        case 5: return K<T, W, V, kBundle, 5, kActBlock>::fn();
+        case 1: return K<T, W, V, kWide, 1, kActBigBlock>::fn();
+        case 2: return K<T, W, V, kWide, 2, kActBigBlock>::fn();
+        case 4: return K<T, W, V, kWide, 4, kActBigBlock>::fn();
+        case 8: return K<T, W, V, kWide, 8, kActBigBlock>::fn();
         }
-    } else if (L.span == kBundles) {
-        switch (L.items) {
-        case 1: return K<T, W, V, kBundles, 1, kActBlock>::fn();
-        case 3: return K<T, W, V, kBundles, 3, kActBlock>::fn();
-        case 5: return K<T, W, V, kBundles, 5, kActBlock>::fn();
-        }
-    } else if (L.block == kActBlock) {
-        switch (L.items) {
-        case 1: return K<T, W, V, kOne, 1, kActBlock>::fn();
-        case 2: return K<T, W, V, kOne, 2, kActBlock>::fn();
-        case 3: return K<T, W, V, kOne, 3, kActBlock>::fn();
-        case 4: return K<T, W, V, kOne, 4, kActBlock>::fn();
-        case 5: return K<T, W, V, kOne, 5, kActBlock>::fn();
-        }
-    } else if (L.block == kActBigBlock) {
-        switch (L.items) {
-        case 2: return K<T, W, V, kOne, 2, kActBigBlock>::fn();
-        case 4: return K<T, W, V, kOne, 4, kActBigBlock>::fn();
-        case 8: return K<T, W, V, kOne, 8, kActBigBlock>::fn();
+    }
+    if constexpr (V > 1) {
+        if (L.span == kBundle && L.items == 1) return K<T, W, V, kBundle, 1, kActBlock>::fn();
+        if (L.span == kBundles && L.items == 1) return K<T, W, V, kBundles, 1, kActBlock>::fn();
+        if constexpr (K<T, W, V, kPart, 1, kActBlock>::kManyItems) {
+            if (L.span == kBundle && L.items == 2) return K<T, W, V, kBundle, 2, kActBlock>::fn();
+            if (L.span == kWaves) switch (L.items) {
+                case 2: return K<T, W, V, kWaves, 2, kActBlock>::fn();
+                case 3: return K<T, W, V, kWaves, 3, kActBlock>::fn();
+                case 4: return K<T, W, V, kWaves, 4, kActBlock>::fn();
+                case 5: return K<T, W, V, kWaves, 5, kActBlock>::fn();
+                }
         }
     }
     return nullptr;

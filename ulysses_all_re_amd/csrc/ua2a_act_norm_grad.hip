@@ -9,21 +9,23 @@ namespace {
 // and keep the sums of dweight for their lanes' slots in registers; at the
 // end each workgroup writes one row of partial sums.
 template <class T, class W, bool SAVED8, int V, Span SPAN, int ITEMS, int BLOCK>
-__global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a, int32_t mode1)
+__global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a)
 {
     __shared__ float red[2][16];
-    __shared__ float join[BLOCK * V];
+    __shared__ float join[SPAN == kWide ? 1 : BLOCK * V];
     const NormGeom& g = a.g;
-    const uint32_t lane = threadIdx.x & ((1u << g.lanes_log) - 1);
+    const uint32_t flags = a.flags;
+    const bool mode1 = flags & kNormMode1;
+    const uint32_t lane = segment_lane<SPAN>(g);
     LaneSlots<ITEMS> l = lane_slots<SPAN, V, ITEMS>(g, lane);
     // a bundle's slots of one lane are the same values of different heads
-    constexpr int kWeights = SPAN == kOne ? ITEMS : 1;
+    constexpr int kWeights = one_norm(SPAN) ? ITEMS : 1;
     Weights<W, V> wt[kWeights];
-    if (a.weight != nullptr) {
+    if (flags & kNormWeight) {
 #pragma unroll
         for (int it = 0; it < kWeights; ++it) wt[it].load(a.weight, weight_offset<SPAN, V>(g, l, lane, it));
     }
-    constexpr int kNorms = SPAN == kOne ? 1 : ITEMS;     // norms of a lane
+    constexpr int kNorms = one_norm(SPAN) ? 1 : ITEMS;     // norms of a lane
     float dw[kWeights][V];
 #pragma unroll
     for (int it = 0; it < kWeights; ++it)
@@ -38,7 +40,7 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a, i
         float rstd[kNorms];
     };
     const auto load = [&](uint32_t group, Loaded& x) {
-        x.s = segment_base<SPAN, BLOCK, ITEMS>(g, group);
+        x.s = segment_base<SPAN>(g, group);
         const SegmentBase& s = x.s;
         const Places<SPAN, V, ITEMS> at(g, s, l, lane);
         if (mode1) {
@@ -52,9 +54,9 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a, i
 #pragma unroll
             for (int it = 0; it < ITEMS; ++it) {
                 x.h[it] = load_once<Held>(static_cast<const uint8_t*>(a.saved) + s.p + at.p(it));
-                x.hs[it] = at.ok(it) ? (a.saved_scales + s.ps)[at.scale_p(it)] : 0u;
+                x.hs[it] = (a.saved_scales + s.ps)[at.scale_p(it)];
             }
-        } else if (a.saved_gathered) {
+        } else if ((flags & kNormGathered)) {
 #pragma unroll
             for (int it = 0; it < ITEMS; ++it) x.h[it] = load_values<T, V>(static_cast<const T*>(a.saved) + s.a, at.a(it));
         } else {
@@ -64,20 +66,16 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a, i
 #pragma unroll
         for (int it = 0; it < kNorms; ++it) x.rstd[it] = a.rstd[at.stat(it)];
     };
-    uint32_t round = 0;
-    Loaded next;
-    load(blockIdx.x, next);                                     // the grid has no more workgroups than groups
-    for (uint32_t group = blockIdx.x; group < g.groups; group += gridDim.x, ++round) {
-        Loaded x = next;
+    const auto work = [&](uint32_t group, Loaded& x, uint32_t after, Loaded& next, uint32_t round) {
         const SegmentBase& s = x.s;
         const Places<SPAN, V, ITEMS> at(g, s, l, lane);
         typename Raw<T, V>::type ds[ITEMS];
-        if (a.dsum != nullptr) {
+        if (flags & kNormResidual) {
 #pragma unroll
             for (int it = 0; it < ITEMS; ++it) ds[it] = load_values<T, V>(static_cast<const T*>(a.dsum) + s.p, at.p(it));
         }
         // the next segment is on its way while this one is worked on
-        if (group + gridDim.x < g.groups) load(group + gridDim.x, next);
+        if (after < g.groups) load(after, next);
         auto& dy = x.dy;
         auto& h = x.h;
         auto& hs = x.hs;
@@ -100,23 +98,24 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a, i
             float d[V], n[V], p = 0.f;
             unpack<T, V>(dy[it], d);
             normed(it, n);
-            const float rstd = x.rstd[SPAN == kOne ? 0 : it];
+            const float rstd = x.rstd[one_norm(SPAN) ? 0 : it];
             const float r = SAVED8 ? rstd * scale_of(hs[it]) : rstd;
+            float* const sums = dw[one_norm(SPAN) ? it : 0];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                n[i] = d[i] * (n[i] * r);
-                dw[SPAN == kOne ? it : 0][i] += n[i];
+                n[i] *= d[i];
+                sums[i] += n[i] * r;
             }
-            if (a.weight != nullptr) {
+            if (flags & kNormWeight) {
                 float wf[V];
-                wt[SPAN == kOne ? it : 0].get(wf);
+                wt[one_norm(SPAN) ? it : 0].get(wf);
 #pragma unroll
                 for (int i = 0; i < V; ++i) p += n[i] * wf[i];
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i) p += n[i];
             }
-            mean[it] = p;
+            mean[it] = p * r;
         }
         norm_sums<SPAN, ITEMS>(g, mean, red, round);
 #pragma unroll
@@ -126,43 +125,63 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a, i
             forget(h[it]);
             unpack<T, V>(dy[it], d);
             normed(it, n);
-            if (a.weight != nullptr) {
+            if (flags & kNormWeight) {
                 float wf[V];
-                wt[SPAN == kOne ? it : 0].get(wf);
+                wt[one_norm(SPAN) ? it : 0].get(wf);
 #pragma unroll
                 for (int i = 0; i < V; ++i) d[i] *= wf[i];
             }
             // the powers of two leave the factor's rounding alone
-            const float rstd = x.rstd[SPAN == kOne ? 0 : it];
+            const float rstd = x.rstd[one_norm(SPAN) ? 0 : it];
             const float m = rstd * (mean[it] * a.inv_len);
             const float r = SAVED8 ? m * scale_of(hs[it]) : m;
 #pragma unroll
             for (int i = 0; i < V; ++i) d[i] = rstd * (d[i] - n[i] * r);
-            if (a.dsum != nullptr) {
+            if (flags & kNormResidual) {
                 float e[V];
                 unpack<T, V>(ds[it], e);
 #pragma unroll
                 for (int i = 0; i < V; ++i) d[i] += e[i];
             }
-            if (s.live && at.ok(it)) {
-                const auto r16 = pack<T, V>(d);
+            const auto r16 = pack<T, V>(d);
+            if (!masked || (s.live && at.ok(it))) {
                 if (mode1)
                     store_values<T, V>(static_cast<T*>(a.dx) + s.a, at.a(it), r16);
                 else
                     store_values<T, V>(static_cast<T*>(a.dx) + s.p, at.p(it), r16);
-                if (a.dresidual != nullptr) store_values<T, V>(static_cast<T*>(a.dresidual) + s.p, at.p(it), r16);
+                if (flags & kNormApart) store_values<T, V>(static_cast<T*>(a.dresidual) + s.p, at.p(it), r16);
             }
         }
+    };
+    // Two segments' worth of registers in turn: handing one over to the other
+    // would wait for its loads.
+    Loaded one, two;
+    uint32_t group = blockIdx.x;                                // the grid has no more workgroups than groups
+    load(group, one);
+    for (;;) {
+        uint32_t after = group + gridDim.x;
+        work(group, one, after, two, 0);
+        if (after >= g.groups) break;
+        group = after + gridDim.x;
+        work(after, two, group, one, 1);
+        if (group >= g.groups) break;
     }
-    if (a.partial == nullptr) return;
-    // one row of sums per workgroup; lanes with the same weights are joined in
-    // order: the workgroup's segments, and in bundles their heads
-    const uint32_t lanes = 1u << (SPAN == kOne ? g.lanes_log : g.head_log);
-    const uint32_t per = BLOCK / lanes;
+    if (!(flags & kNormPartial)) return;
+    // One row of sums per workgroup.  Lanes with the same weights (the
+    // workgroup's segments; in bundles their heads too) are joined within a
+    // wave by exchanging lanes, then over its waves through LDS, in a fixed
+    // order.
     float* row = a.partial + static_cast<int64_t>(blockIdx.x) * g.cols;
+    const uint32_t lanes = one_norm(SPAN) ? g.lanes : 1u << g.head_log;                           // lanes with different weights
+    const uint32_t apart = lanes < 64 ? lanes : 64;             // ... of a wave
+    const uint32_t per = SPAN == kWide ? 1 : BLOCK / (lanes < 64 ? 64 : lanes);    // waves (segments) to join
 #pragma unroll
     for (int it = 0; it < kWeights; ++it) {
-        if (per > 1) {
+        for (uint32_t step = apart; step < 64; step *= 2) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) dw[it][i] += __shfl_xor(dw[it][i], static_cast<int>(step));
+        }
+        if (SPAN != kWide && per > 1) {
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < V; ++i) join[i * BLOCK + threadIdx.x] = dw[it][i];
@@ -170,31 +189,42 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a, i
         }
         if (threadIdx.x < lanes && (l.ok >> it & 1)) {
             const uint32_t to = weight_offset<SPAN, V>(g, l, lane, it);
+            const uint32_t next_one = lanes < 64 ? 64 : lanes;
+            for (uint32_t k = 1; SPAN != kWide && k < per; ++k) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float t = dw[it][i];
-#pragma unroll 1
-                for (uint32_t k = 1; k < per; ++k) t += join[i * BLOCK + k * lanes + threadIdx.x];
-                row[to + i] = t;
+                for (int i = 0; i < V; ++i) dw[it][i] += join[i * BLOCK + k * next_one + threadIdx.x];
             }
+#pragma unroll
+            for (int i = 0; i < V; ++i) row[to + i] = dw[it][i];
         }
     }
 }
 
 // Column sums of the workgroups' rows: 32 columns per workgroup, 32 lanes
-// down each, joined in order.
+// down each with eight loads in flight, joined in order.
 __global__ __launch_bounds__(1024) void ua2a_columns_kernel(ColumnArgs a)
 {
     __shared__ float part[32][33];
     const uint32_t c = blockIdx.x * 32 + (threadIdx.x & 31);
     const uint32_t r0 = threadIdx.x >> 5;
     float t = 0.f;
-    if (c < a.cols)
-        for (uint32_t r = r0; r < a.rows; r += 32) t += a.partial[static_cast<int64_t>(r) * a.cols + c];
+    if (c < a.cols) {
+        const float* p = a.partial + c;
+        uint32_t r = r0;
+        for (; r + 7 * 32 < a.rows; r += 8 * 32) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = p[static_cast<int64_t>(r + 32 * k) * a.cols];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t += v[k];
+        }
+        for (; r < a.rows; r += 32) t += p[static_cast<int64_t>(r) * a.cols];
+    }
     part[r0][threadIdx.x & 31] = t;
     __syncthreads();
     if (r0 == 0 && c < a.cols) {
         t = 0.f;
+#pragma unroll
         for (uint32_t k = 0; k < 32; ++k) t += part[k][threadIdx.x];
         a.out[c] = t;
     }
@@ -202,10 +232,12 @@ __global__ __launch_bounds__(1024) void ua2a_columns_kernel(ColumnArgs a)
 
 template <class T, class W, int V, Span SPAN, int ITEMS, int BLOCK>
 struct GradKernel {
+    static constexpr bool kManyItems = true;
     static const void* fn() { return reinterpret_cast<const void*>(&ua2a_norm_grad_kernel<T, W, false, V, SPAN, ITEMS, BLOCK>); }
 };
 template <class T, class W, int V, Span SPAN, int ITEMS, int BLOCK>
 struct GradKernel8 {
+    static constexpr bool kManyItems = true;
     static const void* fn() { return reinterpret_cast<const void*>(&ua2a_norm_grad_kernel<T, W, true, V, SPAN, ITEMS, BLOCK>); }
 };
 
