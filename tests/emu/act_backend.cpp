@@ -327,41 +327,80 @@ void columns(const ActLaunch& L)
     }
 }
 
-void cache(const ActLaunch& L, bool write)
+void cache_write(const ActLaunch& L)
 {
     const CacheArgs& a = L.cache;
     const CacheGeom& g = a.g;
-    const int64_t e = L.type == UA2A_TYPE_FP32 ? 4 : 2, nval = int64_t(g.rows) * (write ? g.sh.H : g.sh.hl) * g.sh.D;
+    const int64_t e = L.type == UA2A_TYPE_FP32 ? 4 : 2, nval = int64_t(g.rows) * g.sh.H * g.sh.D;
     Buf codes(a.codes, 2 * g.part), scales(a.scales, 2 * g.part_scales);
-    for (uint32_t y = 0; y < L.grid_y; ++y) {
-        Buf val(write ? (y ? a.v : a.k) : (y ? a.v_out : a.k_out), nval * e);
+    for (uint32_t y = 0; y < 2; ++y) {
+        Buf val(y ? a.v : a.k, nval * e);
         if (!val.p) continue;
-        for (uint64_t id = 0; id < uint64_t(L.grid_x) * L.block; ++id) {
-            if (id >= uint64_t(g.rows) * g.slots) continue;
-            const CacheSlot s = cache_slot(g, static_cast<uint32_t>(id), static_cast<uint32_t>(L.V), write);
-            if (s.i >= g.seqs) {
+        std::vector<uint8_t> seen(static_cast<size_t>(g.rows) * g.slots, 0);
+        for (uint32_t wg = 0; wg < L.grid_x; ++wg) {
+            const uint32_t group = cache_group(g, wg);
+            if (group >= g.groups) continue;
+            for (uint32_t tid = 0; tid < L.block; ++tid) {
+                const WriteLane l = write_lane(g, group, tid / g.lanes, tid);
+                if (!l.in) continue;
+                if (seen[static_cast<size_t>(l.token) * g.slots + l.slot]++) flag(3);
+                const TokenPlace at = token_place(g.sh, l.token);
+                const uint32_t i = fdiv(at.a, g.d_each), t = at.a - i * g.each;
+                if (i >= g.seqs) {
+                    flag(1);
+                    continue;
+                }
+                const CacheSpan s = cache_span(g, a.starts ? a.starts[i] : 0, a.counts ? a.counts[i] : int64_t(g.each));
+                if (t < s.first || t >= s.last) continue;
+                const uint32_t b = l.slot >> g.q_log, h = fdiv(b, g.d_nb);
+                const uint32_t d = (b - h * g.sh.nb) * kBlockValues +
+                                   (l.slot & ((1u << g.q_log) - 1)) * static_cast<uint32_t>(L.V);
+                if (g.dense && h * g.sh.D + d != l.slot * static_cast<uint32_t>(L.V)) flag(1);
+                if (d != 0) continue;                           // a head's first slot does the head
+                const uint32_t r = fdiv(h * g.sh.D, g.sh.d_run), rest = h * g.sh.D - r * g.sh.run;
+                const int64_t row = (int64_t(r) * g.seqs + i) * g.cap + s.start + t;
+                std::vector<float> v;
+                for (uint32_t k = 0; k < g.sh.D; ++k)
+                    v.push_back(get(val, (int64_t(l.token) * g.sh.H + h) * g.sh.D + k, L.type));
+                put_head(codes, scales, (y ? g.part : 0) + row * g.sh.run + rest,
+                         (y ? g.part_scales : 0) + row * g.sh.hl * g.sh.nb + int64_t(fdiv(rest, g.d_D)) * g.sh.nb, v,
+                         a.format);
+            }
+        }
+        for (uint8_t n : seen)
+            if (n != 1) flag(2);
+    }
+}
+
+void cache_read(const ActLaunch& L)
+{
+    const CacheArgs& a = L.cache;
+    const CacheGeom& g = a.g;
+    const int64_t e = L.type == UA2A_TYPE_FP32 ? 4 : 2, span = int64_t(g.each) * g.sh.run;
+    Buf codes(a.codes, 2 * g.part), scales(a.scales, 2 * g.part_scales);
+    for (uint32_t y = 0; y < 2; ++y) {
+        Buf val(y ? a.v_out : a.k_out, g.spans * span * e);
+        if (!val.p) continue;
+        for (uint32_t wg = 0; wg < L.grid_x; ++wg) {
+            const uint32_t ri = fdiv(wg, g.d_tiles), tile = wg - ri * g.tiles, r = fdiv(ri, g.d_seqs), i = ri - r * g.seqs;
+            if (i >= g.seqs || ri >= g.spans) {
                 flag(1);
                 continue;
             }
-            const int64_t row = cache_row(g, s, a.starts, a.counts);
-            if (row < 0 || s.d >= g.sh.D) continue;
-            if (write) {
-                const int64_t head = row * g.sh.hl + (s.h - s.r * g.sh.hl);
-                if (s.d != 0) continue;                         // a head's first slot does the head
-                std::vector<float> v;
-                for (uint32_t i = 0; i < g.sh.D; ++i)
-                    v.push_back(get(val, (int64_t(s.row) * g.sh.H + s.h) * g.sh.D + i, L.type));
-                put_head(codes, scales, (y ? g.part : 0) + head * g.sh.D, (y ? g.part_scales : 0) + head * g.sh.nb, v,
-                         a.format);
-            } else {
-                const int64_t head = row * g.sh.hl + s.h;
-                for (int32_t i = 0; i < L.V; ++i) {
-                    double f = code_value(get8(codes, (y ? g.part : 0) + head * g.sh.D + s.d + i), a.format) *
-                               ldexp(1.0, get8(scales, (y ? g.part_scales : 0) + head * g.sh.nb + s.blk) - 127);
+            const CacheSpan s = cache_span(g, a.starts ? a.starts[i] : 0, a.counts ? a.counts[i] : int64_t(g.each));
+            for (uint32_t tid = 0; tid < L.block; ++tid) {
+                const int64_t at = (int64_t(tile) * L.block + tid) * L.V;
+                if (at < s.first * g.sh.run || at >= s.last * g.sh.run) continue;
+                const int64_t row = int64_t(ri) * g.cap + s.start;
+                for (int32_t k = 0; k < L.V; ++k) {
+                    const int64_t h = (at + k) / g.sh.D, d = (at + k) % g.sh.D;
+                    double f = code_value(get8(codes, (y ? g.part : 0) + row * g.sh.run + at + k), a.format) *
+                               ldexp(1.0, get8(scales, (y ? g.part_scales : 0) + row * g.sh.hl * g.sh.nb + h * g.sh.nb +
+                                                           d / kBlockValues) - 127);
                     const double most = L.type == UA2A_TYPE_FP16 ? 65504.0
                                         : bits_f(L.type == UA2A_TYPE_FP32 ? 0x7f7fffffu : 0x7f7f0000u);
                     if (isfinite(f) && fabs(f) > most) f = f < 0 ? -most : most;
-                    put(val, (int64_t(s.row) * g.sh.hl + s.h) * g.sh.D + s.d + i, static_cast<float>(f), L.type);
+                    put(val, ri * span + at + k, static_cast<float>(f), L.type);
                 }
             }
         }
@@ -380,8 +419,8 @@ int act_launch(const ActLaunch& L, void*)
     case ActKernel::Norm: norm(L); break;
     case ActKernel::NormGrad: norm_grad(L); break;
     case ActKernel::Columns: columns(L); break;
-    case ActKernel::CacheWrite: cache(L, true); break;
-    case ActKernel::CacheRead: cache(L, false); break;
+    case ActKernel::CacheWrite: cache_write(L); break;
+    case ActKernel::CacheRead: cache_read(L); break;
     }
     return 0;
 }

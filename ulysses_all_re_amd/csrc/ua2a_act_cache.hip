@@ -6,53 +6,117 @@
 namespace ua2a {
 namespace {
 
-// New keys (grid y = 0) and values (1) in P, quantised into their places.
-template <class T, int V>
+// New keys and values in P, quantised into their places.  A workgroup moves one
+// vector of each per lane, of one token or of several short ones (keys and
+// values together: finding the place takes longer than moving one vector);
+// UNIFORM: a wave's lanes share the token, so its sequence, position and
+// whether it exists are scalar work.  A rank's share of a token is short (hl*D
+// codes, hl*nb scales), so groups of consecutive tokens go to one XCD, whose
+// L2 then puts whole lines together.
+template <class T, int V, bool UNIFORM>
 __global__ __launch_bounds__(kActBlock) void ua2a_cache_write_kernel(CacheArgs a)
 {
     const CacheGeom& g = a.g;
-    const void* x = blockIdx.y ? a.v : a.k;
-    if (x == nullptr) return;
-    const uint32_t idx = blockIdx.x * kActBlock + threadIdx.x;
-    const bool in = idx < g.rows * g.slots;
-    const CacheSlot s = cache_slot(g, in ? idx : 0, V, true);
-    const int64_t row = cache_row(g, s, a.starts, a.counts);
-    const bool ok = in && row >= 0 && s.d < g.sh.D;
-    typename Raw<T, V>::type raw{};
-    if (ok) raw = load_values<T, V>(x, (static_cast<int64_t>(s.row) * g.sh.H + s.h) * g.sh.D + s.d);
-    uint32_t byte;
-    const auto c = encode_raw<T, V>(raw, a.format, &byte);
-    if (!ok) return;
-    const int64_t head = row * g.sh.hl + (s.h - s.r * g.sh.hl);
-    store_once(a.codes + (blockIdx.y ? g.part : 0) + head * g.sh.D + s.d, c);
-    if (s.d == s.blk * kBlockValues)
-        a.scales[(blockIdx.y ? g.part_scales : 0) + head * g.sh.nb + s.blk] = static_cast<uint8_t>(byte);
+    const uint32_t group = cache_group(g, blockIdx.x);
+    if (group >= g.groups) return;
+    uint32_t tid = threadIdx.x;
+    if constexpr (UNIFORM) tid = __builtin_amdgcn_readfirstlane(tid);
+    const WriteLane l = write_lane(g, group, tid >> (31 - __builtin_clz(g.lanes)), 0);
+    const uint32_t slot = l.slot + (threadIdx.x & (g.lanes - 1));
+    const bool in = l.token < g.rows && slot < g.slots;
+    const uint32_t token = l.token < g.rows ? l.token : 0;
+    const TokenPlace at = token_place(g.sh, token);
+    const uint32_t i = fdiv(at.a, g.d_each);
+    const uint32_t t = at.a - i * g.each;
+    // both from memory at once; without counts the second is not looked at
+    const int32_t start = a.starts[i];
+    const int32_t count = (a.counts != nullptr ? a.counts : a.starts)[i];
+    const CacheSpan s = cache_span(g, start, a.counts != nullptr ? static_cast<int64_t>(count) : g.each);
+    const bool live = t >= s.first && t < s.last;
+    if constexpr (UNIFORM) {
+        if (!live) return;
+    }
+    // value e of the token's H * D: of rank r, rest of its hl * D
+    uint32_t e = slot * V, blk = 0;
+    bool ok = in && live;
+    if (!g.dense) {
+        const uint32_t b = slot >> g.q_log;
+        const uint32_t h = fdiv(b, g.d_nb);
+        blk = b - h * g.sh.nb;
+        const uint32_t d = blk * kBlockValues + (slot & ((1u << g.q_log) - 1)) * V;
+        ok = ok && d < g.sh.D;
+        e = h * g.sh.D + d;
+    }
+    const int64_t from = static_cast<int64_t>(token) * (g.sh.H * g.sh.D);
+    typename Raw<T, V>::type raw[2] = {};
+    if (ok && a.k != nullptr) raw[0] = load_values<T, V>(static_cast<const T*>(a.k) + from, e);
+    if (ok && a.v != nullptr) raw[1] = load_values<T, V>(static_cast<const T*>(a.v) + from, e);
+    const uint32_t r = fdiv(e, g.sh.d_run);
+    const uint32_t rest = e - r * g.sh.run;
+    const int64_t rank = static_cast<int64_t>(g.seqs) * g.cap;                  // positions of a rank
+    const int64_t row = static_cast<int64_t>(i) * g.cap + (s.start + t);
+    const uint32_t nscales = g.sh.hl * g.sh.nb;                                 // of a position on one rank
+    uint8_t* codes = a.codes + row * g.sh.run + (r * (rank * g.sh.run) + rest);
+    uint8_t* scales = a.scales + row * nscales +
+                      (r * (rank * nscales) + (g.dense ? rest / kBlockValues : fdiv(rest, g.d_D) * g.sh.nb + blk));
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+        if ((part ? a.v : a.k) == nullptr) continue;
+        uint32_t byte;
+        const auto c = encode_raw<T, V>(raw[part], a.format, &byte);
+        if (!ok) continue;
+        store_once(codes + (part ? g.part : 0), c);
+        if ((slot & ((1u << g.q_log) - 1)) == 0) scales[part ? g.part_scales : 0] = static_cast<uint8_t>(byte);
+    }
 }
 
-// Positions of the cache back in the type.
+// Positions of the cache back in the type.  What a rank holds of a sequence is
+// one stretch of the cache and of the output, so a workgroup's part of it is
+// scalar work and a lane moves one vector.
 template <class T, int V>
 __global__ __launch_bounds__(kActBlock) void ua2a_cache_read_kernel(CacheArgs a)
 {
     const CacheGeom& g = a.g;
-    void* out = blockIdx.y ? a.v_out : a.k_out;
-    if (out == nullptr) return;
-    const uint32_t idx = blockIdx.x * kActBlock + threadIdx.x;
-    if (idx >= g.rows * g.slots) return;
-    const CacheSlot s = cache_slot(g, idx, V, false);
-    const int64_t row = cache_row(g, s, a.starts, a.counts);
-    if (row < 0 || s.d >= g.sh.D) return;
-    const int64_t head = row * g.sh.hl + s.h;
-    const auto c = load_once<typename Codes<V>::type>(a.codes + (blockIdx.y ? g.part : 0) + head * g.sh.D + s.d);
-    const uint32_t byte = a.scales[(blockIdx.y ? g.part_scales : 0) + head * g.sh.nb + s.blk];
-    store_values<T, V>(out, (static_cast<int64_t>(s.row) * g.sh.hl + s.h) * g.sh.D + s.d,
-                       decode_raw<T, V>(c, byte, a.format));
+    const uint32_t ri = fdiv(blockIdx.x, g.d_tiles);            // (rank, sequence)
+    const uint32_t tile = blockIdx.x - ri * g.tiles;
+    const uint32_t r = fdiv(ri, g.d_seqs);
+    const uint32_t i = ri - r * g.seqs;
+    const CacheSpan s = cache_span(g, a.starts ? static_cast<int64_t>(a.starts[i]) : 0,
+                                   a.counts ? static_cast<int64_t>(a.counts[i]) : static_cast<int64_t>(g.each));
+    const int64_t e = (static_cast<int64_t>(tile) * blockDim.x + threadIdx.x) * V;
+    if (e < s.first * g.sh.run || e >= s.last * g.sh.run) return;
+    const int64_t row = static_cast<int64_t>(ri) * g.cap + s.start;             // of the span's first token
+    const uint32_t nscales = g.sh.hl * g.sh.nb;
+    int64_t at_scale = e / kBlockValues;
+    if (!g.dense) {
+        const int64_t h = e / g.sh.D;
+        at_scale = h * g.sh.nb + static_cast<uint32_t>(e - h * g.sh.D) / kBlockValues;
+    }
+    const uint8_t* codes = a.codes + row * g.sh.run + e;
+    const uint8_t* scales = a.scales + row * nscales + at_scale;
+    const int64_t to = static_cast<int64_t>(ri) * g.each * g.sh.run;
+    typename Codes<V>::type c[2] = {};
+    uint32_t byte[2] = {};
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+        if ((part ? a.v_out : a.k_out) == nullptr) continue;
+        c[part] = load_once<typename Codes<V>::type>(codes + (part ? g.part : 0));
+        byte[part] = scales[part ? g.part_scales : 0];
+    }
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+        void* out = part ? a.v_out : a.k_out;
+        if (out == nullptr) continue;
+        store_values<T, V>(static_cast<T*>(out) + to, e, decode_raw<T, V>(c[part], byte[part], a.format));
+    }
 }
 
 template <class T, int V>
 const void* typed_fn(const ActLaunch& L)
 {
-    return L.kernel == ActKernel::CacheWrite ? reinterpret_cast<const void*>(&ua2a_cache_write_kernel<T, V>)
-                                             : reinterpret_cast<const void*>(&ua2a_cache_read_kernel<T, V>);
+    if (L.kernel == ActKernel::CacheRead) return reinterpret_cast<const void*>(&ua2a_cache_read_kernel<T, V>);
+    return L.cache.g.lanes >= 64 ? reinterpret_cast<const void*>(&ua2a_cache_write_kernel<T, V, true>)
+                                 : reinterpret_cast<const void*>(&ua2a_cache_write_kernel<T, V, false>);
 }
 
 }  // namespace

@@ -156,56 +156,66 @@ UA2A_HD int64_t scale_at(const NormGeom& g, const Segment& s, const Slot& sl, bo
 // t < counts[i] and the position lies in [0, cap).
 struct CacheGeom {
     ActShape sh;
-    uint32_t w;
     uint32_t seqs, each;         // sequences, tokens of each in this call
-    int64_t cap;
+    uint32_t dense;              // 1: heads are whole blocks
     uint32_t q_log;
-    uint32_t slots;              // slots of a row: write, one token's H heads; read, one rank's hl heads
-    uint32_t rows;               // write: tokens; read: w * seqs * each
+    int64_t cap;
     int64_t part;                // values from the keys' codes to the values' codes
     int64_t part_scales;
-    Div32 d_nb, d_slots, d_each, d_seqs;
+    Div32 d_nb, d_each, d_D;
+    // write: a token's slots (as a norm's, heads padded to whole blocks) lie on
+    // `lanes` lanes, a power of two, or on `chunks` workgroups
+    uint32_t rows, slots, lanes, chunks, per_log, groups;
+    uint32_t run_log;            // 2^run_log consecutive workgroups per XCD in turn
+    Div32 d_chunks;
+    // read: a sequence's tokens on one rank are one span of values on both
+    // sides, cut into tiles of one vector per lane
+    uint32_t spans, tiles;
+    Div32 d_tiles, d_seqs;
 };
 
-// One lane's slot of a cache call, for slot idx < rows * slots.
-struct CacheSlot {
-    uint32_t row;                // write: token of P; read: row of the output
-    uint32_t h;                  // head of the row: of all H (write), of the rank's (read)
-    uint32_t blk, d;             // block, first value (d >= D: padding)
-    uint32_t r, i, t;            // rank, sequence, token of the sequence
-};
+constexpr uint32_t kCacheXcds = 8;
 
-UA2A_HD CacheSlot cache_slot(const CacheGeom& g, uint32_t idx, uint32_t V, bool write)
+// The group of tokens of a write's workgroup: workgroups go to the XCDs in
+// turn, and 2^run_log consecutive groups to one of them.
+UA2A_HD uint32_t cache_group(const CacheGeom& g, uint32_t id)
 {
-    CacheSlot c;
-    c.row = fdiv(idx, g.d_slots);
-    const uint32_t slot = idx - c.row * g.slots;
-    const uint32_t b = slot >> g.q_log;
-    c.h = fdiv(b, g.d_nb);
-    c.blk = b - c.h * g.sh.nb;
-    c.d = c.blk * kBlockValues + (slot & ((1u << g.q_log) - 1)) * V;
-    if (write) {
-        const uint32_t a = token_place(g.sh, c.row).a;
-        c.i = fdiv(a, g.d_each);
-        c.t = a - c.i * g.each;
-        c.r = fdiv(c.h, g.sh.d_hl);
-    } else {
-        const uint32_t ri = fdiv(c.row, g.d_each);
-        c.t = c.row - ri * g.each;
-        c.r = fdiv(ri, g.d_seqs);
-        c.i = ri - c.r * g.seqs;
-    }
-    return c;
+    const uint32_t xcd = id % kCacheXcds, q = id / kCacheXcds;
+    return ((((q >> g.run_log) * kCacheXcds) + xcd) << g.run_log) + (q & ((1u << g.run_log) - 1));
 }
 
-// Row of the cache, counted over its [w][seqs][cap] rows, for a slot's token;
-// -1 where there is none.  starts null: 0; counts null: all of the call's.
-UA2A_HD int64_t cache_row(const CacheGeom& g, const CacheSlot& s, const int32_t* starts, const int32_t* counts)
+struct WriteLane {
+    uint32_t token;              // of P
+    uint32_t slot;               // of the token
+    uint32_t in;                 // 0: none
+};
+
+// within: the lanes' part of the workgroup, tid / lanes.
+UA2A_HD WriteLane write_lane(const CacheGeom& g, uint32_t group, uint32_t within, uint32_t tid)
 {
-    const int64_t pos = (starts ? static_cast<int64_t>(starts[s.i]) : 0) + s.t;
-    const int64_t count = counts ? static_cast<int64_t>(counts[s.i]) : static_cast<int64_t>(g.each);
-    if (static_cast<int64_t>(s.t) >= count || pos < 0 || pos >= g.cap) return -1;
-    return (static_cast<int64_t>(s.r) * g.seqs + s.i) * g.cap + pos;
+    const uint32_t seg = (group << g.per_log) + within;
+    WriteLane l;
+    l.token = fdiv(seg, g.d_chunks);
+    l.slot = (seg - l.token * g.chunks) * g.lanes + (tid & (g.lanes - 1));
+    l.in = (l.token < g.rows && l.slot < g.slots) ? 1u : 0u;
+    return l;
+}
+
+// A sequence's tokens in this call that exist: [first, last), positions from `start`.
+struct CacheSpan {
+    int64_t start;
+    int64_t first, last;
+};
+
+UA2A_HD CacheSpan cache_span(const CacheGeom& g, int64_t start, int64_t count)
+{
+    CacheSpan s;
+    s.start = start;
+    s.first = s.start < 0 ? -s.start : 0;
+    s.last = count;
+    if (s.last > static_cast<int64_t>(g.each)) s.last = g.each;
+    if (s.last > g.cap - s.start) s.last = g.cap - s.start;
+    return s;
 }
 
 }  // namespace ua2a

@@ -205,15 +205,16 @@ int check_cache(ua2a_plan_t plan, const ua2a_cache_t* c, int64_t* values, int64_
 void cache_geometry(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t V, int64_t each, CacheGeom* g)
 {
     g->sh = shape_of(plan);
-    g->w = static_cast<uint32_t>(plan->w);
     g->seqs = static_cast<uint32_t>(c->sequences);
     g->each = static_cast<uint32_t>(each);
-    g->cap = c->capacity;
+    g->dense = plan->D % kBlockValues == 0 ? 1u : 0u;
     g->q_log = log2_of(kBlockValues / static_cast<uint32_t>(V));
+    g->cap = c->capacity;
     g->part = c->sequences * c->capacity * plan->H * plan->D;
     g->part_scales = c->sequences * c->capacity * plan->H * g->sh.nb;
     g->d_nb = make_div32(g->sh.nb);
     g->d_each = make_div32(g->each);
+    g->d_D = make_div32(g->sh.D);
     g->d_seqs = make_div32(g->seqs);
 }
 
@@ -411,11 +412,24 @@ int ua2a_cache_write(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t type, cons
     L.V = wide ? 16 / plan->elem_bytes : 1;
     CacheArgs& a = L.cache;
     cache_geometry(plan, c, L.V, gathered / c->sequences, &a.g);
-    const int64_t row = plan->H * a.g.sh.nb * (kBlockValues / L.V);
+    CacheGeom& g = a.g;
+    const int64_t row = plan->H * g.sh.nb * (kBlockValues / L.V);
     if (row > kMaxSlots / gathered) return UA2A_ERR_SHAPE;
-    a.g.slots = static_cast<uint32_t>(row);
-    a.g.rows = static_cast<uint32_t>(gathered);
-    a.g.d_slots = make_div32(a.g.slots);
+    g.rows = static_cast<uint32_t>(gathered);
+    g.slots = static_cast<uint32_t>(row);
+    g.lanes = 1;
+    while (g.lanes < kActBlock && g.lanes < g.slots) g.lanes *= 2;
+    g.chunks = (g.slots + g.lanes - 1) / g.lanes;
+    g.d_chunks = make_div32(g.chunks);
+    g.per_log = log2_of(kActBlock / g.lanes);
+    const int64_t groups = ((gathered * g.chunks) + (int64_t(1) << g.per_log) - 1) >> g.per_log;
+    // as many groups in a row to an XCD as fill lines of a rank's scales
+    g.run_log = 0;
+    while (g.run_log < 6 && (int64_t(g.sh.hl) * g.sh.nb << (g.run_log + g.per_log)) < kLineBytes * g.chunks) ++g.run_log;
+    const int64_t turn = int64_t(kCacheXcds) << g.run_log;
+    const int64_t wgs = (groups + turn - 1) / turn * turn;
+    if (wgs > kMaxSlots / kActBlock) return UA2A_ERR_SHAPE;
+    g.groups = static_cast<uint32_t>(groups);
     const int64_t bytes = plan->layout.tensor_bytes;
     const Range ins[] = {{k, bytes}, {v, bytes}, {starts, c->sequences * 4}, {counts, c->sequences * 4}};
     const Range outs[] = {{c->codes, values}, {c->scales, nscales}};
@@ -430,8 +444,8 @@ int ua2a_cache_write(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t type, cons
     a.counts = counts;
     a.format = c->format;
     L.block = kActBlock;
-    L.grid_x = static_cast<uint32_t>((row * gathered + kActBlock - 1) / kActBlock);
-    L.grid_y = 2;
+    L.grid_x = static_cast<uint32_t>(wgs);
+    L.grid_y = 1;
     const int err = act_launch(L, stream);
     return err == 0 ? UA2A_OK : fail(plan, "launching the cache write", err);
 }
@@ -458,13 +472,18 @@ int ua2a_cache_read(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t type, int64
     L.V = wide ? 16 / plan->elem_bytes : 1;
     CacheArgs& a = L.cache;
     cache_geometry(plan, c, L.V, n, &a.g);
-    const int64_t row = int64_t(a.g.sh.hl) * a.g.sh.nb * (kBlockValues / L.V);
+    CacheGeom& g = a.g;
     if (c->sequences > kMaxSlots / plan->w || c->sequences * plan->w > kMaxSlots / n) return UA2A_ERR_SHAPE;
-    const int64_t rows = c->sequences * plan->w * n;
-    if (row > kMaxSlots / rows) return UA2A_ERR_SHAPE;
-    a.g.slots = static_cast<uint32_t>(row);
-    a.g.rows = static_cast<uint32_t>(rows);
-    a.g.d_slots = make_div32(a.g.slots);
+    const int64_t spans = c->sequences * plan->w, rows = spans * n;
+    // a span's vectors, on whole waves of up to kActBlock lanes
+    if (n > kMaxSlots / (int64_t(g.sh.run) / L.V + 1)) return UA2A_ERR_SHAPE;
+    const int64_t vectors = n * (g.sh.run / static_cast<uint32_t>(L.V));
+    L.block = vectors >= kActBlock ? kActBlock : static_cast<uint32_t>((vectors + 63) / 64 * 64);
+    const int64_t tiles = (vectors + L.block - 1) / L.block;
+    if (tiles > kMaxSlots / L.block / spans) return UA2A_ERR_SHAPE;
+    g.spans = static_cast<uint32_t>(spans);
+    g.tiles = static_cast<uint32_t>(tiles);
+    g.d_tiles = make_div32(g.tiles);
     const int64_t bytes = rows * a.g.sh.hl * plan->D * plan->elem_bytes;
     const Range ins[] = {{c->codes, values}, {c->scales, nscales}, {starts, c->sequences * 4},
                          {counts, c->sequences * 4}};
@@ -479,9 +498,8 @@ int ua2a_cache_read(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t type, int64
     a.starts = starts;
     a.counts = counts;
     a.format = c->format;
-    L.block = kActBlock;
-    L.grid_x = static_cast<uint32_t>((row * rows + kActBlock - 1) / kActBlock);
-    L.grid_y = 2;
+    L.grid_x = static_cast<uint32_t>(spans * tiles);
+    L.grid_y = 1;
     const int err = act_launch(L, stream);
     return err == 0 ? UA2A_OK : fail(plan, "launching the cache read", err);
 }

@@ -4,20 +4,6 @@
 namespace ua2a {
 namespace {
 
-// Arguments up front: these empty statements take what the way to the first
-// load reads as scalar-register inputs, so that it is requested in one batch
-// and waited for once, rather than field by field through dependent branches.
-__device__ __forceinline__ void args_up_front(const NormArgs& a)
-{
-    const NormGeom& g = a.g;
-    asm volatile("" ::"s"(g.sh.H), "s"(g.sh.D), "s"(g.sh.nb), "s"(g.sh.hl), "s"(g.sh.S), "s"(g.sh.B), "s"(g.sh.SG),
-                 "s"(g.sh.d_S.m), "s"(g.sh.d_S.s), "s"(g.sh.d_B.m),
-                 "s"(g.sh.d_B.s), "s"(g.sh.d_run.m), "s"(g.sh.d_run.s), "s"(g.sh.run), "s"(g.sh.a_rank), "s"(g.heads), "s"(g.per_token), "s"(g.slots));
-    asm volatile("" ::"s"(g.q_log), "s"(g.head_log), "s"(g.padded), "s"(g.dense), "s"(g.lanes), "s"(g.per_log), "s"(g.segs), "s"(g.groups),
-                 "s"(g.d_per.m), "s"(g.d_per.s), "s"(a.flags), "s"(a.eps),
-                 "s"(a.inv_len), "s"(a.x), "s"(a.weight), "s"(a.out));
-}
-
 // RMS norm joined with the exchange.  A segment's lanes hold it in registers
 // between the pass that sums its squares and the one that writes, so every
 // value is read once.  One workgroup per group of segments: workgroups that
@@ -28,7 +14,6 @@ template <class T, class W, int V, Span SPAN, int ITEMS, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void ua2a_norm_kernel(NormArgs a)
 {
     __shared__ float red[2][16];
-    args_up_front(a);
     const NormGeom& g = a.g;
     const uint32_t flags = a.flags;
     const bool mode1 = flags & kNormMode1;
