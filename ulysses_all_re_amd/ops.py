@@ -26,6 +26,12 @@ growth, and rebuilds the chunked plans that borrowed the old one.  Calls on
 one stream share its window in stream order; other streams get windows of
 their own.
 
+``norm_all_to_all_4D`` is the same entry point with an RMS norm on the
+head-complete side: before the exchange in mode 0 (query and key norms), after
+it in mode 1 (a sub-layer norm, with the residual's addition), each in one
+launch forward and one or two backward.  ``checkpoint`` keeps what the backward
+pass needs of the activations in 8 bits, a little over half a 2-byte type.
+
 Both caches are bounded: at most ``MAX_PLANS`` plans and ``MAX_WINDOWS``
 windows are kept, the least recently used going first (a window's plans go
 with it).  A dropped window returns to torch's allocator in its own stream's
@@ -38,6 +44,7 @@ from __future__ import annotations
 import logging
 import threading
 from collections import OrderedDict
+from typing import Optional, Tuple
 
 import torch
 
@@ -176,3 +183,162 @@ def all_to_all_4D(x: torch.Tensor, scatter_dim: int, gather_dim: int, w: int,
         raise ValueError(f"unsupported (scatter_dim, gather_dim) = ({scatter_dim}, {gather_dim}); "
                          "use (2, 1) for heads -> sequence or (1, 2) for the inverse")
     return exchange(x, w, mode, chunked)
+
+
+# ------------------------------------------------------- norms with the exchange
+
+_FORMATS = {0: None, 1: torch.float8_e4m3fn, 2: torch.float8_e5m2}
+
+
+def _format_code(dtype, what: str) -> int:
+    for code, d in _FORMATS.items():
+        if d == dtype:
+            return code
+    raise TypeError(f"{what} must be torch.float8_e4m3fn, torch.float8_e5m2 or None, not {dtype}")
+
+
+def _norm_shapes(shape, w: int, mode: int, per_head: bool):
+    """(P shape, out shape, rstd shape, blocks per head) of a norm's input shape."""
+    out = _out_shape(shape, w, mode)
+    p = tuple(shape) if mode == 0 else out
+    return p, out, p[:4] if per_head else p[:3], -(-p[4] // 32)
+
+
+@torch.library.custom_op("ua2a::norm_exchange", mutates_args=())
+def norm_exchange(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Optional[torch.Tensor], w: int, mode: int,
+                  per_head: bool, eps: float, out_format: int, saved_format: int) -> Tuple[
+                      torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """RMS norm joined with the rank-stacked exchange on the GPU: (out, scales,
+    sum, saved, saved_scales, rstd) as ``Plan.norm_exchange`` returns them,
+    empty tensors for what the call does not have; formats 0 none, 1 e4m3, 2 e5m2."""
+    if mode not in (0, 1):
+        raise ValueError("mode must be 0 or 1")
+    if x.device.type != "cuda":
+        raise RuntimeError(f"the exchange runs on the GPU only (got a {x.device.type} tensor)")
+    B, S, H, D = _local_shape(x.shape, w, mode)
+    if residual is not None:
+        residual = residual.contiguous()
+    if weight is not None:
+        weight = weight.contiguous()
+    with _lock:
+        plan = _plan_for(w, B, S, H, D, x.dtype, x.device)
+        r = plan.norm_exchange(x.contiguous(), weight, mode, residual=residual, per_head=per_head, eps=eps,
+                               out_dtype=_FORMATS[out_format], checkpoint=_FORMATS[saved_format], rstd=True)
+    none = x.new_empty(0)
+    return tuple(none.clone() if t is None else t for t in r)
+
+
+@norm_exchange.register_fake
+def _norm_exchange_fake(x, weight, residual, w, mode, per_head, eps, out_format, saved_format):
+    p, out, stat, nb = _norm_shapes(x.shape, w, mode, per_head)
+    e8 = torch.float8_e8m0fnu
+    return (x.new_empty(out, dtype=_FORMATS[out_format] or x.dtype),
+            x.new_empty(out[:-1] + (nb,), dtype=e8) if out_format else x.new_empty(0),
+            x.new_empty(p) if residual is not None else x.new_empty(0),
+            x.new_empty(p, dtype=_FORMATS[saved_format]) if saved_format else x.new_empty(0),
+            x.new_empty(p[:-1] + (nb,), dtype=e8) if saved_format else x.new_empty(0),
+            x.new_empty(stat, dtype=torch.float32))
+
+
+@torch.library.custom_op("ua2a::norm_exchange_backward", mutates_args=())
+def norm_exchange_backward(dy: torch.Tensor, weight: Optional[torch.Tensor], saved: torch.Tensor,
+                           saved_scales: Optional[torch.Tensor], rstd: torch.Tensor, dsum: Optional[torch.Tensor], w: int,
+                           mode: int, per_head: bool, residual: bool, dweight: bool) -> Tuple[
+                               torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dx, dresidual, dweight) as ``Plan.norm_exchange_backward`` returns them;
+    dresidual is empty where it is dx (mode 0) or there is no residual."""
+    B, S, H, D = _local_shape(dy.shape, w, 1 - mode)
+    if dsum is not None:
+        dsum = dsum.contiguous()
+    if weight is not None:
+        weight = weight.contiguous()
+    with _lock:
+        plan = _plan_for(w, B, S, H, D, dy.dtype, dy.device)
+        r = plan.norm_exchange_backward(dy.contiguous(), weight, mode, saved.contiguous(), rstd,
+                                        saved_scales=saved_scales, dsum=dsum, residual=residual, per_head=per_head,
+                                        dweight=dweight)
+    none = dy.new_empty(0)
+    return (r.dx, r.dresidual if residual and mode == 1 else none, none.clone() if r.dweight is None else r.dweight)
+
+
+@norm_exchange_backward.register_fake
+def _norm_exchange_backward_fake(dy, weight, saved, saved_scales, rstd, dsum, w, mode, per_head, residual, dweight):
+    x = _out_shape(dy.shape, w, 1 - mode)
+    return (dy.new_empty(x), dy.new_empty(tuple(dy.shape)) if residual and mode == 1 else dy.new_empty(0),
+            dy.new_empty(weight.shape, dtype=torch.float32) if weight is not None and dweight else dy.new_empty(0))
+
+
+def _norm_setup_context(ctx, inputs, output):
+    x, weight, residual, w, mode, per_head, eps, out_format, saved_format = inputs
+    out, scales, total, saved, saved_scales, rstd = output
+    ctx.mark_non_differentiable(scales, saved, saved_scales, rstd)
+    ctx.set_materialize_grads(False)
+    ctx.args = (w, mode, per_head, residual is not None)
+    ctx.weight = weight is not None
+    if saved_format:
+        kept = (saved, saved_scales)
+    else:
+        kept = (x if residual is None else total, None)
+    ctx.save_for_backward(weight, *kept, rstd)
+
+
+def _norm_backward(ctx, g_out, g_scales, g_sum, g_saved, g_saved_scales, g_rstd):
+    weight, saved, saved_scales, rstd = ctx.saved_tensors
+    w, mode, per_head, residual = ctx.args
+    if g_out is None:
+        if g_sum is None:
+            return (None,) * 9
+        g_out = g_sum.new_zeros(_out_shape(g_sum.shape, w, 0) if mode == 0 else g_sum.shape)
+    dx, dres, dw = norm_exchange_backward(g_out, weight, saved, saved_scales, rstd, g_sum, w, mode, per_head, residual,
+                                          ctx.weight and ctx.needs_input_grad[1])
+    dres = (dx if mode == 0 else dres) if residual and ctx.needs_input_grad[2] else None
+    dw = dw.to(weight.dtype) if ctx.weight and ctx.needs_input_grad[1] else None
+    return dx, dw, dres, None, None, None, None, None, None
+
+
+norm_exchange.register_autograd(_norm_backward, setup_context=_norm_setup_context)
+
+
+def norm_all_to_all_4D(x: torch.Tensor, weight: Optional[torch.Tensor], scatter_dim: int, gather_dim: int, w: int,
+                       residual: Optional[torch.Tensor] = None, per_head: bool = False, eps: float = 1e-6,
+                       checkpoint=None, out_dtype=None):
+    """``all_to_all_4D`` with an RMS norm on the head-complete side, in one launch.
+
+    (2, 1): the norm of ``x`` (+ ``residual``), then heads scattered and the
+    sequence gathered; (1, 2): the inverse exchange of ``x`` (+ ``residual``),
+    then the norm.  ``weight``: one value per head value, [H*D], or with
+    ``per_head`` one norm per head and [D]; of x's dtype or float32, None for
+    ones.  ``residual`` is head-complete, ``[w, B, S_local, H, D]``.
+
+    Returns out, with a residual (out, sum): the sum that was normed, in x's
+    dtype.  ``out_dtype`` (torch.float8_e4m3fn or e5m2) makes out a pair (codes,
+    scales) with one power-of-two scale per 32 values along D; such a call has
+    no gradient.  ``checkpoint`` (the same dtypes) keeps 8 bits of what was
+    normed for the backward pass in place of the values: its gradients are those
+    of the norm at the values that the 8 bits stand for, with the exact rstd.
+    """
+    if (scatter_dim, gather_dim) == (2, 1):
+        mode = 0
+    elif (scatter_dim, gather_dim) == (1, 2):
+        mode = 1
+    else:
+        raise ValueError(f"unsupported (scatter_dim, gather_dim) = ({scatter_dim}, {gather_dim}); "
+                         "use (2, 1) for heads -> sequence or (1, 2) for the inverse")
+    out_format, saved_format = _format_code(out_dtype, "out_dtype"), _format_code(checkpoint, "checkpoint")
+    wants = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, residual))
+    if out_format and wants:
+        raise ValueError("an 8-bit result has no gradient: call it under torch.no_grad()")
+    if not wants:
+        saved_format = 0                                   # nothing to keep
+    p, _, _, _ = _norm_shapes(x.shape, w, mode, per_head)
+    if residual is not None and tuple(residual.shape) != p:
+        raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {p}")
+    if residual is not None and residual.dtype != x.dtype:
+        raise TypeError(f"residual has dtype {residual.dtype}, x has {x.dtype}")
+    n = p[4] if per_head else p[3] * p[4]
+    if weight is not None and tuple(weight.shape) != (n,):
+        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected {(n,)}")
+    out, scales, total, _, _, _ = norm_exchange(x, weight, residual, w, mode, per_head, eps, out_format, saved_format)
+    if out_format:
+        out = (out, scales)
+    return out if residual is None else (out, total)
