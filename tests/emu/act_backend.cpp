@@ -319,7 +319,7 @@ void columns(const ActLaunch& L)
 {
     const ColumnArgs& a = L.columns;
     Buf in(a.partial, int64_t(a.rows) * a.cols * 4), out(a.out, int64_t(a.cols) * 4);
-    for (uint32_t c = 0; c < L.grid_x * 32; ++c) {
+    for (uint32_t c = 0; c < L.grid_x << a.across_log; ++c) {
         if (c >= a.cols) continue;
         float t = 0.f;
         for (uint32_t r = 0; r < a.rows; ++r) t += get(in, int64_t(r) * a.cols + c, UA2A_TYPE_FP32);
@@ -394,6 +394,9 @@ void cache_read(const ActLaunch& L)
                 const int64_t row = int64_t(ri) * g.cap + s.start;
                 for (int32_t k = 0; k < L.V; ++k) {
                     const int64_t h = (at + k) / g.sh.D, d = (at + k) % g.sh.D;
+                    if (k == 0 && !g.dense && scale_of_value(g, int64_t(tile) * L.block * L.V, tid * L.V) !=
+                                                  h * g.sh.nb + d / kBlockValues)
+                        flag(1);
                     double f = code_value(get8(codes, (y ? g.part : 0) + row * g.sh.run + at + k), a.format) *
                                ldexp(1.0, get8(scales, (y ? g.part_scales : 0) + row * g.sh.hl * g.sh.nb + h * g.sh.nb +
                                                            d / kBlockValues) - 127);

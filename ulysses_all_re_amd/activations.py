@@ -13,9 +13,12 @@ tensors of the exchange's layouts themselves.
 from __future__ import annotations
 
 import ctypes
+import sys
 from typing import NamedTuple, Optional
 
-from . import UA2A_OK, UA2AError
+from . import UA2A_ERR_DEVICE, UA2A_OK, UA2AError
+
+_pkg = sys.modules[__package__]      # its functions are looked up when they are called
 
 UA2A_BLOCK = 32          # values that share a scale
 
@@ -150,8 +153,11 @@ class Cache:
         return cache
 
     def _set(self, codes, scales) -> None:
+        import torch
         self.codes, self.scales = codes, scales
+        self.device, self.int32 = codes.device, torch.int32
         _, self.w, self.sequences, self.capacity, self.heads, self.D = codes.shape
+        self.per_sequence = (self.sequences,)
         self._struct = ua2a_cache_t(codes.data_ptr(), scales.data_ptr(), self.sequences, self.capacity,
                                     _format_of(codes.dtype, "codes"))
         self._ref = ctypes.byref(self._struct)
@@ -185,32 +191,61 @@ class ActivationCalls:
         if weight is None:
             return 0
         n = self.D if per_head else self.H * self.D
-        if weight.dtype != self.dtype and weight.dtype not in _types()[0]:
+        code = _types()[0].get(weight.dtype)
+        if code is None or (code != 2 and weight.dtype is not self.dtype):
             raise TypeError(f"weight has dtype {weight.dtype}, expected {self.dtype} or float32")
-        code = _types()[0][weight.dtype]
-        if weight.dtype != self.dtype and code != 2:
-            raise TypeError(f"weight has dtype {weight.dtype}, expected {self.dtype} or float32")
-        self._expect(weight, weight.dtype, (n,), "weight")
+        if not self._fits(weight, weight.dtype, (n,)):
+            self._expect(weight, weight.dtype, (n,), "weight")
         return code
 
     def _rstd_shape(self, per_head: bool):
         lead = (self.w, self.B, self.S_local)
         return lead + (self.H,) if per_head else lead
 
-    def _issue(self, fn, name: str, stream, *args) -> None:
-        """fn(handle, *args, stream) on `stream` (None: torch's current one), with the
-        plan's device current."""
-        from . import UA2A_ERR_DEVICE, _current_raw_stream, ua2a_plan_last_error
-        import torch
-        sptr = (_current_raw_stream(self.device) if stream is None else stream.cuda_stream) or None
+    def _fits(self, t, dtype, shape) -> bool:
+        """Whether t is a contiguous tensor of the given type and shape on the plan's device."""
+        return t.shape == shape and t.dtype is dtype and t.device == self.device and t.is_contiguous()
+
+    def _issue(self, name: str, stream, *args) -> None:
+        """The library's `name`(handle, *args, stream) on `stream` (None: torch's
+        current one), with the plan's device current."""
+        sptr = (_pkg._current_raw_stream(self.device) if stream is None else stream.cuda_stream) or None
         handle = self.handle
+        fn = getattr(_pkg._lib or _pkg.load_library(), name)
         rc = fn(handle, *args, sptr)
+        if rc == UA2A_OK:
+            return
         if rc == UA2A_ERR_DEVICE and handle:
             # another device is current: the library changed nothing; retry on the plan's
+            import torch
             with torch.cuda.device(self.device):
                 rc = fn(handle, *args, sptr)
         if rc != UA2A_OK:
-            raise UA2AError(rc, name, ua2a_plan_last_error(handle) if handle else "")
+            raise UA2AError(rc, name, _pkg.ua2a_plan_last_error(handle) if handle else "")
+
+    def _norm_spec(self, mode, per_head, out_dtype, checkpoint, rstd, residual):
+        """What a kind of norm_exchange call takes and gives, worked out once:
+        (type code, format codes, x's shape, P shape, ((dtype, shape) or None)
+        of each result)."""
+        specs = self.__dict__.setdefault("_norm_specs", {})
+        key = (mode, per_head, out_dtype, checkpoint, rstd, residual)
+        spec = specs.get(key)
+        if spec is None:
+            import torch
+            code = self._type()
+            if mode not in (0, 1):
+                raise ValueError("mode must be 0 or 1")
+            ofmt, sfmt = _format_of(out_dtype, "out_dtype"), _format_of(checkpoint, "checkpoint")
+            p, oshape, nb = self.in_shape(0), self.out_shape(mode), (_blocks(self.D),)
+            e8 = torch.float8_e8m0fnu
+            want = ((self.dtype if out_dtype is None else out_dtype, oshape),
+                    (e8, oshape[:-1] + nb) if ofmt else None,
+                    (self.dtype, p) if residual else None,
+                    (checkpoint, p) if sfmt else None,
+                    (e8, p[:-1] + nb) if sfmt else None,
+                    (torch.float32, self._rstd_shape(per_head)) if rstd or sfmt else None)
+            spec = specs[key] = (code, ofmt, sfmt, self.in_shape(mode), p, want)
+        return spec
 
     def _on_stream(self, stream):
         """Allocations inside belong to `stream`, so that torch reuses their memory
@@ -236,40 +271,27 @@ class ActivationCalls:
         ``norm_exchange_backward`` needs; ``rstd=True`` returns rstd alone.
         ``out``: an earlier result whose tensors are written again.
         """
-        import torch
-        code = self._type()
-        if mode not in (0, 1):
-            raise ValueError("mode must be 0 or 1")
-        ofmt, sfmt = _format_of(out_dtype, "out_dtype"), _format_of(checkpoint, "checkpoint")
-        self._check(x, self.in_shape(mode), "input")
-        p, oshape = self.in_shape(0), self.out_shape(mode)
-        if residual is not None:
+        per_head = bool(per_head)
+        code, ofmt, sfmt, xshape, p, want = self._norm_spec(mode, per_head, out_dtype, checkpoint, bool(rstd),
+                                                            residual is not None)
+        if not self._fits(x, self.dtype, xshape):
+            self._check(x, xshape, "input")
+        if residual is not None and not self._fits(residual, self.dtype, p):
             self._check(residual, p, "residual")
-        wcode = self._weight(weight, per_head)
-        odt = self.dtype if out_dtype is None else out_dtype
-        nb = (_blocks(self.D),)
-        rstd = rstd or checkpoint is not None
-        want = (
-            (odt, oshape),
-            (torch.float8_e8m0fnu, oshape[:-1] + nb) if ofmt else None,
-            (self.dtype, p) if residual is not None else None,
-            (checkpoint, p) if sfmt else None,
-            (torch.float8_e8m0fnu, p[:-1] + nb) if sfmt else None,
-            (torch.float32, self._rstd_shape(per_head)) if rstd else None,
-        )
+        wcode = self._weight(weight, per_head) if weight is not None else 0
         if out is None:
+            import torch
             with self._on_stream(stream):
                 out = NormExchange(*(None if q is None else torch.empty(q[1], dtype=q[0], device=self.device)
                                      for q in want))
         else:
             for name, t, q in zip(NormExchange._fields, out, want):
-                if q is not None:
+                if q is not None and (t is None or not self._fits(t, q[0], q[1])):
                     self._expect(t, q[0], q[1], f"out.{name}")
-            out = NormExchange(*(t if q is not None else None for t, q in zip(out, want)))
-        args = ua2a_norm_t(x.data_ptr(), _ptr(residual), _ptr(weight), *map(_ptr, out), eps, code, wcode,
-                           int(bool(per_head)), ofmt, sfmt)
-        from . import load_library
-        self._issue(load_library().ua2a_norm_exchange, "ua2a_norm_exchange", stream, mode, ctypes.byref(args))
+            out = NormExchange(*[t if q is not None else None for t, q in zip(out, want)])
+        args = ua2a_norm_t(x.data_ptr(), _ptr(residual), _ptr(weight), *[None if t is None else t.data_ptr() for t in out],
+                           eps, code, wcode, per_head, ofmt, sfmt)
+        self._issue("ua2a_norm_exchange", stream, mode, ctypes.byref(args))
         return out
 
     def norm_exchange_backward(self, dy, weight, mode: int, saved, rstd, *, saved_scales=None, dsum=None,
@@ -286,7 +308,7 @@ class ActivationCalls:
         ``dweight=False``).  ``out``: an earlier result to write again.
         """
         import torch
-        from . import load_library
+        per_head = bool(per_head)
         code = self._type()
         if mode not in (0, 1):
             raise ValueError("mode must be 0 or 1")
@@ -310,14 +332,13 @@ class ActivationCalls:
         dweight = bool(dweight) and weight is not None
         wshape = (self.D if per_head else self.H * self.D,)
         apart = residual and mode == 1
-        lib = load_library()
         space, nspace = None, 0
         if dweight:
             spaces = self.__dict__.setdefault("_norm_workspace", {})
             nspace = spaces.get(per_head)
             if nspace is None:
                 n = ctypes.c_int64()
-                rc = lib.ua2a_norm_workspace(self.handle, int(bool(per_head)), ctypes.byref(n))
+                rc = _pkg.load_library().ua2a_norm_workspace(self.handle, per_head, ctypes.byref(n))
                 if rc != UA2A_OK:
                     raise UA2AError(rc, "ua2a_norm_workspace")
                 nspace = spaces[per_head] = n.value
@@ -334,20 +355,19 @@ class ActivationCalls:
                 dw = self._expect(out.dweight, torch.float32, wshape, "out.dweight") if dweight else None
         args = ua2a_norm_grad_t(dy.data_ptr(), _ptr(dsum), saved.data_ptr(), _ptr(saved_scales), _ptr(weight),
                                 rstd.data_ptr(), dx.data_ptr(), _ptr(dres), _ptr(dw), _ptr(space), nspace, code, wcode,
-                                int(bool(per_head)), fmt, int(mode == 1 and not residual and fmt == 0))
-        self._issue(lib.ua2a_norm_exchange_backward, "ua2a_norm_exchange_backward", stream, mode, ctypes.byref(args))
+                                per_head, fmt, int(mode == 1 and not residual and fmt == 0))
+        self._issue("ua2a_norm_exchange_backward", stream, mode, ctypes.byref(args))
         return NormGradients(dx, dres if apart else dx if residual else None, dw)
 
     def _check_cache(self, cache: Cache, starts, counts) -> None:
-        import torch
-        if (cache.w, cache.heads, cache.D) != (self.w, self.H // self.w, self.D):
+        if (cache.w, cache.heads * cache.w, cache.D) != (self.w, self.H, self.D):
             raise ValueError(f"cache has w = {cache.w}, {cache.heads} heads of {cache.D} per rank; "
                              f"the plan w = {self.w}, {self.H // self.w} of {self.D}")
-        if cache.codes.device != self.device:
-            raise ValueError(f"cache is on {cache.codes.device}, plan is on {self.device}")
+        if cache.device != self.device:
+            raise ValueError(f"cache is on {cache.device}, plan is on {self.device}")
         for t, what in ((starts, "starts"), (counts, "counts")):
-            if t is not None:
-                self._expect(t, torch.int32, (cache.sequences,), what)
+            if t is not None and not self._fits(t, cache.int32, cache.per_sequence):
+                self._expect(t, cache.int32, cache.per_sequence, what)
 
     def cache_write(self, cache: Cache, k, v, starts, counts=None, stream=None) -> Cache:
         """The mode-0 exchange of new keys and values (P layout; one may be
@@ -365,12 +385,11 @@ class ActivationCalls:
             raise ValueError("nothing to write: k and v are both None")
         if starts is None:
             raise ValueError("starts is missing")
+        shape = (self.w, self.B, self.S_local, self.H, self.D)
         for t, what in ((k, "k"), (v, "v")):
-            if t is not None:
-                self._check(t, self.in_shape(0), what)
-        from . import load_library
-        self._issue(load_library().ua2a_cache_write, "ua2a_cache_write", stream, cache._ref, code, _ptr(k), _ptr(v),
-                    starts.data_ptr(), _ptr(counts))
+            if t is not None and not self._fits(t, self.dtype, shape):
+                self._check(t, shape, what)
+        self._issue("ua2a_cache_write", stream, cache._ref, code, _ptr(k), _ptr(v), starts.data_ptr(), _ptr(counts))
         return cache
 
     def cache_read(self, cache: Cache, tokens: int, starts=None, counts=None, out=None, stream=None):
@@ -380,23 +399,22 @@ class ActivationCalls:
         without a position are left as they were, zeros without ``out``; an
         entry of ``out`` that is None is not read.
         """
-        import torch
-        from . import load_library
         code = self._type()
         self._check_cache(cache, starts, counts)
         if tokens < 1:
             raise ValueError(f"tokens must be at least 1, not {tokens}")
         shape = (self.w, cache.sequences, tokens, self.H // self.w, self.D)
         if out is None:
+            import torch
             with self._on_stream(stream):
                 out = tuple(torch.zeros(shape, dtype=self.dtype, device=self.device) for _ in range(2))
         else:
             if len(out) != 2 or (out[0] is None and out[1] is None):
                 raise ValueError("out must be (k, v), one of which may be None")
             for t, what in zip(out, ("out[0]", "out[1]")):
-                if t is not None:
+                if t is not None and not self._fits(t, self.dtype, shape):
                     self._check(t, shape, what)
             out = tuple(out)
-        self._issue(load_library().ua2a_cache_read, "ua2a_cache_read", stream, cache._ref, code, tokens, _ptr(starts),
-                    _ptr(counts), _ptr(out[0]), _ptr(out[1]))
+        self._issue("ua2a_cache_read", stream, cache._ref, code, tokens, _ptr(starts), _ptr(counts), _ptr(out[0]),
+                    _ptr(out[1]))
         return out

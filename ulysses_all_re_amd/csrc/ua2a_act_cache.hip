@@ -87,11 +87,8 @@ __global__ __launch_bounds__(kActBlock) void ua2a_cache_read_kernel(CacheArgs a)
     if (e < s.first * g.sh.run || e >= s.last * g.sh.run) return;
     const int64_t row = static_cast<int64_t>(ri) * g.cap + s.start;             // of the span's first token
     const uint32_t nscales = g.sh.hl * g.sh.nb;
-    int64_t at_scale = e / kBlockValues;
-    if (!g.dense) {
-        const int64_t h = e / g.sh.D;
-        at_scale = h * g.sh.nb + static_cast<uint32_t>(e - h * g.sh.D) / kBlockValues;
-    }
+    const int64_t at_scale = g.dense ? e / kBlockValues
+                                     : scale_of_value(g, static_cast<int64_t>(tile) * (blockDim.x * V), threadIdx.x * V);
     const uint8_t* codes = a.codes + row * g.sh.run + e;
     const uint8_t* scales = a.scales + row * nscales + at_scale;
     const int64_t to = static_cast<int64_t>(ri) * g.each * g.sh.run;

@@ -218,4 +218,14 @@ UA2A_HD CacheSpan cache_span(const CacheGeom& g, int64_t start, int64_t count)
     return s;
 }
 
+// The scale of value e0 + f of a span of whole heads, e0 uniform, f < 2^16: the
+// head by 32-bit arithmetic but for spans past 2^32 values.
+UA2A_HD int64_t scale_of_value(const CacheGeom& g, int64_t e0, uint32_t f)
+{
+    const int64_t h0 = (e0 >> 32) == 0 ? static_cast<int64_t>(fdiv(static_cast<uint32_t>(e0), g.d_D)) : e0 / g.sh.D;
+    const uint32_t x = static_cast<uint32_t>(e0 - h0 * g.sh.D) + f;             // < D + 2^16
+    const uint32_t h = fdiv(x, g.d_D);
+    return (h0 + h) * g.sh.nb + (x - h * g.sh.D) / kBlockValues;
+}
+
 }  // namespace ua2a

@@ -384,8 +384,9 @@ int ua2a_norm_exchange_backward(ua2a_plan_t plan, int32_t mode, const ua2a_norm_
     L.columns.out = n->dweight;
     L.columns.rows = rows;
     L.columns.cols = cols;
+    L.columns.across_log = cols >= 1024 ? 5 : 3;                // lines of 128 bytes, or of 32
     L.block = 1024;
-    L.grid_x = (cols + 31) / 32;
+    L.grid_x = (cols + (1u << L.columns.across_log) - 1) >> L.columns.across_log;
     err = act_launch(L, stream);
     return err == 0 ? UA2A_OK : fail(plan, "launching the weight gradient's sum", err);
 }

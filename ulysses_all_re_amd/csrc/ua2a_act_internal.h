@@ -70,6 +70,7 @@ struct ColumnArgs {              // dweight[c] = sum over rows of partial[row][c
     const float* partial;
     float* out;
     uint32_t rows, cols;
+    uint32_t across_log;         // columns of a workgroup = 2^across_log
 };
 
 struct CacheArgs {

@@ -200,32 +200,38 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a)
     }
 }
 
-// Column sums of the workgroups' rows: 32 columns per workgroup, 32 lanes
-// down each with eight loads in flight, joined in order.
-__global__ __launch_bounds__(1024) void ua2a_columns_kernel(ColumnArgs a)
+// Column sums of the workgroups' rows, joined in a fixed order: 2^across_log
+// columns per workgroup, its other lanes down the rows with eight loads in
+// flight each.  Few columns take narrow workgroups, so that a lane has few rows
+// to wait for (64 columns of 1024 rows: 32 wide 3.9 us).
+constexpr int kColumnsBlock = 1024;
+__global__ __launch_bounds__(kColumnsBlock) void ua2a_columns_kernel(ColumnArgs a)
 {
-    __shared__ float part[32][33];
-    const uint32_t c = blockIdx.x * 32 + (threadIdx.x & 31);
-    const uint32_t r0 = threadIdx.x >> 5;
+    __shared__ float part[kColumnsBlock / 64][64];
+    const uint32_t across = 1u << a.across_log;
+    const uint32_t down = kColumnsBlock >> a.across_log;
+    const uint32_t c = blockIdx.x * across + (threadIdx.x & (across - 1));
     float t = 0.f;
     if (c < a.cols) {
         const float* p = a.partial + c;
-        uint32_t r = r0;
-        for (; r + 7 * 32 < a.rows; r += 8 * 32) {
+        uint32_t r = threadIdx.x >> a.across_log;
+        for (; r + 7 * down < a.rows; r += 8 * down) {
             float v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = p[static_cast<int64_t>(r + 32 * k) * a.cols];
+            for (int k = 0; k < 8; ++k) v[k] = p[static_cast<int64_t>(r + k * down) * a.cols];
 #pragma unroll
             for (int k = 0; k < 8; ++k) t += v[k];
         }
-        for (; r < a.rows; r += 32) t += p[static_cast<int64_t>(r) * a.cols];
+        for (; r < a.rows; r += down) t += p[static_cast<int64_t>(r) * a.cols];
     }
-    part[r0][threadIdx.x & 31] = t;
+    for (uint32_t step = across; step < 64; step *= 2) t += __shfl_xor(t, static_cast<int>(step));
+    const uint32_t lane = threadIdx.x & 63;
+    if (lane < across) part[threadIdx.x >> 6][lane] = t;
     __syncthreads();
-    if (r0 == 0 && c < a.cols) {
+    if (threadIdx.x < across && c < a.cols) {
         t = 0.f;
 #pragma unroll
-        for (uint32_t k = 0; k < 32; ++k) t += part[k][threadIdx.x];
+        for (int k = 0; k < kColumnsBlock / 64; ++k) t += part[k][threadIdx.x];
         a.out[c] = t;
     }
 }
