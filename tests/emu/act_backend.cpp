@@ -4,7 +4,6 @@
 // Each access is checked against the size of the buffer it belongs to, and
 // each output byte may be written once; a violation sets an error that the
 // test reads.  The exchange's own launches are not part of this library.
-#include <immintrin.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -58,6 +57,28 @@ uint32_t f_bits(float f)
     return u;
 }
 
+float half_value(uint16_t u)
+{
+    const int e = u >> 10 & 31, m = u & 1023;
+    const double v = e == 31 ? (m ? NAN : INFINITY) : e ? ldexp(1024 + m, e - 25) : ldexp(m, -24);
+    return static_cast<float>(u & 0x8000 ? -v : v);
+}
+
+uint16_t half_of(float f)
+{
+    const uint16_t sign = signbit(f) ? 0x8000 : 0;
+    const double a = fabs(static_cast<double>(f));
+    if (f != f) return sign | 0x7e00;
+    if (a >= 65520.0) return sign | 0x7c00;
+    int e = -14;
+    if (a != 0) {
+        frexp(a, &e);
+        e = e - 1 < -14 ? -14 : e - 1;
+    }
+    const int n = static_cast<int>(nearbyint(ldexp(a, 10 - e)));   // steps of the value's size
+    return sign | static_cast<uint16_t>(((e + 14) << 10) + n);     // a carry moves on to the exponent
+}
+
 // one value of the type at element `at`
 float get(const Buf& b, int64_t at, int32_t type)
 {
@@ -74,13 +95,13 @@ float get(const Buf& b, int64_t at, int32_t type)
     uint16_t u;
     memcpy(&u, b.p + at * 2, 2);
     if (type == UA2A_TYPE_BF16) return bits_f(uint32_t(u) << 16);
-    return _cvtsh_ss(u);
+    return half_value(u);
 }
 
 float round_to(float f, int32_t type)
 {
     if (type == UA2A_TYPE_FP32) return f;
-    if (type == UA2A_TYPE_FP16) return _cvtsh_ss(_cvtss_sh(f, 0));
+    if (type == UA2A_TYPE_FP16) return half_value(half_of(f));
     if (f != f) return f;
     uint32_t u = f_bits(f);
     u += 0x7fffu + ((u >> 16) & 1);
@@ -99,7 +120,7 @@ void put(Buf& b, int64_t at, float f, int32_t type)
     if (type == UA2A_TYPE_BF16) {
         u = static_cast<uint16_t>(f_bits(round_to(f, type)) >> 16);
     } else {
-        u = _cvtss_sh(f, 0);
+        u = half_of(f);
     }
     memcpy(b.p + at * 2, &u, 2);
 }

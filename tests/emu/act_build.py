@@ -21,7 +21,7 @@ def build() -> str:
     if os.path.exists(LIBRARY) and all(os.path.getmtime(s) <= os.path.getmtime(LIBRARY) for s in SOURCES + HEADERS):
         return LIBRARY
     tmp = f"{LIBRARY}.tmp{os.getpid():x}"
-    subprocess.check_call(["g++", "-std=c++17", "-O2", "-g", "-mf16c", "-fPIC", "-shared", "-Wall", "-Wextra", "-Werror",
+    subprocess.check_call(["g++", "-std=c++17", "-O2", "-g", "-fPIC", "-shared", "-Wall", "-Wextra", "-Werror",
                            "-Wno-unused-parameter", "-Wno-unknown-pragmas", "-D__HIP_PLATFORM_AMD__",
                            "-I/opt/rocm/include", f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}", *SOURCES,
                            "-o", tmp])

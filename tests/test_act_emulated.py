@@ -86,7 +86,7 @@ def run_norm(lib, plan, x, weight, mode, residual=None, per_head=False, out_fmt=
 # are no multiple of a block or of 16 bytes, one token, long norms
 SHAPES = [(1, 1, 1, 1, 8), (2, 1, 5, 8, 128), (5, 1, 9, 5, 32), (1, 1, 7, 10, 128), (2, 1, 8, 4, 16), (3, 2, 5, 6, 40), (2, 1, 3, 4, 7), (5, 1, 4, 10, 2), (1, 2, 3, 5, 33),
           (4, 2, 7, 8, 80), (2, 1, 3, 6, 128), (2, 1, 2, 12, 128), (2, 1, 2, 32, 128), (8, 1, 3, 40, 128),
-          (1, 1, 2, 96, 128), (1, 1, 2, 256, 128), (2, 1, 1, 60, 7)]
+          (1, 1, 2, 96, 128), (1, 1, 2, 256, 128), (2, 1, 1, 60, 7), (2, 1, 3, 2, 640), (1, 2, 2, 3, 1000)]
 
 
 @pytest.mark.parametrize("t", ["bf16", "fp16", "fp32"])
@@ -211,6 +211,21 @@ def test_cache(lib, c, t):
                 ref.cache_read(want[part], codes, scales, fmt, starts.tolist(), counts.tolist() if k else [n] * seqs, part)
                 assert torch.equal(outs[part], want[part])
             assert lib.ua2a_act_emu_error() == 0
+
+
+def test_half_precision_of_the_emulation(lib):
+    """The stand-in's own half conversions, through a cache read: every code
+    and scale comes back as torch rounds it."""
+    codes = torch.arange(256, dtype=torch.uint8).repeat(2, 1).view(2, 1, 1, 8, 1, 32).contiguous()
+    for scale in (90, 101, 112, 120, 127, 134, 140):
+        scales = torch.full((2, 1, 1, 8, 1, 1), scale, dtype=torch.uint8)
+        out = torch.zeros(1, 1, 8, 1, 32, dtype=torch.float16)
+        with Plan(lib, 1, 1, 1, 1, 32, torch.float16) as plan:
+            cache = ua2a_cache_t(ptr(codes), ptr(scales), 1, 8, 1)
+            assert lib.ua2a_cache_read(plan.h, ctypes.byref(cache), 1, 8, None, None, ptr(out), None, None) == 0
+        want = torch.zeros_like(out)
+        ref.cache_read(want, codes, scales, E4M3, [0], [8], 0)
+        assert torch.equal(out.nan_to_num(7.0), want.nan_to_num(7.0)), scale
 
 
 # ------------------------------------------------------------------ refusals

@@ -26,6 +26,13 @@ def test_header_binding_and_library_agree():
     assert set(declared) <= exported
 
 
+def test_header_is_plain_c():
+    code = '#include "ua2a_act.h"\nint main(void) { ua2a_norm_t n; ua2a_cache_t c; (void)n; (void)c; return UA2A_BLOCK - 32; }\n'
+    cmd = ["gcc", "-std=c99", "-Wall", "-Wextra", "-pedantic", "-Werror", "-fsyntax-only", "-x", "c", "-I",
+           os.path.dirname(HEADER), "-"]
+    subprocess.run(cmd, input=code, text=True, check=True, timeout=60)
+
+
 @pytest.mark.parametrize("per_head", [False, True])
 @pytest.mark.parametrize("w,B,S,H,D", [(2, 1, 8, 4, 16), (8, 1, 9450, 40, 128), (3, 2, 4681, 12, 80)])
 def test_fake_shapes(w, B, S, H, D, per_head):

@@ -50,7 +50,7 @@ def cpu(t):
 SHAPES = [(1, 1, 1, 1, 8), (2, 1, 5, 8, 128), (5, 1, 9, 5, 32), (1, 1, 7, 10, 128), (2, 1, 8, 4, 16), (3, 2, 5, 6, 40), (2, 1, 3, 4, 7), (5, 1, 4, 10, 2), (1, 2, 3, 5, 33),
           (4, 2, 7, 8, 80), (2, 1, 3, 6, 128), (2, 1, 2, 12, 128), (2, 1, 2, 32, 128), (8, 1, 3, 40, 128),
           (1, 1, 2, 96, 128), (1, 1, 2, 256, 128), (2, 1, 1, 60, 7), (4, 1, 700, 8, 64), (3, 2, 211, 12, 80),
-          (1, 1, 1, 1, 8191)]
+          (1, 1, 1, 1, 8191), (2, 1, 3, 2, 640), (1, 2, 2, 3, 1000)]
 
 
 def check_norm(plan, mode, per_head, with_res, weight_type, out_fmt, save, seed=0, scale=3.0):
@@ -122,6 +122,7 @@ def test_long_norms():
         plan = ua.Plan(*shape, TYPES[t], device=DEV)
         check_norm(plan, 0, False, False, TYPES[t], None, E4M3)
         check_norm(plan, 1, False, True, TYPES[t], None, None, 1)
+        check_norm(plan, 0, True, True, torch.float32, E5M2, E4M3, 2)
         plan.close()
 
 
