@@ -152,6 +152,8 @@ def test_cache_object_and_refusals():
     cache = ua.Cache(2, 4, 40, 3, 7, device="cpu")
     assert cache.codes.shape == (2, 2, 3, 7, 2, 40) and cache.scales.shape == (2, 2, 3, 7, 2, 2)
     assert cache.codes.dtype == E4M3 and cache.scales.dtype == torch.float8_e8m0fnu
+    with pytest.raises(AttributeError):                 # its library struct holds their addresses
+        cache.codes = cache.codes.clone()
     for args in [(2, 3, 16, 1, 1), (0, 4, 16, 1, 1), (2, 4, 16, 0, 1), (2, 4, 16, 1, 0), (2, 4, 0, 1, 1)]:
         with pytest.raises(ValueError):
             ua.Cache(*args, device="cpu")

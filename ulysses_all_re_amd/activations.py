@@ -152,9 +152,17 @@ class Cache:
         cache._set(codes, scales)
         return cache
 
+    @property
+    def codes(self):
+        return self._codes
+
+    @property
+    def scales(self):
+        return self._scales
+
     def _set(self, codes, scales) -> None:
         import torch
-        self.codes, self.scales = codes, scales
+        self._codes, self._scales = codes, scales
         self.device, self.int32 = codes.device, torch.int32
         _, self.w, self.sequences, self.capacity, self.heads, self.D = codes.shape
         self.per_sequence = (self.sequences,)

@@ -101,7 +101,9 @@ uint32_t log2_of(uint32_t pow2)
 // needs with one, two or four slots per lane, up to kActBlock lanes (measured:
 // single precision, 288 slots, 82 us against 88 with 512 lanes; 640 slots 341
 // against 339, and 489 with 640 lanes); backward the fewest of one, two or four
-// waves with at most kActItems slots each.  Beyond them up to kActBigBlock lanes.
+// waves with at most kActItems slots each.  Beyond them up to kActBigBlock lanes
+// (backward with as few slots per lane as those allow: four would not fit the
+// registers of so many lanes).
 //
 // A norm per head of up to 64 slots (the next power of two): heads in
 // bundles, which leaves all sums within a wave.  A bundle's lanes are the most
@@ -140,7 +142,7 @@ int norm_geometry(const ua2a_plan_s* p, int32_t per_head, int32_t V, bool backwa
             n = static_cast<uint32_t>((slots + lanes - 1) / lanes);
             L->span = kSpanWaves;
         } else {
-            while (kActBlock * n < slots && n < 4) n *= 2;
+            while (!backward && kActBlock * n < slots && n < 4) n *= 2;
             while (kActBigBlock * n < slots) n *= 2;            // 1, 2, 4 or 8
             lanes = static_cast<uint32_t>((slots + n - 1) / n + 63) / 64 * 64;
             L->block = lanes;
