@@ -199,3 +199,29 @@ def test_special_values_in_8_bits(t, fmt):
     assert torch.equal(got.nan_to_num(123.0, 1.0, -1.0), want.nan_to_num(123.0, 1.0, -1.0))
     assert torch.equal(torch.isinf(got), torch.isinf(want))
     plan.close()
+
+
+@pytest.mark.parametrize("per_head", [False, True], ids=["token", "head"])
+@pytest.mark.parametrize("t,size,eps", [("fp16", 2.0 ** -18, 2.0 ** -38), ("bf16", 2.0 ** -64, 2.0 ** -126),
+                                        ("fp32", 2.0 ** -64, 2.0 ** -126)], ids=["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 33])
+def test_norms_of_the_smallest_values(t, size, eps, per_head, D):
+    """Values that are fp16's subnormals, or whose squares are fp32's, beside
+    an eps of their size.  A square's subnormal step is 2^-149, at most 2^-24
+    of mean + eps with its rounding, which the tolerance's 2^-18 holds."""
+    dtype = TYPES[t]
+    plan = ua.Plan(2, 1, 3, 4, D, dtype, device=DEV)
+    n = D if per_head else 4 * D
+    x, weight = values(plan.in_shape(0), dtype, 1, size), values((n,), dtype, 2)
+    y, h, rstd = ref.norm(x, weight, 0, 2, None, per_head, eps)
+    r = plan.norm_exchange(dev(x), dev(weight), 0, per_head=per_head, eps=eps, rstd=True)
+    torch.cuda.synchronize()
+    ref.check_values(cpu(r.rstd), rstd, torch.float32, t)
+    ref.check_values(cpu(r.out), y, dtype, t)
+    dy = values(plan.out_shape(0), dtype, 3, 2.0 ** -12)
+    b = plan.norm_exchange_backward(dev(dy), dev(weight), 0, dev(x), r.rstd, per_head=per_head)
+    torch.cuda.synchronize()
+    rs = cpu(r.rstd)
+    ref.check_backward(cpu(b.dx), None, cpu(b.dweight), ref.norm_backward(dy, weight, 0, 2, h, rs, None, per_head),
+                       ref.backward_terms(dy, weight, 0, 2, h, rs, None, per_head), dtype, 0, 2, t)
+    plan.close()
