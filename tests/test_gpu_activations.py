@@ -225,3 +225,31 @@ def test_norms_of_the_smallest_values(t, size, eps, per_head, D):
     ref.check_backward(cpu(b.dx), None, cpu(b.dweight), ref.norm_backward(dy, weight, 0, 2, h, rs, None, per_head),
                        ref.backward_terms(dy, weight, 0, 2, h, rs, None, per_head), dtype, 0, 2, t)
     plan.close()
+
+
+@pytest.mark.parametrize("save", [None, E4M3, E5M2], ids=["values", "e4m3", "e5m2"])
+@pytest.mark.parametrize("up", [50, -50])
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("mode,per_head", [(0, False), (1, True)], ids=["token", "head"])
+def test_backward_of_values_far_from_one(mode, per_head, t, up, save):
+    """Values of 2^50 with gradients of 2^90, and of 2^-50 with 2^-90: every
+    result lies well within 32 bits, the products h * dy do not."""
+    dtype = TYPES[t]
+    plan = ua.Plan(2, 1, 5, 4, 64, dtype, device=DEV)
+    eps = 2.0 ** -106
+    n = 64 if per_head else 4 * 64
+    x, weight = values(plan.in_shape(mode), dtype, 1, 2.0 ** up), values((n,), dtype, 2)
+    dy = values(plan.out_shape(mode), dtype, 3, 2.0 ** (90 if up > 0 else -90))
+    _, h, _ = ref.norm(x, weight, mode, 2, None, per_head, eps)
+    r = plan.norm_exchange(dev(x), dev(weight), mode, per_head=per_head, eps=eps, rstd=True, checkpoint=save)
+    b = plan.norm_exchange_backward(dev(dy), dev(weight), mode, r.saved if save else dev(x), r.rstd,
+                                    saved_scales=r.saved_scales if save else None, per_head=per_head)
+    torch.cuda.synchronize()
+    rs = cpu(r.rstd)
+    if save:
+        h = ref.dequantise(cpu(r.saved), cpu(r.saved_scales), save)
+    want = ref.norm_backward(dy, weight, mode, 2, h, rs, None, per_head)
+    assert all(bool(torch.isfinite(v).all()) for v in want)
+    ref.check_backward(cpu(b.dx), None, cpu(b.dweight), want, ref.backward_terms(dy, weight, mode, 2, h, rs, None, per_head),
+                       dtype, mode, 2, t)
+    plan.close()

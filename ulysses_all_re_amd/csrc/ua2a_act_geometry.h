@@ -1,5 +1,5 @@
 // Index math of the activation operators: norms joined with the exchange and
-// the 8-bit cache.  Shared by the kernels (ua2a_act_kernels.hip), the host
+// the 8-bit cache.  Shared by the kernels (ua2a_act_*.hip), the host
 // code that fills it (ua2a_act_host.cpp) and a CPU check that walks every lane.
 //
 // Two layouts of one tensor (see ua2a.h): P [w][B][S][H][D] and

@@ -1,5 +1,5 @@
 // Internal declarations shared by the activation operators' host code
-// (ua2a_act_host.cpp) and kernels (ua2a_act_kernels.hip).
+// (ua2a_act_host.cpp) and kernels (ua2a_act_*.hip).
 #pragma once
 
 #include "ua2a_act.h"

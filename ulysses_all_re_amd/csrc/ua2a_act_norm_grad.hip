@@ -12,9 +12,9 @@ namespace {
 // dweight for their lanes' slots in registers, so the order of the sums is
 // fixed; at the end each workgroup writes one row of partial sums.  Those
 // registers leave two waves per SIMD, so the next segment's loads are issued
-// before one is worked on.  Measured: video-DiT from an e4m3 checkpoint 364 us
-// (5.35 TB/s; without the early loads 374 on a box where this form took 347),
-// from the values 395 us (5.9 TB/s).
+// before one is worked on.  Measured: video-DiT from an e4m3 checkpoint 367 us
+// (5.3 TB/s; without the early loads 374 on a box where this form took 347),
+// from the values 394 us (5.9 TB/s).
 template <class T, class W, bool SAVED8, int V, Span SPAN, int ITEMS, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a)
 {
@@ -108,10 +108,13 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a)
             const float rstd = x.rstd[one_norm(SPAN) ? 0 : it];
             const float r = SAVED8 ? rstd * scale_of(hs[it]) : rstd;
             float* const sums = dw[one_norm(SPAN) ? it : 0];
+            // n * dy with n near 1: h * dy may leave 32 bits where no result does
+            // (one operation more per value, 0.5 % of the time)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
+                n[i] *= r;
+                sums[i] += n[i] * d[i];
                 n[i] *= d[i];
-                sums[i] += n[i] * r;
             }
             if (flags & kNormWeight) {
                 float wf[V];
@@ -122,7 +125,7 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a)
 #pragma unroll
                 for (int i = 0; i < V; ++i) p += n[i];
             }
-            mean[it] = p * r;
+            mean[it] = p;
         }
         norm_sums<SPAN, ITEMS>(g, mean, red, round);
 #pragma unroll
