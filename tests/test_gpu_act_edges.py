@@ -1,0 +1,91 @@
+"""GPU: activation calls at the edges of what they take -- rows of NaN beside
+others, scale bytes that are NaN, weights at any address, many sequences."""
+from __future__ import annotations
+
+import sys
+
+import pytest
+import torch
+
+import ulysses_all_re_amd as ua
+from tests import act_reference as ref
+from tests.test_gpu_activations import E4M3, E5M2, TYPES, cpu, dev, values
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+def note(msg):
+    print(f"[gpu-case] {msg}", flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ua.load_library()
+    torch.cuda.set_device(0)
+    yield
+    torch.cuda.synchronize()
+
+
+# heads of 40: eight lanes of which three are padding; of 24 in fp32: eight, two of
+# them padding; of 33: single values; heads that share a bundle, or a wave
+@pytest.mark.parametrize("save", [None, E4M3, E5M2], ids=["values", "e4m3", "e5m2"])
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("t,H,D", [("bf16", 16, 40), ("fp16", 10, 40), ("fp32", 16, 24), ("fp32", 6, 40),
+                                   ("bf16", 8, 33), ("bf16", 3, 72)])
+def test_a_head_of_nan_leaves_the_others_alone(t, H, D, mode, save):
+    """Norms per head with NaN in the first head of a token: that head's
+    gradients are NaN, every other head's are those of the definition."""
+    dtype, w = TYPES[t], 1
+    note(f"nan head {t} {H}x{D} mode {mode} {save}")
+    plan = ua.Plan(w, 1, 5, H, D, dtype, device=DEV)
+    x, weight = values(plan.in_shape(mode), dtype, 1), values((D,), dtype, 2)
+    x[0, 0, 2, 0, 1] = float("nan")                             # w = 1: P and A are the same
+    dy = values(plan.out_shape(mode), dtype, 3)
+    r = plan.norm_exchange(dev(x), dev(weight), mode, per_head=True, checkpoint=save, rstd=True)
+    b = plan.norm_exchange_backward(dev(dy), dev(weight), mode, r.saved if save else dev(x), r.rstd,
+                                    saved_scales=r.saved_scales, per_head=True)
+    torch.cuda.synchronize()
+    y, h, _ = ref.norm(x, weight, mode, w, None, True)
+    ref.check_values(cpu(r.out), y, dtype, "out")
+    rs = cpu(r.rstd)
+    assert int(torch.isnan(rs).sum()) == 1
+    if save:
+        h = ref.dequantise(cpu(r.saved), cpu(r.saved_scales), save)
+    want = ref.norm_backward(dy, weight, mode, w, h, rs, None, True)
+    parts = ref.backward_terms(dy, weight, mode, w, h, rs, None, True)
+    assert int(torch.isnan(want[0]).sum()) == D
+    ref.check_backward(cpu(b.dx), None, None, want, parts, dtype, mode, w, "nan head")
+    assert bool(torch.isnan(cpu(b.dweight)).all())
+    plan.close()
+
+
+@pytest.mark.parametrize("save", [None, E4M3], ids=["values", "e4m3"])
+@pytest.mark.parametrize("per_head", [False, True], ids=["token", "head"])
+@pytest.mark.parametrize("t,H,D", [("bf16", 8, 40), ("fp32", 6, 24), ("fp16", 3, 33), ("bf16", 24, 40)])
+def test_an_infinite_weight_meets_values_only(t, H, D, per_head, save):
+    """The first weight is infinite: gradients are the definition's infinities,
+    which lanes of padding (they hold that weight too) do not turn into NaN."""
+    dtype, w = TYPES[t], 1
+    note(f"infinite weight {t} {H}x{D} head {per_head} {save}")
+    plan = ua.Plan(w, 1, 5, H, D, dtype, device=DEV)
+    x, weight = values(plan.in_shape(0), dtype, 1), values((D if per_head else H * D,), dtype, 2)
+    weight[0] = float("inf")
+    dy = values(plan.out_shape(0), dtype, 3)
+    r = plan.norm_exchange(dev(x), dev(weight), 0, per_head=per_head, checkpoint=save, rstd=True)
+    b = plan.norm_exchange_backward(dev(dy), dev(weight), 0, r.saved if save else dev(x), r.rstd,
+                                    saved_scales=r.saved_scales, per_head=per_head)
+    torch.cuda.synchronize()
+    _, h, _ = ref.norm(x, weight, 0, w, None, per_head)
+    if save:
+        h = ref.dequantise(cpu(r.saved), cpu(r.saved_scales), save)
+    rs = cpu(r.rstd)
+    want = ref.norm_backward(dy, weight, 0, w, h, rs, None, per_head)
+    parts = ref.backward_terms(dy, weight, 0, w, h, rs, None, per_head)
+    assert bool(torch.isinf(want[0]).any())
+    ref.check_backward(cpu(b.dx), None, cpu(b.dweight), want, parts, dtype, 0, w, "infinite weight")
+    plan.close()

@@ -127,6 +127,16 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a)
             }
             mean[it] = p;
         }
+        // A lane of padding looks at another slot's rstd, scale and weight: a NaN or
+        // an infinity among them passes the product with its zeros, so its part of
+        // the norm's sum is zero by itself.  (Its sums of dweight are not used; a
+        // lane past the last segment looks at the same slot of the first, whose own
+        // lane adds such a NaN to dweight anyway.)
+        if (masked) {
+#pragma unroll
+            for (int it = 0; it < ITEMS; ++it)
+                if (!at.ok(it)) mean[it] = 0.f;
+        }
         norm_sums<SPAN, ITEMS>(g, mean, red, round);
 #pragma unroll
         for (int it = 0; it < ITEMS; ++it) {
