@@ -15,7 +15,7 @@
  * 8 bits with scales.  A tensor [..., D] is held as codes [..., D], one byte
  * per value, and scales [..., ceil(D/32)], one byte per block of 32 values
  * along D (the last block of a head may be shorter).  A scale byte s stands
- * for 2^(s - 127) (e8m0); a code is e4m3 (largest value 448) or e5m2
+ * for 2^(s - 127), 255 for NaN (e8m0); a code is e4m3 (largest value 448) or e5m2
  * (57344).  Of a block with largest finite magnitude m, the scale is the
  * least power of two, 2^-127 at least, with m <= scale * (largest code): no
  * finite value overflows, and a value's error is at most half a step of its

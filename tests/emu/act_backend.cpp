@@ -184,6 +184,9 @@ uint8_t code_of(double x, int32_t f)
     return sign | static_cast<uint8_t>(((e + q.bias) << q.mantissa) + (static_cast<int>(n) - (1 << q.mantissa)));
 }
 
+// what a scale byte stands for
+double scale_value(uint8_t s) { return s == 255 ? NAN : ldexp(1.0, s - 127); }
+
 // scale exponent of a block's values, by search
 int scale_exponent(const std::vector<float>& v, int32_t f)
 {
@@ -305,7 +308,7 @@ void norm_grad(const ActLaunch& L)
         double h;
         if (a.saved_format)
             h = code_value(get8(saved, value_at(g, s, sl, false) + i), a.saved_format) *
-                ldexp(1.0, get8(ssc, scale_at(g, s, sl, false)) - 127);
+                scale_value(get8(ssc, scale_at(g, s, sl, false)));
         else
             h = get(saved, value_at(g, s, sl, (a.flags & kNormGathered) != 0) + i, L.type);
         const float wt = w.p ? get(w, weight_at(g, sl) + i, a.weight_f32 ? UA2A_TYPE_FP32 : L.type) : 1.f;
@@ -419,8 +422,8 @@ void cache_read(const ActLaunch& L)
                                                   h * g.sh.nb + d / kBlockValues)
                         flag(1);
                     double f = code_value(get8(codes, (y ? g.part : 0) + row * g.sh.run + at + k), a.format) *
-                               ldexp(1.0, get8(scales, (y ? g.part_scales : 0) + row * g.sh.hl * g.sh.nb + h * g.sh.nb +
-                                                           d / kBlockValues) - 127);
+                               scale_value(get8(scales, (y ? g.part_scales : 0) + row * g.sh.hl * g.sh.nb + h * g.sh.nb +
+                                                            d / kBlockValues));
                     const double most = L.type == UA2A_TYPE_FP16 ? 65504.0
                                         : bits_f(L.type == UA2A_TYPE_FP32 ? 0x7f7fffffu : 0x7f7f0000u);
                     if (isfinite(f) && fabs(f) > most) f = f < 0 ? -most : most;

@@ -89,3 +89,58 @@ def test_an_infinite_weight_meets_values_only(t, H, D, per_head, save):
     assert bool(torch.isinf(want[0]).any())
     ref.check_backward(cpu(b.dx), None, cpu(b.dweight), want, parts, dtype, 0, w, "infinite weight")
     plan.close()
+
+
+@pytest.mark.parametrize("fmt", [E4M3, E5M2], ids=["e4m3", "e5m2"])
+@pytest.mark.parametrize("t", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("D", [96, 40, 33])
+def test_a_scale_of_nan_reads_back_as_nan(t, fmt, D):
+    """The scale byte 255 is NaN: its block reads back as NaN, codes of zero and
+    infinities among it, and every other block as before."""
+    dtype = TYPES[t]
+    note(f"nan scale read {t} {fmt} {D}")
+    nb = -(-D // 32)
+    plan = ua.Plan(2, 1, 1, 4, D, dtype, device=DEV)
+    g = torch.Generator().manual_seed(5)
+    codes = torch.randint(0, 256, (2, 2, 3, 7, 2, D), generator=g, dtype=torch.uint8)
+    codes[..., 0] = 0
+    scales = torch.randint(100, 130, (2, 2, 3, 7, 2, nb), generator=g, dtype=torch.uint8)
+    hit = torch.rand(scales.shape, generator=g) < 0.2
+    scales[hit] = 255
+    cache = ua.Cache.of(dev(codes).view(fmt), dev(scales).view(torch.float8_e8m0fnu))
+    got = plan.cache_read(cache, 7)
+    torch.cuda.synchronize()
+    want = [torch.zeros(2, 3, 7, 2, D, dtype=dtype) for _ in range(2)]
+    plain = torch.where(hit, torch.full_like(scales, 127), scales)
+    for part in (0, 1):
+        ref.cache_read(want[part], codes, plain, fmt, [0] * 3, [7] * 3, part)
+        want[part][hit[part].repeat_interleave(32, -1)[..., :D]] = float("nan")
+        k = cpu(got[part])
+        assert torch.equal(torch.isnan(k), torch.isnan(want[part]))
+        assert torch.equal(k.nan_to_num(1.0, 2.0, 3.0), want[part].nan_to_num(1.0, 2.0, 3.0))
+    plan.close()
+
+
+@pytest.mark.parametrize("per_head", [False, True], ids=["token", "head"])
+@pytest.mark.parametrize("t,H,D", [("bf16", 8, 64), ("fp16", 6, 40), ("fp32", 4, 72), ("bf16", 3, 33), ("bf16", 40, 128)])
+def test_a_scale_of_nan_in_a_checkpoint(t, H, D, per_head):
+    """A checkpoint with the scale byte 255: its norm's gradients are NaN, all others as before."""
+    dtype, w = TYPES[t], 1
+    note(f"nan scale backward {t} {H}x{D} head {per_head}")
+    plan = ua.Plan(w, 1, 5, H, D, dtype, device=DEV)
+    x, weight = values(plan.in_shape(0), dtype, 1), values((D if per_head else H * D,), dtype, 2)
+    dy = values(plan.out_shape(0), dtype, 3)
+    r = plan.norm_exchange(dev(x), dev(weight), 0, per_head=per_head, checkpoint=E4M3)
+    codes, scales = cpu(r.saved), cpu(r.saved_scales)
+    h = ref.dequantise(codes, scales, E4M3)
+    scales[0, 0, 2, 0, 0] = 255
+    h[0, 0, 2, 0, :32] = float("nan")
+    b = plan.norm_exchange_backward(dev(dy), dev(weight), 0, r.saved, r.rstd, per_head=per_head,
+                                    saved_scales=dev(scales).view(torch.float8_e8m0fnu))
+    torch.cuda.synchronize()
+    rs = cpu(r.rstd)
+    want = ref.norm_backward(dy, weight, 0, w, h, rs, None, per_head)
+    parts = ref.backward_terms(dy, weight, 0, w, h, rs, None, per_head)
+    assert int(torch.isnan(want[0]).sum()) == (D if per_head else H * D)
+    ref.check_backward(cpu(b.dx), None, cpu(b.dweight), want, parts, dtype, 0, w, "nan scale")
+    plan.close()

@@ -203,6 +203,12 @@ __device__ __forceinline__ float scale_of(uint32_t byte)
 {
     return __uint_as_float(byte ? byte << 23 : 0x400000u);
 }
+// The same of a byte that was read: 255 is NaN.  One bit below the exponent
+// makes both of its ends what they stand for.
+__device__ __forceinline__ float read_scale_of(uint32_t byte)
+{
+    return __uint_as_float(byte << 23 | (((byte + 1) & 0xfe) == 0 ? 0x400000u : 0u));
+}
 
 // The codes of V values at a scale, by gfx950's scaled conversions: each
 // divides by the power of two exactly and rounds once to nearest even
@@ -358,7 +364,7 @@ template <class T, int V>
 __device__ __forceinline__ typename Raw<T, V>::type decode_raw(typename Codes<V>::type c, uint32_t byte, int32_t format)
 {
     constexpr bool kHalf = __is_same(T, _Float16);
-    const float s = scale_of(byte);
+    const float s = read_scale_of(byte);
     const uint32_t high = 127u + (kHalf ? 15u : 127u) - (format == UA2A_FORMAT_E4M3 ? 8u : 15u) + 1u;
     float f[V];
     if (__builtin_amdgcn_ballot_w64(byte >= high) == 0) {

@@ -106,7 +106,7 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a)
             unpack<T, V>(dy[it], d);
             normed(it, n);
             const float rstd = x.rstd[one_norm(SPAN) ? 0 : it];
-            const float r = SAVED8 ? rstd * scale_of(hs[it]) : rstd;
+            const float r = SAVED8 ? rstd * read_scale_of(hs[it]) : rstd;
             float* const sums = dw[one_norm(SPAN) ? it : 0];
             // n * dy with n near 1: h * dy may leave 32 bits where no result does
             // (one operation more per value, 0.5 % of the time)
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a)
             // the powers of two leave the factor's rounding alone
             const float rstd = x.rstd[one_norm(SPAN) ? 0 : it];
             const float m = rstd * (mean[it] * a.inv_len);
-            const float r = SAVED8 ? m * scale_of(hs[it]) : m;
+            const float r = SAVED8 ? m * read_scale_of(hs[it]) : m;
 #pragma unroll
             for (int i = 0; i < V; ++i) d[i] = rstd * (d[i] - n[i] * r);
             if (flags & kNormResidual) {
