@@ -136,6 +136,12 @@ class Cache:
     @classmethod
     def of(cls, codes, scales) -> "Cache":
         """A cache over the caller's tensors (contiguous, shaped as above)."""
+        cache = cls.__new__(cls)
+        cache._set(codes, scales)
+        return cache
+
+    @staticmethod
+    def _check(codes, scales) -> None:
         import torch
         _format_of(codes.dtype, "a cache's codes")
         if scales.dtype not in (torch.float8_e8m0fnu, torch.uint8):
@@ -148,9 +154,9 @@ class Cache:
             raise ValueError(f"scales are on {scales.device}, codes are on {codes.device}")
         if not (codes.is_contiguous() and scales.is_contiguous()):
             raise ValueError("codes and scales must be contiguous")
-        cache = cls.__new__(cls)
-        cache._set(codes, scales)
-        return cache
+        for t, what in ((codes, "codes"), (scales, "scales")):
+            if t.untyped_storage().nbytes() < t.storage_offset() + t.numel():
+                raise ValueError(f"{what} have lost their memory")
 
     @property
     def codes(self):
@@ -162,13 +168,15 @@ class Cache:
 
     def _set(self, codes, scales) -> None:
         import torch
+        self._check(codes, scales)
         self._codes, self._scales = codes, scales
         self.device, self.int32 = codes.device, torch.int32
         _, self.w, self.sequences, self.capacity, self.heads, self.D = codes.shape
         self.per_sequence = (self.sequences,)
-        self._struct = ua2a_cache_t(codes.data_ptr(), scales.data_ptr(), self.sequences, self.capacity,
-                                    _format_of(codes.dtype, "codes"))
-        self._ref = ctypes.byref(self._struct)
+        self.heads_of = (self.w, self.heads * self.w, self.D)
+        self._codes_at, self._scales_at = codes.data_ptr(), scales.data_ptr()
+        self._ref = ctypes.byref(ua2a_cache_t(self._codes_at, self._scales_at, self.sequences, self.capacity,
+                                              _format_of(codes.dtype, "codes")))
 
 
 class ActivationCalls:
@@ -368,7 +376,10 @@ class ActivationCalls:
         return NormGradients(dx, dres if apart else dx if residual else None, dw)
 
     def _check_cache(self, cache: Cache, starts, counts) -> None:
-        if (cache.w, cache.heads * cache.w, cache.D) != (self.w, self.H, self.D):
+        codes, scales = cache._codes, cache._scales
+        if codes.data_ptr() != cache._codes_at or scales.data_ptr() != cache._scales_at:
+            cache._set(codes, scales)                          # a tensor has been given other memory
+        if cache.heads_of != (self.w, self.H, self.D):
             raise ValueError(f"cache has w = {cache.w}, {cache.heads} heads of {cache.D} per rank; "
                              f"the plan w = {self.w}, {self.H // self.w} of {self.D}")
         if cache.device != self.device:
