@@ -18,6 +18,7 @@ namespace {
 
 int g_error = 0;              // first violation: 1 read, 2 write, 3 written twice
 int g_launches = 0;
+int g_dry = 0;                // launches are recorded only
 ActLaunch g_last;
 
 void flag(int e)
@@ -361,8 +362,8 @@ void cache_write(const ActLaunch& L)
         Buf val(y ? a.v : a.k, nval * e);
         if (!val.p) continue;
         std::vector<uint8_t> seen(static_cast<size_t>(g.rows) * g.slots, 0);
-        for (uint32_t wg = 0; wg < L.grid_x; ++wg) {
-            const uint32_t group = cache_group(g, wg);
+        for (uint32_t wg = 0; wg < L.grid_x * L.grid_y; ++wg) {
+            const uint32_t group = cache_group(g, cache_workgroup(wg % L.grid_x, wg / L.grid_x));
             if (group >= g.groups) continue;
             for (uint32_t tid = 0; tid < L.block; ++tid) {
                 const WriteLane l = write_lane(g, group, tid / g.lanes, tid);
@@ -442,6 +443,7 @@ int act_launch(const ActLaunch& L, void*)
 {
     ++g_launches;
     g_last = L;
+    if (g_dry) return 0;
     switch (L.kernel) {
     case ActKernel::Norm: norm(L); break;
     case ActKernel::NormGrad: norm_grad(L); break;
@@ -471,7 +473,8 @@ void ua2a_act_emu_reset()
     g_error = 0;
     g_launches = 0;
 }
-int ua2a_act_emu_last(int what)   // 0 V, 1 items, 2 block, 3 grid, 4 lanes
+void ua2a_act_emu_dry(int on) { g_dry = on; }
+int ua2a_act_emu_last(int what)   // 0 V, 1 items, 2 block, 3 grid, 4 lanes, 5 grid along y
 {
     const NormGeom& g = g_last.kernel == ActKernel::NormGrad ? g_last.grad.g : g_last.norm.g;
     switch (what) {
@@ -479,6 +482,7 @@ int ua2a_act_emu_last(int what)   // 0 V, 1 items, 2 block, 3 grid, 4 lanes
     case 1: return g_last.items;
     case 2: return static_cast<int>(g_last.block);
     case 3: return static_cast<int>(g_last.grid_x);
+    case 5: return static_cast<int>(g_last.grid_y);
     default: return static_cast<int>(g.lanes);
     }
 }

@@ -1,11 +1,15 @@
 """Activation calls at the edges of what they take: the host side, without a GPU."""
 from __future__ import annotations
 
+import ctypes
+
 import pytest
 import torch
 
 import ulysses_all_re_amd as ua
+from tests.emu import act_build
 from tests.test_binding_cpu import _host_plan
+from ulysses_all_re_amd.activations import ua2a_cache_t
 
 
 class Calls:
@@ -52,3 +56,54 @@ def test_a_cache_follows_its_tensors():
         plan.cache_write(cache, k, k, starts)
     assert len(calls.seen) == done + 1
     plan.close()
+
+
+@pytest.fixture(scope="module")
+def lib():
+    so = ctypes.CDLL(act_build.build())
+    i32, i64, vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+    so.ua2a_plan.argtypes = [ctypes.POINTER(vp), i32, i64, i64, i64, i64, i32, i32, vp, i64, i32]
+    so.ua2a_destroy.argtypes = [vp]
+    return ua.declare_activation_signatures(so)
+
+
+@pytest.fixture
+def dry(lib):
+    """Launches are recorded and not carried out: any size, any address."""
+    lib.ua2a_act_emu_reset()
+    lib.ua2a_act_emu_dry(1)
+    yield lib
+    lib.ua2a_act_emu_dry(0)
+
+
+def make_plan(lib, w, B, S, H, D, e=2):
+    h = ctypes.c_void_p()
+    assert lib.ua2a_plan(ctypes.byref(h), w, B, S, H, D, e, 0, None, 0, 0) == 0
+    return h
+
+
+def grid(lib):
+    """Workgroups along x and y of the last launch, and lanes of one."""
+    x, y, lanes = (lib.ua2a_act_emu_last(k) for k in (3, 5, 2))
+    assert x * lanes <= 2 ** 31 and y <= 65535
+    return x, y, lanes
+
+
+@pytest.mark.parametrize("H,D,pieces,chunks", [
+    (40, 128, 640, 3),             # 640 vectors of 16 bytes on three workgroups of 256 lanes
+    (16, 128, 256, 1),
+    (257, 32, 1028, 5),
+    (9, 1, 288, 2),                # single values, a block of 32 for each head
+])
+def test_cache_writes_up_to_the_stated_size(dry, H, D, pieces, chunks):
+    """2^31 - 1 pieces at most, however many lanes the tokens' padding adds."""
+    most = (2 ** 31 - 1) // pieces
+    for tokens in (most, most + 1, 2 ** 23 // chunks - 600, 2 ** 23 // chunks + 600):
+        code = 0 if tokens <= most else ua.UA2A_ERR_SHAPE
+        plan = make_plan(dry, 1, tokens, 1, H, D)
+        cache = ua2a_cache_t(1 << 44, 1 << 46, 1, 1, 1)
+        assert dry.ua2a_cache_write(plan, ctypes.byref(cache), 0, 1 << 40, None, 1 << 47, None, None) == code, tokens
+        if code == 0:
+            x, y, _ = grid(dry)
+            assert x * y >= tokens * chunks and (y > 1) == (tokens * chunks > 2 ** 23)
+        dry.ua2a_destroy(plan)

@@ -144,3 +144,21 @@ def test_a_scale_of_nan_in_a_checkpoint(t, H, D, per_head):
     assert int(torch.isnan(want[0]).sum()) == (D if per_head else H * D)
     ref.check_backward(cpu(b.dx), None, cpu(b.dweight), want, parts, dtype, 0, w, "nan scale")
     plan.close()
+
+
+def test_a_write_of_more_workgroups_than_fit_along_x():
+    """4.3 million tokens of nine heads of one value: two workgroups a token."""
+    w, H, D, S = 1, 9, 1, 4_300_000
+    note("cache write, 8.6 million workgroups")
+    plan = ua.Plan(w, 1, S, H, D, torch.bfloat16, device=DEV)
+    k = values(plan.in_shape(0), torch.bfloat16, 1)
+    cache = ua.Cache(w, H, D, 1, S + 3, E4M3, DEV)
+    starts = torch.tensor([2], dtype=torch.int32)
+    plan.cache_write(cache, dev(k), None, dev(starts))
+    torch.cuda.synchronize()
+    q, s = ref.quantise(k, E4M3)
+    codes, scales = cpu(cache.codes), cpu(cache.scales)
+    assert torch.equal(codes[0, 0, 0, 2:S + 2], q[0, 0]) and torch.equal(scales[0, 0, 0, 2:S + 2], s[0, 0])
+    for t in (codes, scales):
+        assert not bool(t[1].any()) and not bool(t[0, 0, 0, :2].any()) and not bool(t[0, 0, 0, S + 2:].any())
+    plan.close()

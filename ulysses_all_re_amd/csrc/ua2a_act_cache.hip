@@ -19,7 +19,7 @@ template <class T, int V, bool UNIFORM>
 __global__ __launch_bounds__(kActBlock) void ua2a_cache_write_kernel(CacheArgs a)
 {
     const CacheGeom& g = a.g;
-    const uint32_t group = cache_group(g, blockIdx.x);
+    const uint32_t group = cache_group(g, cache_workgroup(blockIdx.x, blockIdx.y));
     if (group >= g.groups) return;
     uint32_t tid = threadIdx.x;
     if constexpr (UNIFORM) tid = __builtin_amdgcn_readfirstlane(tid);

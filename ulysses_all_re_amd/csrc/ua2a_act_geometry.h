@@ -176,6 +176,11 @@ struct CacheGeom {
 
 constexpr uint32_t kCacheXcds = 8;
 
+// A cache launch's workgroups: up to 2^kCacheGridLog along x (2^31 lanes of
+// workgroups of 256), the rest along y.
+constexpr uint32_t kCacheGridLog = 23;
+UA2A_HD uint32_t cache_workgroup(uint32_t x, uint32_t y) { return (y << kCacheGridLog) + x; }
+
 // The group of tokens of a write's workgroup: workgroups go to the XCDs in
 // turn, and 2^run_log consecutive groups to one of them.
 UA2A_HD uint32_t cache_group(const CacheGeom& g, uint32_t id)

@@ -13,7 +13,8 @@ using namespace ua2a;
 namespace {
 
 constexpr int64_t kMaxSegments = int64_t(1) << 31;
-constexpr int64_t kMaxSlots = int64_t(kMaxGridWorkItems) - kActBlock;    // lane slots of a cache call
+constexpr int64_t kMaxSlots = int64_t(kMaxGridWorkItems) - kActBlock;    // lanes of a cache read
+constexpr int64_t kMaxPieces = (int64_t(1) << 31) - 1;                   // vectors of a cache call's tensor
 constexpr int64_t kMaxCacheValues = int64_t(1) << 38;
 
 struct Range {
@@ -220,6 +221,15 @@ void cache_geometry(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t V, int64_t 
     g->d_seqs = make_div32(g->seqs);
 }
 
+// `wgs` workgroups, within what a dispatch counts along x (cache_workgroup takes
+// the two parts together again).
+void cache_grid(int64_t wgs, ActLaunch* L)
+{
+    const int64_t along = int64_t(1) << kCacheGridLog;
+    L->grid_x = static_cast<uint32_t>(wgs < along ? wgs : along);
+    L->grid_y = static_cast<uint32_t>((wgs + along - 1) >> kCacheGridLog);
+}
+
 }  // namespace
 
 extern "C" {
@@ -417,7 +427,7 @@ int ua2a_cache_write(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t type, cons
     cache_geometry(plan, c, L.V, gathered / c->sequences, &a.g);
     CacheGeom& g = a.g;
     const int64_t row = plan->H * g.sh.nb * (kBlockValues / L.V);
-    if (row > kMaxSlots / gathered) return UA2A_ERR_SHAPE;
+    if (row > kMaxPieces / gathered) return UA2A_ERR_SHAPE;
     g.rows = static_cast<uint32_t>(gathered);
     g.slots = static_cast<uint32_t>(row);
     g.lanes = 1;
@@ -430,8 +440,7 @@ int ua2a_cache_write(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t type, cons
     g.run_log = 0;
     while (g.run_log < 6 && (int64_t(g.sh.hl) * g.sh.nb << (g.run_log + g.per_log)) < kLineBytes * g.chunks) ++g.run_log;
     const int64_t turn = int64_t(kCacheXcds) << g.run_log;
-    const int64_t wgs = (groups + turn - 1) / turn * turn;
-    if (wgs > kMaxSlots / kActBlock) return UA2A_ERR_SHAPE;
+    const int64_t wgs = (groups + turn - 1) / turn * turn;     // below 2^25: the lanes are less than twice the pieces
     g.groups = static_cast<uint32_t>(groups);
     const int64_t bytes = plan->layout.tensor_bytes;
     const Range ins[] = {{k, bytes}, {v, bytes}, {starts, c->sequences * 4}, {counts, c->sequences * 4}};
@@ -447,8 +456,7 @@ int ua2a_cache_write(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t type, cons
     a.counts = counts;
     a.format = c->format;
     L.block = kActBlock;
-    L.grid_x = static_cast<uint32_t>(wgs);
-    L.grid_y = 1;
+    cache_grid(wgs, &L);
     const int err = act_launch(L, stream);
     return err == 0 ? UA2A_OK : fail(plan, "launching the cache write", err);
 }
