@@ -406,9 +406,11 @@ void cache_read(const ActLaunch& L)
     for (uint32_t y = 0; y < 2; ++y) {
         Buf val(y ? a.v_out : a.k_out, g.spans * span * e);
         if (!val.p) continue;
-        for (uint32_t wg = 0; wg < L.grid_x; ++wg) {
+        for (uint32_t id = 0; id < L.grid_x * L.grid_y; ++id) {
+            const uint32_t wg = cache_workgroup(id % L.grid_x, id / L.grid_x);
             const uint32_t ri = fdiv(wg, g.d_tiles), tile = wg - ri * g.tiles, r = fdiv(ri, g.d_seqs), i = ri - r * g.seqs;
-            if (i >= g.seqs || ri >= g.spans) {
+            if (ri >= g.spans) continue;
+            if (i >= g.seqs) {
                 flag(1);
                 continue;
             }

@@ -107,3 +107,24 @@ def test_cache_writes_up_to_the_stated_size(dry, H, D, pieces, chunks):
             x, y, _ = grid(dry)
             assert x * y >= tokens * chunks and (y > 1) == (tokens * chunks > 2 ** 23)
         dry.ua2a_destroy(plan)
+
+
+@pytest.mark.parametrize("w,H,D,n,vectors,lanes", [
+    (1, 1, 8, 1, 1, 64),           # one vector of 16 bytes a sequence, on a wave
+    (2, 2, 8, 65, 65, 128),
+    (1, 1, 8, 257, 257, 256),
+    (1, 3, 1, 1, 3, 64),           # single values
+])
+def test_cache_reads_up_to_the_stated_size(dry, w, H, D, n, vectors, lanes):
+    """2^31 - 1 pieces at most, however short the sequences."""
+    most = (2 ** 31 - 1) // (vectors * w)
+    turn = 2 ** 23 // (-(-vectors // lanes) * w)                # sequences that fill x
+    for seqs in (most, most + 1, turn, turn + 1):
+        code = 0 if seqs <= most else ua.UA2A_ERR_SHAPE
+        plan = make_plan(dry, w, 1, 1, H, D)
+        cache = ua2a_cache_t(1 << 44, 1 << 46, seqs, 1, 1)
+        assert dry.ua2a_cache_read(plan, ctypes.byref(cache), 0, n, None, None, 1 << 40, None, None) == code, seqs
+        if code == 0:
+            x, y, block = grid(dry)
+            assert block == lanes and x * y >= seqs * w * -(-vectors // lanes) and (y > 1) == (seqs > turn)
+        dry.ua2a_destroy(plan)

@@ -162,3 +162,18 @@ def test_a_write_of_more_workgroups_than_fit_along_x():
     for t in (codes, scales):
         assert not bool(t[1].any()) and not bool(t[0, 0, 0, :2].any()) and not bool(t[0, 0, 0, S + 2:].any())
     plan.close()
+
+
+def test_a_read_of_more_workgroups_than_fit_along_x():
+    """The first position of 33.6 million sequences, a vector each."""
+    seqs = 2 ** 25 + 5
+    note("cache read, 33.6 million workgroups")
+    plan = ua.Plan(1, 1, 1, 1, 8, torch.bfloat16, device=DEV)
+    codes = torch.arange(2 * seqs * 8, device=DEV).remainder_(251).remainder_(120).to(torch.uint8)
+    codes = codes.view(2, 1, seqs, 1, 1, 8).view(E4M3)
+    scales = torch.full((2, 1, seqs, 1, 1, 1), 128, dtype=torch.uint8, device=DEV)
+    out = torch.zeros(1, seqs, 1, 1, 8, dtype=torch.bfloat16, device=DEV)
+    plan.cache_read(ua.Cache.of(codes, scales), 1, out=(None, out))
+    torch.cuda.synchronize()
+    assert torch.equal(out, (codes[1].float() * 2).bfloat16())
+    plan.close()

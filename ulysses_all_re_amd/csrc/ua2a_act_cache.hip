@@ -81,14 +81,16 @@ template <class T, int V>
 __global__ __launch_bounds__(kActBlock) void ua2a_cache_read_kernel(CacheArgs a)
 {
     const CacheGeom& g = a.g;
-    const uint32_t ri = fdiv(blockIdx.x, g.d_tiles);            // (rank, sequence)
-    const uint32_t tile = blockIdx.x - ri * g.tiles;
+    const uint32_t wg = cache_workgroup(blockIdx.x, blockIdx.y);
+    const uint32_t ri = fdiv(wg, g.d_tiles);                    // (rank, sequence)
+    const uint32_t tile = wg - ri * g.tiles;
     const uint32_t r = fdiv(ri, g.d_seqs);
     const uint32_t i = ri - r * g.seqs;
     const CacheSpan s = cache_span(g, a.starts ? static_cast<int64_t>(a.starts[i]) : 0,
                                    a.counts ? static_cast<int64_t>(a.counts[i]) : static_cast<int64_t>(g.each));
     const int64_t e = (static_cast<int64_t>(tile) * blockDim.x + threadIdx.x) * V;
-    if (e < s.first * g.sh.run || e >= s.last * g.sh.run) return;
+    // past the last span too, here rather than ahead of the loads (read_ragged 12.1 us)
+    if (e < s.first * g.sh.run || e >= s.last * g.sh.run || ri >= g.spans) return;
     const int64_t row = static_cast<int64_t>(ri) * g.cap + s.start;             // of the span's first token
     const uint32_t nscales = g.sh.hl * g.sh.nb;
     const int64_t at_scale = g.dense ? e / kBlockValues

@@ -13,7 +13,6 @@ using namespace ua2a;
 namespace {
 
 constexpr int64_t kMaxSegments = int64_t(1) << 31;
-constexpr int64_t kMaxSlots = int64_t(kMaxGridWorkItems) - kActBlock;    // lanes of a cache read
 constexpr int64_t kMaxPieces = (int64_t(1) << 31) - 1;                   // vectors of a cache call's tensor
 constexpr int64_t kMaxCacheValues = int64_t(1) << 38;
 
@@ -484,14 +483,12 @@ int ua2a_cache_read(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t type, int64
     CacheArgs& a = L.cache;
     cache_geometry(plan, c, L.V, n, &a.g);
     CacheGeom& g = a.g;
-    if (c->sequences > kMaxSlots / plan->w || c->sequences * plan->w > kMaxSlots / n) return UA2A_ERR_SHAPE;
-    const int64_t spans = c->sequences * plan->w, rows = spans * n;
+    const int64_t spans = c->sequences * plan->w, each = g.sh.run / static_cast<uint32_t>(L.V);
+    if (n > kMaxPieces / each || spans > kMaxPieces / (n * each)) return UA2A_ERR_SHAPE;
     // a span's vectors, on whole waves of up to kActBlock lanes
-    if (n > kMaxSlots / (int64_t(g.sh.run) / L.V + 1)) return UA2A_ERR_SHAPE;
-    const int64_t vectors = n * (g.sh.run / static_cast<uint32_t>(L.V));
+    const int64_t rows = spans * n, vectors = n * each;
     L.block = vectors >= kActBlock ? kActBlock : static_cast<uint32_t>((vectors + 63) / 64 * 64);
     const int64_t tiles = (vectors + L.block - 1) / L.block;
-    if (tiles > kMaxSlots / L.block / spans) return UA2A_ERR_SHAPE;
     g.spans = static_cast<uint32_t>(spans);
     g.tiles = static_cast<uint32_t>(tiles);
     g.d_tiles = make_div32(g.tiles);
@@ -509,8 +506,7 @@ int ua2a_cache_read(ua2a_plan_t plan, const ua2a_cache_t* c, int32_t type, int64
     a.starts = starts;
     a.counts = counts;
     a.format = c->format;
-    L.grid_x = static_cast<uint32_t>(spans * tiles);
-    L.grid_y = 1;
+    cache_grid(spans * tiles, &L);                             // no more workgroups than pieces
     const int err = act_launch(L, stream);
     return err == 0 ? UA2A_OK : fail(plan, "launching the cache read", err);
 }
