@@ -62,8 +62,8 @@ extern "C" {
  *   rstd       optional: [w][B][S_local], with per_head [w][B][S_local][H]
  * A norm covers at most 65536 values of a 2-byte type or 32768 of fp32, heads
  * counted as whole blocks of 32, where D * elem_bytes is a multiple of 16 and
- * x, residual, out, sum and weight are 16-byte aligned (codes 8-byte); at most
- * 8192 otherwise.
+ * x, residual, out and sum are 16-byte aligned (codes 8-byte); at most 8192
+ * otherwise.
  * x, residual and weight may overlap one another; no output may overlap an
  * input or another output.
  * Errors: INVALID_ARG (NULL where needed, a type that is not the plan's, bad

@@ -7,9 +7,11 @@ import pytest
 import torch
 
 import ulysses_all_re_amd as ua
+from tests import act_reference as ref
 from tests.emu import act_build
+from tests.test_act_emulated import ptr, values
 from tests.test_binding_cpu import _host_plan
-from ulysses_all_re_amd.activations import ua2a_cache_t
+from ulysses_all_re_amd.activations import ua2a_cache_t, ua2a_norm_grad_t, ua2a_norm_t
 
 
 class Calls:
@@ -128,3 +130,38 @@ def test_cache_reads_up_to_the_stated_size(dry, w, H, D, n, vectors, lanes):
             x, y, block = grid(dry)
             assert block == lanes and x * y >= seqs * w * -(-vectors // lanes) and (y > 1) == (seqs > turn)
         dry.ua2a_destroy(plan)
+
+
+@pytest.mark.parametrize("fp32", [False, True], ids=["type", "fp32"])
+def test_a_weight_at_any_address_leaves_the_path(lib, fp32):
+    """A weight off a 16-byte boundary (a view into a flat parameter buffer)
+    costs a call neither its vectors nor its longest norm."""
+    for shape, per_head in (((2, 1, 4, 4, 16), 0), ((2, 1, 4, 4, 16), 1), ((1, 1, 2, 4, 4096), 0)):
+        w, B, S, H, D = shape
+        plan = make_plan(lib, *shape)
+        lib.ua2a_act_emu_reset()
+        n = D if per_head else H * D
+        x = values(shape, torch.bfloat16, 1)
+        weight = values((n + 1,), torch.float32 if fp32 else torch.bfloat16, 2)[1:]
+        assert weight.data_ptr() % 16 != 0
+        out, rstd = torch.zeros((w, B, S * w, H // w, D), dtype=torch.bfloat16), torch.zeros(w * B * S * H)
+        args = ua2a_norm_t(x=ptr(x), weight=ptr(weight), out=ptr(out), rstd=ptr(rstd), eps=1e-6, per_head=per_head,
+                           weight_type=2 if fp32 else 0)
+        assert lib.ua2a_norm_exchange(plan, 0, ctypes.byref(args), None) == 0
+        assert lib.ua2a_act_emu_last(0) == 8 and lib.ua2a_act_emu_error() == 0
+        y, h, _ = ref.norm(x, weight, 0, w, None, bool(per_head))
+        ref.check_values(out, y, torch.bfloat16, str(shape))
+        rstd = rstd[:w * B * S * (H if per_head else 1)].view((w, B, S) + ((H,) if per_head else ()))
+        dy, dx, dw = values(tuple(out.shape), torch.bfloat16, 3), torch.zeros_like(x), torch.zeros(n)
+        need = ctypes.c_int64()
+        assert lib.ua2a_norm_workspace(plan, per_head, ctypes.byref(need)) == 0
+        space = torch.zeros(need.value // 4)
+        args = ua2a_norm_grad_t(dy=ptr(dy), saved=ptr(x), weight=ptr(weight), rstd=ptr(rstd), dx=ptr(dx), dweight=ptr(dw),
+                                workspace=ptr(space), workspace_bytes=need.value, per_head=per_head,
+                                weight_type=2 if fp32 else 0)
+        assert lib.ua2a_norm_exchange_backward(plan, 0, ctypes.byref(args), None) == 0
+        assert lib.ua2a_act_emu_error() == 0
+        want = ref.norm_backward(dy, weight, 0, w, h, rstd, None, bool(per_head))
+        parts = ref.backward_terms(dy, weight, 0, w, h, rstd, None, bool(per_head))
+        ref.check_backward(dx, None, dw, want, parts, torch.bfloat16, 0, w, str(shape))
+        lib.ua2a_destroy(plan)

@@ -177,3 +177,30 @@ def test_a_read_of_more_workgroups_than_fit_along_x():
     torch.cuda.synchronize()
     assert torch.equal(out, (codes[1].float() * 2).bfloat16())
     plan.close()
+
+
+@pytest.mark.parametrize("t,wt", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("shape", [(2, 1, 5, 8, 128), (2, 1, 9, 4, 16), (1, 1, 5, 128, 128), (3, 1, 5, 6, 40)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_weights_at_any_address_give_the_same_bits(shape, t, wt):
+    """Weights one value past a 16-byte boundary, forward and backward, against aligned ones."""
+    note(f"weight address {shape} {t} {wt}")
+    plan = ua.Plan(*shape, TYPES[t], device=DEV)
+    w, B, S, H, D = shape
+    x = values(plan.in_shape(0), TYPES[t], 1).to(DEV)
+    dy = values(plan.out_shape(0), TYPES[t], 2).to(DEV)
+    for per_head in (False, True):
+        n = D if per_head else H * D
+        weight = values((n,), TYPES[wt], 3).to(DEV)
+        flat = torch.zeros(n + 1, dtype=TYPES[wt], device=DEV)
+        flat[1:] = weight
+        assert weight.data_ptr() % 16 == 0 and flat[1:].data_ptr() % 16 != 0
+        got = []
+        for v in (weight, flat[1:]):
+            r = plan.norm_exchange(x, v, 0, per_head=per_head, checkpoint=E4M3)
+            b = plan.norm_exchange_backward(dy, v, 0, r.saved, r.rstd, saved_scales=r.saved_scales, per_head=per_head)
+            got.append((r.out, b.dx, b.dweight))
+        torch.cuda.synchronize()
+        for p, q in zip(*got):
+            assert torch.equal(p, q)
+    plan.close()

@@ -257,7 +257,7 @@ int ua2a_norm_exchange(ua2a_plan_t plan, int32_t mode, const ua2a_norm_t* n, voi
         (n->weight != nullptr && misaligned(n->weight, static_cast<uintptr_t>(wbytes))) || misaligned(n->rstd, 4))
         return UA2A_ERR_ALIGN;
     const bool wide = (plan->D * plan->elem_bytes) % 16 == 0 && !misaligned(n->x, 16) && !misaligned(n->residual, 16) &&
-                      !misaligned(n->sum, 16) && !misaligned(n->weight, 16) && !misaligned(n->saved, 8) &&
+                      !misaligned(n->sum, 16) && !misaligned(n->saved, 8) &&
                       !misaligned(n->out, n->out_format ? 8 : 16);
     ActLaunch L;
     memset(&L, 0, sizeof L);
@@ -344,7 +344,7 @@ int ua2a_norm_exchange_backward(ua2a_plan_t plan, int32_t mode, const ua2a_norm_
         misaligned(n->dweight, 4) || misaligned(n->workspace, 16))
         return UA2A_ERR_ALIGN;
     const bool wide = (plan->D * plan->elem_bytes) % 16 == 0 && !misaligned(n->dy, 16) && !misaligned(n->dsum, 16) &&
-                      !misaligned(n->dx, 16) && !misaligned(n->dresidual, 16) && !misaligned(n->weight, 16) &&
+                      !misaligned(n->dx, 16) && !misaligned(n->dresidual, 16) &&
                       !misaligned(n->saved, n->saved_format ? 8 : 16);
     ActLaunch L;
     memset(&L, 0, sizeof L);

@@ -166,7 +166,9 @@ struct Places {
 };
 
 // The weights of a lane's slots as they are stored (W is the type or float);
-// the ones of a norm without weights are not looked at.
+// the ones of a norm without weights are not looked at.  They may start at any
+// value (a view into a flat buffer of parameters): the loads are the same whole
+// vectors, which global memory takes at any address.
 template <class W, int V>
 struct Weights {
     static constexpr int kRaws = sizeof(W) * V / 16 > 0 ? sizeof(W) * V / 16 : 1;
@@ -174,7 +176,8 @@ struct Weights {
     __device__ __forceinline__ void load(const void* weight, uint32_t at)
     {
         typedef typename Raw<W, V == 1 ? 1 : 16 / sizeof(W)>::type R;
-        const R* p = reinterpret_cast<const R*>(static_cast<const W*>(weight) + at);
+        typedef R Anywhere __attribute__((aligned(sizeof(W))));
+        const Anywhere* p = reinterpret_cast<const Anywhere*>(static_cast<const W*>(weight) + at);
 #pragma unroll
         for (int k = 0; k < kRaws; ++k) raw[k] = p[k];
     }
