@@ -1,9 +1,11 @@
 // Host stand-in for the device side of the activation operators (tests only):
-// every launch is carried out lane by lane on host memory with the kernels'
-// own index functions (ua2a_act_geometry.h), the arithmetic written plainly.
+// every launch is carried out lane by lane on host memory with the index
+// functions of ua2a_act_geometry.h, the arithmetic written plainly.
 // Each access is checked against the size of the buffer it belongs to, and
 // each output byte may be written once; a violation sets an error that the
-// test reads.  The exchange's own launches are not part of this library.
+// test reads.  The norm kernels address their lanes' slots by offsets from a
+// segment's base: those functions are walked too, for the kernel that the
+// launch takes, and compared with the slots' own places (check_places).  The exchange's own launches are not part of this library.
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -16,7 +18,7 @@ using namespace ua2a;
 
 namespace {
 
-int g_error = 0;              // first violation: 1 read, 2 write, 3 written twice
+int g_error = 0;              // first violation: 1 read, 2 write, 3 written twice, 4 place, 5 no such kernel
 int g_launches = 0;
 int g_dry = 0;                // launches are recorded only
 ActLaunch g_last;
@@ -241,8 +243,73 @@ size_t stat(const NormGeom& g, const Segment& s, const Slot& sl)
 }
 int64_t weight_at(const NormGeom& g, const Slot& sl) { return (per_head(g) ? 0 : int64_t(sl.hh) * g.sh.D) + sl.d; }
 
+// What every lane of a norm kernel would address, padding and lanes past the
+// last segment included: where a slot has values the place of those, else some
+// place within the buffers.
+template <Span SPAN, int V, int ITEMS>
+void check_lanes(const ActLaunch& L, const NormGeom& g)
+{
+    const int64_t n = values_of(g), ns = scales_of(g);
+    for (uint32_t group = 0; group < g.groups; ++group)
+        for (uint32_t tid = 0; tid < L.block; ++tid) {
+            const uint32_t lane = segment_lane<SPAN>(g, tid), within = segment_within<SPAN>(g, tid);
+            if (lane != tid % g.lanes || within != tid / g.lanes) flag(4);
+            const LaneSlots<ITEMS> l = lane_slots<SPAN, V, ITEMS>(g, lane);
+            const SegmentBase b = segment_base<SPAN>(g, group, within);
+            const SlotPlaces<SPAN, V, ITEMS> at{g, b, l, lane};
+            const Segment s = segment_of(g, group, within);
+            if (b.live != (s.live != 0)) flag(4);
+            for (int it = 0; it < ITEMS; ++it) {
+                const uint32_t slot = lane + static_cast<uint32_t>(it) * g.lanes;
+                const Slot sl = g.head_log ? bundle_slot(g, slot, V) : norm_slot(g, slot, V);
+                const int64_t p = b.p + at.p(it), a = b.a + at.a(it), sp = b.ps + at.scale_p(it), st = at.stat(it);
+                const int64_t wt = weight_offset<SPAN, V>(g, l, lane, it);
+                if (p < 0 || p + V > n || a < 0 || a + V > n || p % V || a % V || wt < 0 || wt + V > g.cols || wt % V ||
+                    sp < 0 || sp >= ns || st < 0 || st >= stats_of(g))
+                    flag(4);
+                if (at.ok(it) != (sl.ok != 0) || (!sl.ok && !g.padded)) flag(4);
+                if (!sl.ok) continue;
+                if (p != value_at(g, s, sl, false) || a != value_at(g, s, sl, true) || sp != scale_at(g, s, sl, false) ||
+                    b.as + at.scale_a(it) != scale_at(g, s, sl, true) || wt != weight_at(g, sl) ||
+                    st != static_cast<int64_t>(stat(g, s, sl)))
+                    flag(4);
+            }
+        }
+}
+
+// The kernels that are built: the slots per lane of each span.
+template <int V>
+void check_places_of(const ActLaunch& L, const NormGeom& g)
+{
+    const bool grad = L.kernel == ActKernel::NormGrad;
+    if (L.span == kSpanPart && L.items == 1) return check_lanes<kPart, V, 1>(L, g);
+    if (L.span == kSpanWide && L.items == 1) return check_lanes<kWide, V, 1>(L, g);
+    if (L.span == kSpanWide && L.items == 2) return check_lanes<kWide, V, 2>(L, g);
+    if (L.span == kSpanWide && L.items == 4) return check_lanes<kWide, V, 4>(L, g);
+    if (L.span == kSpanWide && L.items == 8) return check_lanes<kWide, V, 8>(L, g);
+    if (V == 1) return flag(5);
+    if (L.span == kSpanBundle && L.items == 1) return check_lanes<kBundle, V, 1>(L, g);
+    if (L.span == kSpanBundles && L.items == 1) return check_lanes<kBundles, V, 1>(L, g);
+    if (grad && L.span == kSpanBundle && L.items == 2) return check_lanes<kBundle, V, 2>(L, g);
+    if (grad && L.span == kSpanWaves && L.items == 2) return check_lanes<kWaves, V, 2>(L, g);
+    if (grad && L.span == kSpanWaves && L.items == 3) return check_lanes<kWaves, V, 3>(L, g);
+    if (grad && L.span == kSpanWaves && L.items == 4) return check_lanes<kWaves, V, 4>(L, g);
+    if (grad && L.span == kSpanWaves && L.items == 5) return check_lanes<kWaves, V, 5>(L, g);
+    flag(5);
+}
+void check_places(const ActLaunch& L, const NormGeom& g)
+{
+    if (L.V == 1)
+        check_places_of<1>(L, g);
+    else if (L.V == (L.type == UA2A_TYPE_FP32 ? 4 : 8))
+        L.V == 4 ? check_places_of<4>(L, g) : check_places_of<8>(L, g);
+    else
+        flag(5);
+}
+
 void norm(const ActLaunch& L)
 {
+    check_places(L, L.norm.g);
     const NormArgs& a = L.norm;
     const bool mode1 = a.flags & kNormMode1;
     const int32_t out_format = !(a.flags & kNormOut8) ? 0 : a.flags & kNormOutE5M2 ? UA2A_FORMAT_E5M2 : UA2A_FORMAT_E4M3;
@@ -296,6 +363,7 @@ void norm(const ActLaunch& L)
 
 void norm_grad(const ActLaunch& L)
 {
+    check_places(L, L.grad.g);
     const NormGradArgs& a = L.grad;
     const bool mode1 = a.flags & kNormMode1;
     const NormGeom& g = a.g;

@@ -9,7 +9,7 @@ import torch
 import ulysses_all_re_amd as ua
 from tests import act_reference as ref
 from tests.emu import act_build
-from tests.test_act_emulated import ptr, values
+from tests.test_act_emulated import TYPES, ptr, values
 from tests.test_binding_cpu import _host_plan
 from ulysses_all_re_amd.activations import ua2a_cache_t, ua2a_norm_grad_t, ua2a_norm_t
 
@@ -165,3 +165,51 @@ def test_a_weight_at_any_address_leaves_the_path(lib, fp32):
         parts = ref.backward_terms(dy, weight, 0, w, h, rstd, None, bool(per_head))
         ref.check_backward(dx, None, dw, want, parts, torch.bfloat16, 0, w, str(shape))
         lib.ua2a_destroy(plan)
+
+
+# (shape, per head, type): every way that segments lie on lanes, among them the
+# ones that only long norms or single values take
+LANES = [((3, 2, 5, 6, 40), True, "bf16"), ((2, 1, 7, 10, 96), True, "fp16"), ((5, 1, 3, 15, 32), True, "fp32"),
+         ((2, 1, 3, 2, 2048), True, "bf16"), ((1, 1, 5, 3, 24), False, "fp32"), ((4, 1, 3, 8, 80), False, "bf16"),
+         ((2, 1, 3, 10, 520), False, "fp16"), ((1, 1, 3, 86, 128), False, "bf16"), ((2, 1, 2, 32, 520), False, "bf16"),
+         ((2, 1, 2, 64, 512), False, "fp16"), ((1, 1, 2, 2, 32768), False, "bf16"), ((2, 1, 2, 28, 250), False, "fp32"),
+         ((2, 1, 2, 66, 33), False, "bf16"), ((3, 1, 2, 3, 1001), False, "fp32"), ((1, 1, 2, 1, 8191), True, "fp16")]
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("shape,per_head,t", LANES, ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else str(v))
+def test_every_lane_has_its_place(lib, shape, per_head, t, mode):
+    """A forward and a backward call of each kind, each lane's places checked."""
+    w, B, S, H, D = shape
+    dtype, code = TYPES[t]
+    e = torch.empty((), dtype=dtype).element_size()
+    plan = make_plan(lib, *shape, e=e)
+    lib.ua2a_act_emu_reset()
+    p, a = shape, (w, B, S * w, H // w, D)
+    n = D if per_head else H * D
+    nb = -(-D // 32)
+    x, weight = values(p if mode == 0 else a, dtype, 1), values((n,), dtype, 2)
+    oshape = a if mode == 0 else p
+    out, osc = torch.zeros(oshape, dtype=torch.uint8), torch.zeros(oshape[:-1] + (nb,), dtype=torch.uint8)
+    saved, ssc = torch.zeros(p, dtype=torch.uint8), torch.zeros(p[:-1] + (nb,), dtype=torch.uint8)
+    rstd = torch.zeros(p[:4] if per_head else p[:3])
+    args = ua2a_norm_t(ptr(x), None, ptr(weight), ptr(out), ptr(osc), None, ptr(saved), ptr(ssc), ptr(rstd), 1e-6, code,
+                       code, int(per_head), 1, 1)
+    assert lib.ua2a_norm_exchange(plan, mode, ctypes.byref(args), None) == 0
+    assert lib.ua2a_act_emu_error() == 0
+    y, h, r = ref.norm(x, weight, mode, w, None, per_head)
+    ref.check_values(rstd, r, torch.float32, "rstd")
+    ref.check_codes(out, osc, y, torch.float8_e4m3fn, "out")
+    dy, dx, dw = values(oshape, dtype, 3), torch.zeros_like(x), torch.zeros(n)
+    need = ctypes.c_int64()
+    assert lib.ua2a_norm_workspace(plan, int(per_head), ctypes.byref(need)) == 0
+    space = torch.zeros(need.value // 4)
+    args = ua2a_norm_grad_t(ptr(dy), None, ptr(saved), ptr(ssc), ptr(weight), ptr(rstd), ptr(dx), None, ptr(dw), ptr(space),
+                            need.value, code, code, int(per_head), 1, 0)
+    assert lib.ua2a_norm_exchange_backward(plan, mode, ctypes.byref(args), None) == 0
+    assert lib.ua2a_act_emu_error() == 0
+    hq = ref.dequantise(saved, ssc, torch.float8_e4m3fn)
+    want = ref.norm_backward(dy, weight, mode, w, hq, rstd, None, per_head)
+    parts = ref.backward_terms(dy, weight, mode, w, hq, rstd, None, per_head)
+    ref.check_backward(dx, None, dw, want, parts, dtype, mode, w, "lanes")
+    lib.ua2a_destroy(plan)

@@ -150,6 +150,152 @@ UA2A_HD int64_t scale_at(const NormGeom& g, const Segment& s, const Slot& sl, bo
     return (static_cast<int64_t>(s.at.p) * g.sh.H + h) * g.sh.nb + sl.blk;
 }
 
+// How a norm's segments lie on lanes: one norm on part of a wave (a power of
+// two of lanes, so several share it), on a workgroup, or on one, two or four
+// waves of a workgroup of four; bundles of heads on a wave, or several bundles
+// sharing one.
+constexpr int32_t kSpanPart = 0, kSpanWide = 1, kSpanWaves = 2, kSpanBundle = 3, kSpanBundles = 4;
+enum Span { kPart = kSpanPart, kWide = kSpanWide, kWaves = kSpanWaves, kBundle = kSpanBundle, kBundles = kSpanBundles };
+UA2A_HD constexpr bool one_norm(Span s) { return s == kPart || s == kWide || s == kWaves; }
+
+// The lane of the segment, and the segment of the workgroup, of a workgroup's lane.
+template <Span SPAN>
+UA2A_HD uint32_t segment_lane(const NormGeom& g, uint32_t tid)
+{
+    return SPAN == kWide ? tid : tid & (g.lanes - 1);
+}
+template <Span SPAN>
+UA2A_HD uint32_t segment_within(const NormGeom& g, uint32_t tid)
+{
+    if constexpr (SPAN == kWide) return 0;
+    return tid >> (31 - __builtin_clz(g.lanes));
+}
+
+// What a lane needs to know of its slots, whatever the segment: offsets from
+// the segment's first value on either side, and which slots are no padding
+// (those look at the segment's first value and are not counted).  The A
+// offset counts the heads' ranks, so it has 64 bits; a bundle may start at any
+// head, so its A offsets are worked out for each.
+template <int ITEMS>
+struct LaneSlots {
+    int64_t a[ITEMS];
+    uint32_t p[ITEMS];
+    uint32_t ok;                 // bit per slot
+};
+
+template <Span SPAN, int V>
+UA2A_HD Slot slot_of(const NormGeom& g, uint32_t lane, int it)
+{
+    const uint32_t slot = lane + static_cast<uint32_t>(it) * g.lanes;
+    return one_norm(SPAN) ? norm_slot(g, slot, V) : bundle_slot(g, slot, V);
+}
+
+template <Span SPAN, int V, int ITEMS>
+UA2A_HD LaneSlots<ITEMS> lane_slots(const NormGeom& g, uint32_t lane)
+{
+    LaneSlots<ITEMS> l;
+    l.ok = 0;
+    if (one_norm(SPAN) && g.dense) {
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+            const uint32_t slot = lane + static_cast<uint32_t>(it) * g.lanes;
+            const bool ok = slot < g.slots;
+            l.p[it] = ok ? slot * V : 0;
+            l.a[it] = a_offset_of_value(g.sh, l.p[it]);
+            l.ok |= (ok ? 1u : 0u) << it;
+        }
+        return l;
+    }
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+        const Slot s = slot_of<SPAN, V>(g, lane, it);
+        l.p[it] = s.ok ? s.hh * g.sh.D + s.d : 0;
+        l.a[it] = s.ok && one_norm(SPAN) ? a_offset(g.sh, 0, s.hh, g.sh.D, g.sh.a_rank, s.d) : 0;
+        l.ok |= s.ok << it;
+    }
+    return l;
+}
+
+// Offset of a slot's weights: of the segment's values, in bundles of a head's.
+template <Span SPAN, int V, int ITEMS>
+UA2A_HD uint32_t weight_offset(const NormGeom& g, const LaneSlots<ITEMS>& l, uint32_t lane, int it)
+{
+    if constexpr (one_norm(SPAN)) return l.p[it];
+    return l.ok & 1 ? slot_of<SPAN, V>(g, lane, 0).d : 0;
+}
+
+// A segment's first value (and scale) on either side; for bundles the A side
+// is the row's first head of a rank, and h0 the segment's first head.
+struct SegmentBase {
+    int64_t p, a, ps, as;
+    uint32_t seg;
+    uint32_t token;
+    uint32_t h0;
+    bool live;
+};
+
+template <Span SPAN>
+UA2A_HD SegmentBase segment_base(const NormGeom& g, uint32_t group, uint32_t within)
+{
+    const Segment s = segment_of(g, group, within);
+    const Slot first = {0, 0, 0, 1};
+    SegmentBase b;
+    b.p = value_at(g, s, first, false);
+    b.ps = scale_at(g, s, first, false);
+    if constexpr (one_norm(SPAN)) {
+        b.a = value_at(g, s, first, true);
+        b.as = scale_at(g, s, first, true);
+    } else {
+        b.a = static_cast<int64_t>(s.at.a) * g.sh.hl * g.sh.D;
+        b.as = static_cast<int64_t>(s.at.a) * g.sh.hl * g.sh.nb;
+    }
+    b.seg = s.seg;
+    b.token = s.at.p;
+    b.h0 = s.h0;
+    b.live = s.live;
+    return b;
+}
+
+// Where the segment's offsets are used: on the A side a bundle's depend on its
+// first head; scales' are worked out on the spot, for only calls with 8 bits
+// ask for them.
+template <Span SPAN, int V, int ITEMS>
+struct SlotPlaces {
+    const NormGeom& g;
+    const SegmentBase& s;
+    const LaneSlots<ITEMS>& l;
+    uint32_t lane;
+
+    UA2A_HD Slot slot(int it) const { return slot_of<SPAN, V>(g, lane, it); }
+    UA2A_HD bool ok(int it) const { return l.ok >> it & 1; }
+    UA2A_HD uint32_t p(int it) const { return l.p[it]; }
+    UA2A_HD int64_t a(int it) const
+    {
+        if constexpr (one_norm(SPAN)) return l.a[it];
+        const Slot sl = slot(it);
+        return sl.ok ? a_offset(g.sh, 0, s.h0 + sl.hh, g.sh.D, g.sh.a_rank, sl.d) : 0;
+    }
+    UA2A_HD uint32_t scale_p(int it) const
+    {
+        if (!ok(it)) return 0;
+        // one norm: blocks in the order of the slots
+        if constexpr (one_norm(SPAN)) return (lane + static_cast<uint32_t>(it) * g.lanes) / (kBlockValues / V);
+        const Slot sl = slot(it);
+        return sl.hh * g.sh.nb + sl.blk;
+    }
+    UA2A_HD int64_t scale_a(int it) const
+    {
+        const Slot sl = slot(it);
+        return a_offset(g.sh, 0, (one_norm(SPAN) ? 0 : s.h0) + sl.hh, g.sh.nb, g.sh.a_rank_scales, sl.blk);
+    }
+    // index of the slot's rstd
+    UA2A_HD uint32_t stat(int it) const
+    {
+        if constexpr (one_norm(SPAN)) return s.seg;
+        return s.token * g.sh.H + s.h0 + (ok(it) ? slot(it).hh : 0);
+    }
+};
+
 // --------------------------------------------------------------------- cache
 // Codes [2][w][seqs][cap][hl][D], scales [2][w][seqs][cap][hl][nb].  A call's
 // token t of sequence i has position starts[i] + t; it exists when

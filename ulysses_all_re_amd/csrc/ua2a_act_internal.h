@@ -13,12 +13,6 @@ constexpr uint32_t kActBigBlock = 1024;      // most lanes of a workgroup that o
 constexpr uint32_t kActItems = 5;            // most slots per lane of a kActBlock workgroup
 constexpr uint32_t kActBigItems = 8;         // ... of a workgroup that one norm has to itself
 
-// How a norm's segments lie on lanes: one norm on part of a wave (a power of
-// two of lanes, so several share it), on a workgroup, or on one, two or four
-// waves of a workgroup of four; bundles of heads on a wave, or several bundles
-// sharing one.
-constexpr int32_t kSpanPart = 0, kSpanWide = 1, kSpanWaves = 2, kSpanBundle = 3, kSpanBundles = 4;
-
 // What a norm call is about, one bit each.
 constexpr uint32_t kNormMode1 = 1;           // x, or dx, in A; out, or dy, in P
 constexpr uint32_t kNormWeight = 2;

@@ -1,5 +1,5 @@
-// What the norm kernels, forward and backward, share: the lanes' places in a
-// segment and the weights.
+// What the norm kernels, forward and backward, share: the lanes' segments, the
+// weights and the sums.
 #pragma once
 
 #include "ua2a_act_device.h"
@@ -7,161 +7,28 @@
 namespace ua2a {
 namespace {
 
-enum Span { kPart = kSpanPart, kWide = kSpanWide, kWaves = kSpanWaves, kBundle = kSpanBundle, kBundles = kSpanBundles };
-constexpr bool one_norm(Span s) { return s == kPart || s == kWide || s == kWaves; }
-
-// The lane of the segment, and the segment of the workgroup.  A segment of
-// whole waves is the same in every lane, so what follows from it is scalar.
+// The segment of this lane's workgroup.  A segment of whole waves is the same in
+// every lane, so what follows from it is scalar.
 template <Span SPAN>
-__device__ __forceinline__ uint32_t segment_lane(const NormGeom& g)
+__device__ __forceinline__ uint32_t my_segment(const NormGeom& g)
 {
-    return SPAN == kWide ? threadIdx.x : threadIdx.x & (g.lanes - 1);
-}
-template <Span SPAN>
-__device__ __forceinline__ uint32_t segment_within(const NormGeom& g)
-{
-    if constexpr (SPAN == kWide) return 0;
     uint32_t tid = threadIdx.x;
     if constexpr (SPAN == kWaves || SPAN == kBundle) tid = __builtin_amdgcn_readfirstlane(tid);
-    return tid >> (31 - __builtin_clz(g.lanes));
+    return segment_within<SPAN>(g, tid);
 }
 
-// What a lane needs to know of its slots, whatever the segment: offsets from
-// the segment's first value on either side, and which slots are no padding
-// (those look at the segment's first value and are not counted).  The A
-// offset counts the heads' ranks, so it has 64 bits; a bundle may start at any
-// head, so its A offsets are worked out for each.
-template <int ITEMS>
-struct LaneSlots {
-    int64_t a[ITEMS];
-    uint32_t p[ITEMS];
-    uint32_t ok;                 // bit per slot
-};
-
-template <Span SPAN, int V>
-__device__ __forceinline__ Slot slot_of(const NormGeom& g, uint32_t lane, int it)
-{
-    const uint32_t slot = lane + static_cast<uint32_t>(it) * g.lanes;
-    return one_norm(SPAN) ? norm_slot(g, slot, V) : bundle_slot(g, slot, V);
-}
-
+// SlotPlaces of which nothing derived is kept from one segment to the next.
 template <Span SPAN, int V, int ITEMS>
-__device__ __forceinline__ LaneSlots<ITEMS> lane_slots(const NormGeom& g, uint32_t lane)
-{
-    LaneSlots<ITEMS> l;
-    l.ok = 0;
-    if (one_norm(SPAN) && g.dense) {
-#pragma unroll
-        for (int it = 0; it < ITEMS; ++it) {
-            const uint32_t slot = lane + static_cast<uint32_t>(it) * g.lanes;
-            const bool ok = slot < g.slots;
-            l.p[it] = ok ? slot * V : 0;
-            l.a[it] = a_offset_of_value(g.sh, l.p[it]);
-            l.ok |= (ok ? 1u : 0u) << it;
-        }
-        return l;
-    }
-#pragma unroll
-    for (int it = 0; it < ITEMS; ++it) {
-        const Slot s = slot_of<SPAN, V>(g, lane, it);
-        l.p[it] = s.ok ? s.hh * g.sh.D + s.d : 0;
-        l.a[it] = s.ok && one_norm(SPAN) ? a_offset(g.sh, 0, s.hh, g.sh.D, g.sh.a_rank, s.d) : 0;
-        l.ok |= s.ok << it;
-    }
-    return l;
-}
-
-// Offset of a slot's weights: of the segment's values, in bundles of a head's.
-template <Span SPAN, int V, int ITEMS>
-__device__ __forceinline__ uint32_t weight_offset(const NormGeom& g, const LaneSlots<ITEMS>& l, uint32_t lane, int it)
-{
-    if constexpr (one_norm(SPAN)) return l.p[it];
-    return l.ok & 1 ? slot_of<SPAN, V>(g, lane, 0).d : 0;
-}
-
-// A segment's first value (and scale) on either side; for bundles the A side
-// is the row's first head of a rank, and h0 the segment's first head.
-struct SegmentBase {
-    int64_t p, a, ps, as;
-    uint32_t seg;
-    uint32_t token;
-    uint32_t h0;
-    bool live;
-};
-
-template <Span SPAN>
-__device__ __forceinline__ SegmentBase segment_base(const NormGeom& g, uint32_t group)
-{
-    const Segment s = segment_of(g, group, segment_within<SPAN>(g));
-    const Slot first = {0, 0, 0, 1};
-    SegmentBase b;
-    b.p = value_at(g, s, first, false);
-    b.ps = scale_at(g, s, first, false);
-    if constexpr (one_norm(SPAN)) {
-        b.a = value_at(g, s, first, true);
-        b.as = scale_at(g, s, first, true);
-    } else {
-        b.a = static_cast<int64_t>(s.at.a) * g.sh.hl * g.sh.D;
-        b.as = static_cast<int64_t>(s.at.a) * g.sh.hl * g.sh.nb;
-    }
-    b.seg = s.seg;
-    b.token = s.at.p;
-    b.h0 = s.h0;
-    b.live = s.live;
-    return b;
-}
-
-// Where the segment's offsets are used: on the A side a bundle's depend on its
-// first head; scales' are worked out on the spot, for only calls with 8 bits
-// ask for them.
-template <Span SPAN, int V, int ITEMS>
-struct Places {
-    const NormGeom& g;
-    const SegmentBase& s;
-    LaneSlots<ITEMS>& l;
-    uint32_t lane;
-
-    __device__ __forceinline__ Places(const NormGeom& g_, const SegmentBase& s_, LaneSlots<ITEMS>& l_, uint32_t lane_)
-        : g(g_), s(s_), l(l_), lane(lane_)
+struct Places : SlotPlaces<SPAN, V, ITEMS> {
+    __device__ __forceinline__ Places(const NormGeom& g, const SegmentBase& s, LaneSlots<ITEMS>& l, uint32_t lane_)
+        : SlotPlaces<SPAN, V, ITEMS>{g, s, l, lane_}
     {
-        // nothing derived from these is kept from one segment to the next
-        forget(lane);
+        forget(this->lane);
 #pragma unroll
         for (int it = 0; it < ITEMS; ++it) {
             forget(l.a[it]);
             forget(l.p[it]);
         }
-    }
-    __device__ __forceinline__ Slot slot(int it) const
-    {
-        return slot_of<SPAN, V>(g, lane, it);
-    }
-    __device__ __forceinline__ bool ok(int it) const { return l.ok >> it & 1; }
-    __device__ __forceinline__ uint32_t p(int it) const { return l.p[it]; }
-    __device__ __forceinline__ int64_t a(int it) const
-    {
-        if constexpr (one_norm(SPAN)) return l.a[it];
-        const Slot sl = slot(it);
-        return sl.ok ? a_offset(g.sh, 0, s.h0 + sl.hh, g.sh.D, g.sh.a_rank, sl.d) : 0;
-    }
-    __device__ __forceinline__ uint32_t scale_p(int it) const
-    {
-        if (!ok(it)) return 0;
-        // one norm: blocks in the order of the slots
-        if constexpr (one_norm(SPAN)) return (lane + static_cast<uint32_t>(it) * g.lanes) / (kBlockValues / V);
-        const Slot sl = slot(it);
-        return sl.hh * g.sh.nb + sl.blk;
-    }
-    __device__ __forceinline__ int64_t scale_a(int it) const
-    {
-        const Slot sl = slot(it);
-        return a_offset(g.sh, 0, (one_norm(SPAN) ? 0 : s.h0) + sl.hh, g.sh.nb, g.sh.a_rank_scales, sl.blk);
-    }
-    // index of the slot's rstd
-    __device__ __forceinline__ uint32_t stat(int it) const
-    {
-        if constexpr (one_norm(SPAN)) return s.seg;
-        return s.token * g.sh.H + s.h0 + (ok(it) ? slot(it).hh : 0);
     }
 };
 

@@ -22,9 +22,9 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_kernel(NormArgs a)
     const bool mode1 = flags & kNormMode1;
     const uint32_t group = blockIdx.y * gridDim.x + blockIdx.x;
     if (group >= g.groups) return;
-    const uint32_t lane = segment_lane<SPAN>(g);
+    const uint32_t lane = segment_lane<SPAN>(g, threadIdx.x);
     LaneSlots<ITEMS> l = lane_slots<SPAN, V, ITEMS>(g, lane);
-    const SegmentBase s = segment_base<SPAN>(g, group);
+    const SegmentBase s = segment_base<SPAN>(g, group, my_segment<SPAN>(g));
     const Places<SPAN, V, ITEMS> at(g, s, l, lane);
     typename Raw<T, V>::type h[ITEMS];
     if (mode1) {

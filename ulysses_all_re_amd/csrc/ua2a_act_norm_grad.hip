@@ -23,7 +23,7 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a)
     const NormGeom& g = a.g;
     const uint32_t flags = a.flags;
     const bool mode1 = flags & kNormMode1;
-    const uint32_t lane = segment_lane<SPAN>(g);
+    const uint32_t lane = segment_lane<SPAN>(g, threadIdx.x);
     LaneSlots<ITEMS> l = lane_slots<SPAN, V, ITEMS>(g, lane);
     // a bundle's slots of one lane are the same values of different heads
     constexpr int kWeights = one_norm(SPAN) ? ITEMS : 1;
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a)
         float rstd[kNorms];
     };
     const auto load = [&](uint32_t group, Loaded& x) {
-        x.s = segment_base<SPAN>(g, group);
+        x.s = segment_base<SPAN>(g, group, my_segment<SPAN>(g));
         const SegmentBase& s = x.s;
         const Places<SPAN, V, ITEMS> at(g, s, l, lane);
         if (mode1) {
