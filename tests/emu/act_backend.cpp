@@ -544,7 +544,8 @@ void ua2a_act_emu_reset()
     g_launches = 0;
 }
 void ua2a_act_emu_dry(int on) { g_dry = on; }
-int ua2a_act_emu_last(int what)   // 0 V, 1 items, 2 block, 3 grid, 4 lanes, 5 grid along y
+int ua2a_act_emu_last(int what)   // 0 V, 1 items, 2 block, 3 grid, 4 lanes, 5 grid along y,
+                                  // 6 groups of segments, 7 span
 {
     const NormGeom& g = g_last.kernel == ActKernel::NormGrad ? g_last.grad.g : g_last.norm.g;
     switch (what) {
@@ -553,6 +554,8 @@ int ua2a_act_emu_last(int what)   // 0 V, 1 items, 2 block, 3 grid, 4 lanes, 5 g
     case 2: return static_cast<int>(g_last.block);
     case 3: return static_cast<int>(g_last.grid_x);
     case 5: return static_cast<int>(g_last.grid_y);
+    case 6: return static_cast<int>(g.groups);
+    case 7: return g_last.span;
     default: return static_cast<int>(g.lanes);
     }
 }

@@ -11,6 +11,7 @@ from tests import act_reference as ref
 from tests.emu import act_build
 from tests.test_act_emulated import TYPES, ptr, values
 from tests.test_binding_cpu import _host_plan
+from tests.test_gpu_act_walks import WALKS
 from ulysses_all_re_amd.activations import ua2a_cache_t, ua2a_norm_grad_t, ua2a_norm_t
 
 
@@ -213,3 +214,22 @@ def test_every_lane_has_its_place(lib, shape, per_head, t, mode):
     parts = ref.backward_terms(dy, weight, mode, w, hq, rstd, None, per_head)
     ref.check_backward(dx, None, dw, want, parts, dtype, mode, w, "lanes")
     lib.ua2a_destroy(plan)
+
+
+def test_walks_are_walks(dry):
+    """Each shape of the walk tests has more than two segments for a workgroup's
+    every place, and together they take every way that segments lie on lanes."""
+    kinds = set()
+    for shape, per_head, t in WALKS:
+        dtype, code = TYPES[t]
+        plan = make_plan(dry, *shape, e=torch.empty((), dtype=dtype).element_size())
+        args = ua2a_norm_grad_t(dy=1 << 40, saved=1 << 42, rstd=1 << 44, dx=1 << 45, type=code, per_head=int(per_head))
+        assert dry.ua2a_norm_exchange_backward(plan, 0, ctypes.byref(args), None) == 0
+        V, items, _, x, _, _, groups, span = (dry.ua2a_act_emu_last(k) for k in range(8))
+        assert groups > 2 * x, shape
+        kinds.add((span, items, V == 1))
+        dry.ua2a_destroy(plan)
+    part, wide, waves, bundle, bundles = range(5)
+    assert kinds >= {(part, 1, False), (wide, 1, True), (wide, 4, True), (waves, 2, False), (waves, 3, False),
+                     (waves, 4, False), (waves, 5, False), (wide, 2, False), (bundle, 2, False), (bundle, 1, False),
+                     (bundles, 1, False)}, kinds
