@@ -10,6 +10,7 @@ import torch
 import ulysses_all_re_amd as ua
 from tests import act_reference as ref
 from tests.test_gpu_activations import E4M3, E5M2, TYPES, cpu, dev, values
+from ulysses_all_re_amd import ops
 
 pytestmark = pytest.mark.gpu
 
@@ -203,4 +204,49 @@ def test_weights_at_any_address_give_the_same_bits(shape, t, wt):
         torch.cuda.synchronize()
         for p, q in zip(*got):
             assert torch.equal(p, q)
+    plan.close()
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("checkpoint", [None, E5M2], ids=["values", "e5m2"])
+def test_an_unused_norm_adds_nothing_to_the_sums_gradient(mode, checkpoint):
+    """Where only the sum is used its gradient is x's and the residual's, beside
+    NaN, infinities and rows of zeros too, and the weight's is zero."""
+    w, B, S, H, D = 2, 1, 6, 4, 40
+    p, a = (w, B, S, H, D), (w, B, S * w, H // w, D)
+    x, res, g = values(p if mode == 0 else a, torch.bfloat16, 1), values(p, torch.bfloat16, 2), values(p, torch.bfloat16, 3)
+    res[0, 0, 1, 2, 3], res[1, 0, 0, 0, 0] = float("nan"), float("inf")
+    x[0, 0, 3], x[1, 0, 2] = float("inf"), 0
+    xd, rd = x.to(DEV).requires_grad_(True), res.to(DEV).requires_grad_(True)
+    wd = values((H * D,), torch.float32, 4).to(DEV).requires_grad_(True)
+    _, total = ops.norm_all_to_all_4D(xd, wd, *((2, 1) if mode == 0 else (1, 2)), w, residual=rd, checkpoint=checkpoint)
+    total.backward(g.to(DEV))
+    assert torch.equal(xd.grad.cpu(), g if mode == 0 else ref.to_a(g, w)) and torch.equal(rd.grad.cpu(), g)
+    assert xd.grad.data_ptr() != rd.grad.data_ptr()
+    assert wd.grad.shape == wd.shape and not bool(wd.grad.any())
+    rd.grad = None
+    _, total = ops.norm_all_to_all_4D(x.to(DEV), None, *((2, 1) if mode == 0 else (1, 2)), w, residual=rd)
+    total.backward(g.to(DEV))
+    assert torch.equal(rd.grad.cpu(), g)
+
+
+def test_a_norm_of_more_workgroups_than_fit_along_x():
+    """11.3 million tokens of five heads of one value, a workgroup of 192 lanes
+    each, forward and backward.  The weight's gradient: a workgroup of 512 adds
+    11,300,000 / 512 products in a row, with the rows' joins under 2^14.5."""
+    w, H, D, S = 1, 5, 1, 11_300_000
+    note("norm, 11.3 million workgroups")
+    plan = ua.Plan(w, 1, S, H, D, torch.bfloat16, device=DEV)
+    x, weight = values(plan.in_shape(0), torch.bfloat16, 1), values((H * D,), torch.float32, 2)
+    dy = values(plan.out_shape(0), torch.bfloat16, 3)
+    r = plan.norm_exchange(dev(x), dev(weight), 0, rstd=True)
+    b = plan.norm_exchange_backward(dev(dy), dev(weight), 0, dev(x), r.rstd)
+    torch.cuda.synchronize()
+    y, h, rstd = ref.norm(x, weight, 0, w)
+    rs = cpu(r.rstd)
+    ref.check_values(rs, rstd, torch.float32, "rstd")
+    ref.check_values(cpu(r.out), y, torch.bfloat16, "out")
+    want, parts = ref.norm_backward(dy, weight, 0, w, h, rs), ref.backward_terms(dy, weight, 0, w, h, rs)
+    ref.check_backward(cpu(b.dx), None, None, want, parts, torch.bfloat16, 0, w, "dx")
+    ref.assert_close(cpu(b.dweight), want[2], parts[1] * 2.0 ** (14.5 - 24), "dweight")
     plan.close()

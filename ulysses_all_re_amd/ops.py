@@ -288,7 +288,11 @@ def _norm_backward(ctx, g_out, g_scales, g_sum, g_saved, g_saved_scales, g_rstd)
     if g_out is None:
         if g_sum is None:
             return (None,) * 9
-        g_out = g_sum.new_zeros(_out_shape(g_sum.shape, w, 0) if mode == 0 else g_sum.shape)
+        # only the sum is used: the norm adds nothing, whatever its values are
+        needs = ctx.needs_input_grad
+        dx = None if not needs[0] else g_sum if mode == 0 else exchange(g_sum.contiguous(), w, 0)
+        dw = torch.zeros_like(weight) if ctx.weight and needs[1] else None
+        return dx, dw, g_sum if needs[2] else None, None, None, None, None, None, None
     dx, dres, dw = norm_exchange_backward(g_out, weight, saved, saved_scales, rstd, g_sum, w, mode, per_head, residual,
                                           ctx.weight and ctx.needs_input_grad[1])
     dres = (dx if mode == 0 else dres) if residual and ctx.needs_input_grad[2] else None
