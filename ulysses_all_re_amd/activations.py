@@ -415,8 +415,9 @@ class ActivationCalls:
         """Positions ``starts[i] + t`` (None: from 0), t < ``tokens`` and
         ``counts[i]`` (None: all), of every sequence, back in the plan's dtype:
         (k, v), each ``[w, sequences, tokens, H/w, D]``, one launch.  Rows
-        without a position are left as they were, zeros without ``out``; an
-        entry of ``out`` that is None is not read.
+        without a position are left as they were; without ``out`` they are
+        zeros, which fills both results first (two launches more).  An entry
+        of ``out`` that is None is not read.
         """
         code = self._type()
         self._check_cache(cache, starts, counts)

@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kActBlock) void ua2a_cache_write_kernel(CacheArgs a
 // Positions of the cache back in the type.  What a rank holds of a sequence is
 // one stretch of the cache and of the output, so a workgroup's part of it is
 // scalar work and a lane moves one vector of keys and one of values.  Measured:
-// 75,600 positions of 40 heads 375 us (6.2 TB/s; keys and values in halves of the
+// 75,600 positions of 40 heads 378 us (6.2 TB/s; keys and values in halves of the
 // grid 409).
 template <class T, int V>
 __global__ __launch_bounds__(kActBlock) void ua2a_cache_read_kernel(CacheArgs a)

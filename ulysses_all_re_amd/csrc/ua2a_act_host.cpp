@@ -101,9 +101,11 @@ uint32_t log2_of(uint32_t pow2)
 // needs with one, two or four slots per lane, up to kActBlock lanes (measured:
 // single precision, 288 slots, 82 us against 88 with 512 lanes; 640 slots 341
 // against 339, and 489 with 640 lanes); backward the fewest of one, two or four
-// waves with at most kActItems slots each.  Beyond them up to kActBigBlock lanes
-// (backward with as few slots per lane as those allow: four would not fit the
-// registers of so many lanes).
+// waves with at most kActItems slots each.  Beyond them up to kActBigBlock lanes,
+// backward with as few slots per lane as those allow (12,288 values from 8 bits:
+// two slots on 768 lanes 205 us, four on 384 773).  The lanes of so wide a
+// workgroup have 128 registers: eight slots, backward four too, spill (24,576
+// values backward 768 us; 49,152 forward 273, four slots at 32,768 190).
 //
 // A norm per head of up to 64 slots (the next power of two): heads in
 // bundles, which leaves all sums within a wave.  A bundle's lanes are the most
@@ -167,11 +169,16 @@ int norm_geometry(const ua2a_plan_s* p, int32_t per_head, int32_t V, bool backwa
     return UA2A_OK;
 }
 
-// Most workgroups of a backward launch: as many as the device holds at once,
-// each walking over segments (its kernels keep sums in registers, so fewer fit
-// as the slots per lane grow).  A grid that is no multiple of what is resident
-// leaves part of the device idle at the end: video-DiT with five slots per
-// lane 354 us with 512 workgroups, 451 with 768, 377 with 1024.
+// Most workgroups of a backward launch, each walking over segments: about as many
+// as the device holds at once of the kernels with 2-byte values and weights (they
+// keep sums in registers, so fewer fit as the slots per lane grow).  A grid that
+// is no multiple of what is resident leaves part of the device idle at the end:
+// video-DiT with five slots per lane 354 us with 512 workgroups, 451 with 768,
+// 377 with 1024.  The rule sees slots only.  Of the kernels with a weight in
+// single precision 256 workgroups of five slots are resident, 512 of three: two
+// rounds, and one and a half (video-DiT 514 us, 359 with the weight in bf16).  Of
+// those with single-precision values more would fit (four slots 768, two 1280),
+// and of kSpanWide workgroups past 512 lanes one per CU.
 uint32_t grad_grid(int32_t span, int32_t items)
 {
     if (span == kSpanWide) return 512;
