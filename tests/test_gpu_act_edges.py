@@ -3,6 +3,7 @@ others, scale bytes that are NaN, weights at any address, many sequences."""
 from __future__ import annotations
 
 import sys
+import threading
 
 import pytest
 import torch
@@ -249,4 +250,104 @@ def test_a_norm_of_more_workgroups_than_fit_along_x():
     want, parts = ref.norm_backward(dy, weight, 0, w, h, rs), ref.backward_terms(dy, weight, 0, w, h, rs)
     ref.check_backward(cpu(b.dx), None, None, want, parts, torch.bfloat16, 0, w, "dx")
     ref.assert_close(cpu(b.dweight), want[2], parts[1] * 2.0 ** (14.5 - 24), "dweight")
+    plan.close()
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("eps", [1e-45, 1e38], ids=["least", "large"])
+def test_the_least_and_large_eps_on_rows_of_zeros(t, eps):
+    """Tokens of zeros have rstd = 1 / sqrt(eps), eps being any positive float."""
+    plan = ua.Plan(2, 1, 3, 4, 16, TYPES[t], device=DEV)
+    x = values(plan.in_shape(0), TYPES[t], 1)
+    x[0, 0, 1], x[1, 0, 2] = 0, 0
+    eps32 = float(torch.tensor(eps, dtype=torch.float32))
+    y, h, rstd = ref.norm(x, None, 0, 2, None, False, eps32)
+    r = plan.norm_exchange(dev(x), None, 0, eps=eps, rstd=True)
+    dy = values(plan.out_shape(0), TYPES[t], 2, 2.0 ** -24)
+    b = plan.norm_exchange_backward(dev(dy), None, 0, dev(x), r.rstd)
+    torch.cuda.synchronize()
+    rs = cpu(r.rstd)
+    ref.check_values(rs, rstd, torch.float32, "rstd")
+    ref.check_values(cpu(r.out), y, TYPES[t], "out")
+    want = ref.norm_backward(dy, None, 0, 2, h, rs)
+    most = torch.finfo(TYPES[t]).max
+    fits = bool((want[0].abs() < most).all())                   # fp16 holds no gradient of 2^50
+    assert fits or t == "fp16"
+    if fits:
+        ref.check_backward(cpu(b.dx), None, None, want, ref.backward_terms(dy, None, 0, 2, h, rs), TYPES[t], 0, 2, "dx")
+    plan.close()
+
+
+def test_forward_and_backward_captured_together():
+    """The operator's forward and backward pass in one graph, replayed on new
+    inputs with eager work in between: the eager bits every time."""
+    w, B, S, H, D = 2, 1, 300, 8, 64
+    note("operator captured")
+    p, a = (w, B, S, H, D), (w, B, S * w, H // w, D)
+    x = values(p, torch.bfloat16, 1).to(DEV).requires_grad_(True)
+    res = values(p, torch.bfloat16, 2).to(DEV).requires_grad_(True)
+    weight = values((H * D,), torch.float32, 3).to(DEV).requires_grad_(True)
+    gy, gs = values(a, torch.bfloat16, 4).to(DEV), values(p, torch.bfloat16, 5).to(DEV)
+
+    def step():
+        y, total = ops.norm_all_to_all_4D(x, weight, 2, 1, w, residual=res, checkpoint=E4M3)
+        return (y, total) + torch.autograd.grad([y, total], [x, res, weight], [gy, gs])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [t.detach() for t in step()]
+    for seed in (10, 20, 30):
+        with torch.no_grad():
+            for t, s in ((x, 0), (res, 1), (weight, 2), (gy, 3), (gs, 4)):
+                t.copy_(values(tuple(t.shape), t.dtype, seed + s))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in got]
+        want = [t.detach() for t in step()]
+        torch.cuda.synchronize()
+        for k, e in zip(kept, want):
+            assert torch.equal(k, e), seed
+
+
+def test_one_plan_in_several_threads():
+    """Calls of one plan from four threads on streams of their own: each thread's bits are its own."""
+    plan = ua.Plan(4, 1, 400, 8, 64, torch.bfloat16, device=DEV)
+    weight = values((512,), torch.float32, 1).to(DEV)
+    sets = []
+    for i in range(4):
+        x, dy = values(plan.in_shape(0), torch.bfloat16, 10 + i).to(DEV), values(plan.out_shape(0), torch.bfloat16, 20 + i).to(DEV)
+        starts = torch.tensor([3 * i], dtype=torch.int32, device=DEV)
+        sets.append((x, dy, starts, ua.Cache(4, 8, 64, 1, 1700, E4M3, DEV)))
+
+    def calls(x, dy, starts, cache, stream):
+        f = plan.norm_exchange(x, weight, 0, checkpoint=E5M2, stream=stream)
+        b = plan.norm_exchange_backward(dy, weight, 0, f.saved, f.rstd, saved_scales=f.saved_scales, stream=stream)
+        plan.cache_write(cache, x, x, starts, stream=stream)
+        k, v = plan.cache_read(cache, 1600, starts, stream=stream)
+        return f.out, f.saved, f.rstd, b.dx, b.dweight, k, v
+
+    want = [calls(*s, torch.cuda.current_stream()) for s in sets]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def run(i):
+        stream = torch.cuda.Stream()
+        for _ in range(5):
+            got[i] = calls(*sets[i], stream)
+        stream.synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for g, e in zip(got, want):
+        for p, q in zip(g, e):
+            assert torch.equal(cpu(p), cpu(q))
     plan.close()
