@@ -13,7 +13,7 @@ namespace {
 // fixed; at the end each workgroup writes one row of partial sums.  Those
 // registers leave two waves per SIMD, so the next segment's loads are issued
 // before one is worked on.  Measured: video-DiT from an e4m3 checkpoint 367 us
-// (5.3 TB/s; without the early loads 374 on a box where this form took 347),
+// (5.3 TB/s; without the early loads 374 on a card where this form took 347),
 // from the values 394 us (5.9 TB/s).
 template <class T, class W, bool SAVED8, int V, Span SPAN, int ITEMS, int BLOCK>
 __global__ __launch_bounds__(BLOCK) void ua2a_norm_grad_kernel(NormGradArgs a)
