@@ -101,7 +101,7 @@ def load_library() -> ctypes.CDLL:
         raise RuntimeError(
             f"{LIBRARY} is missing: build it with `python -m ulysses_all_re_amd.build` "
             "(the exchange has no non-HIP implementation)")
-    _lib = declare_activation_signatures(declare_signatures(ctypes.CDLL(LIBRARY)))
+    _lib = declare_attention_signatures(declare_activation_signatures(declare_signatures(ctypes.CDLL(LIBRARY))))
     return _lib
 
 
@@ -282,6 +282,9 @@ def ua2a_describe(plan: int, mode: int, chunked: int, inp: int, out: int) -> dic
 # the operators of include/ua2a_act.h: norms joined with the exchange, the 8-bit cache
 from .activations import (  # noqa: E402  (uses the names above)
     ActivationCalls, Cache, NormExchange, NormGradients, declare_activation_signatures)
+# those of include/ua2a_attn.h: rotary positions, attention with a sliding window and sinks
+from .attention import (  # noqa: E402
+    Attention, AttentionCalls, AttentionGradients, Rotary, declare_attention_signatures)
 
 
 # ------------------------------------------------------------- torch wrapper
@@ -296,7 +299,7 @@ def _current_raw_stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-class Plan(ActivationCalls):
+class Plan(ActivationCalls, AttentionCalls):
     """A ua2a plan bound to torch tensors on one device.
 
     ``window``: optional device tensor used as the one-plane window of

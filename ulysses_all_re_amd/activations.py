@@ -376,10 +376,14 @@ class ActivationCalls:
         return NormGradients(dx, dres if apart else dx if residual else None, dw)
 
     def _check_cache(self, cache: Cache, starts, counts) -> None:
+        self._check_cache_of(cache, self.H, starts, counts)
+
+    def _check_cache_of(self, cache: Cache, heads, starts, counts) -> None:
+        """Checks a cache of `heads` heads on all ranks (None: any), and what goes with it."""
         codes, scales = cache._codes, cache._scales
         if codes.data_ptr() != cache._codes_at or scales.data_ptr() != cache._scales_at:
             cache._set(codes, scales)                          # a tensor has been given other memory
-        if cache.heads_of != (self.w, self.H, self.D):
+        if cache.heads_of != (self.w, cache.heads_of[1] if heads is None else heads, self.D):
             raise ValueError(f"cache has w = {cache.w}, {cache.heads} heads of {cache.D} per rank; "
                              f"the plan w = {self.w}, {self.H // self.w} of {self.D}")
         if cache.device != self.device:

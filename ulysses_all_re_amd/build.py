@@ -20,12 +20,16 @@ LIBRARY = os.path.join(PKG, "libua2a.so")
 SOURCES = [os.path.join(CSRC, "ua2a_kernels.hip"), os.path.join(CSRC, "ua2a_host.cpp"),
            os.path.join(CSRC, "ua2a_act_norm.hip"), os.path.join(CSRC, "ua2a_act_norm_grad.hip"),
            os.path.join(CSRC, "ua2a_act_cache.hip"), os.path.join(CSRC, "ua2a_act_launch.hip"),
-           os.path.join(CSRC, "ua2a_act_host.cpp")]
+           os.path.join(CSRC, "ua2a_act_host.cpp"), os.path.join(CSRC, "ua2a_rope.hip"),
+           os.path.join(CSRC, "ua2a_attn_forward.hip"), os.path.join(CSRC, "ua2a_attn_backward.hip"),
+           os.path.join(CSRC, "ua2a_attn_launch.hip"), os.path.join(CSRC, "ua2a_attn_host.cpp")]
 HEADERS = [os.path.join(INCLUDE, "ua2a.h"), os.path.join(INCLUDE, "ua2a_act.h"),
            os.path.join(CSRC, "ua2a_geometry.h"), os.path.join(CSRC, "ua2a_bodies.h"),
            os.path.join(CSRC, "ua2a_internal.h"), os.path.join(CSRC, "ua2a_act_geometry.h"),
            os.path.join(CSRC, "ua2a_act_internal.h"), os.path.join(CSRC, "ua2a_act_device.h"),
-           os.path.join(CSRC, "ua2a_act_norm.h")]
+           os.path.join(CSRC, "ua2a_act_norm.h"), os.path.join(CSRC, "ua2a_act_checks.h"),
+           os.path.join(INCLUDE, "ua2a_attn.h"), os.path.join(CSRC, "ua2a_attn_geometry.h"),
+           os.path.join(CSRC, "ua2a_attn_internal.h"), os.path.join(CSRC, "ua2a_attn_device.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,384 @@
+// gfx950 kernels of windowed attention's backward pass (ua2a_attn.h).
+//
+// With P = exp(scale s - lse), delta = sum(dout * out) of a row and
+// dS = P * (dout v^T - delta):
+//   dq = scale dS k,  dk = scale dS^T q,  dv = P^T dout.
+// The first two products (s and dout v^T) are made twice, once where rows keep
+// their sums (dq) and once where keys keep theirs (dk, dv): seven products
+// instead of five, and in return no atomics, so equal inputs give equal bits.
+#include "ua2a_attn_device.h"
+
+namespace ua2a {
+namespace {
+
+// Rows of two tensors on their way from memory to LDS, CH chunks of eight values
+// per lane of each.
+template <int DP, int ROWS>
+struct PairLoads {
+    static constexpr int kAcross = DP / 8;
+    static constexpr int kChunks = ROWS * kAcross;
+    static constexpr int CH = (kChunks + static_cast<int>(kAttnBlock) - 1) / static_cast<int>(kAttnBlock);
+    u32x4v a[CH], b[CH];
+
+    // whether the lane's chunk c is one of the tile's
+    __device__ __forceinline__ static bool has(int c)
+    {
+        return kChunks % kAttnBlock == 0 || threadIdx.x + c * kAttnBlock < static_cast<uint32_t>(kChunks);
+    }
+
+    // at(row): elements from the tensors' starts, or -1 for zeros
+    template <class F>
+    __device__ __forceinline__ void load(const void* pa, const void* pb, uint32_t D, F at)
+    {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const uint32_t i = threadIdx.x + c * kAttnBlock, d = i % kAcross * 8;
+            a[c] = b[c] = u32x4v{0, 0, 0, 0};
+            if (!has(c)) continue;
+            const int64_t e = at(i / kAcross);
+            if (e >= 0 && d < D) {
+                a[c] = *reinterpret_cast<const u32x4v*>(static_cast<const uint16_t*>(pa) + e + d);
+                b[c] = *reinterpret_cast<const u32x4v*>(static_cast<const uint16_t*>(pb) + e + d);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(char* ta, char* tb) const
+    {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const uint32_t i = threadIdx.x + c * kAttnBlock;
+            if (!has(c)) continue;
+            const uint32_t to = i / kAcross * row_stride<DP>() + i % kAcross * 16;
+            *reinterpret_cast<u32x4v*>(ta + to) = a[c];
+            *reinterpret_cast<u32x4v*>(tb + to) = b[c];
+        }
+    }
+};
+
+__device__ __forceinline__ float dot2_sum(u32x4v a, u32x4v b, float sum, __bf16)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sum = __builtin_amdgcn_fdot2_f32_bf16(pair_of<__bf16>(a[i]), pair_of<__bf16>(b[i]), sum, false);
+    return sum;
+}
+__device__ __forceinline__ float dot2_sum(u32x4v a, u32x4v b, float sum, _Float16)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = __builtin_amdgcn_fdot2(pair_of<_Float16>(a[i]), pair_of<_Float16>(b[i]), sum, false);
+    return sum;
+}
+
+// lse times log2(e), such that a row without weight (-inf) gets none.
+__device__ __forceinline__ float lse2_of(float lse)
+{
+    return lse == -__builtin_inff() ? __builtin_inff() : lse * kLog2e;
+}
+
+template <int N>
+__device__ __forceinline__ void zero(f32x16v (&x)[N])
+{
+#pragma unroll
+    for (int b = 0; b < N; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[b][i] = 0.f;
+}
+
+// A lane's column of a transposed sum, times `factor`, as a row of values.
+template <class T, int DP>
+__device__ __forceinline__ void store_row(void* out, int64_t at, uint32_t D, const f32x16v (&x)[DP / 32], float factor,
+                                          bool live)
+{
+    const uint32_t half = (threadIdx.x & 63) >> 5;
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t d = db * 32 + b * 8 + half * 4;
+            u32x2v y = {0, 0};
+            if (live)
+                y = u32x2v{pack2<T>(x[db][4 * b] * factor, x[db][4 * b + 1] * factor),
+                           pack2<T>(x[db][4 * b + 2] * factor, x[db][4 * b + 3] * factor)};
+            if (d < D) *reinterpret_cast<u32x2v*>(static_cast<uint16_t*>(out) + at + d) = y;
+        }
+}
+
+// dq, and delta for the other kernel.  As forward, a wave has 32 rows as columns
+// of its matrix tiles and walks tiles of 64 keys: scores and dout v^T come as
+// keys x rows, dS goes on to its product with k from the registers it is in.
+template <class T, int DP>
+__global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(AttnGradArgs a)
+{
+    constexpr int KEYS = kAttnKeys, NK = KEYS / 32;
+    constexpr uint32_t kTile = KEYS * row_stride<DP>();
+    __shared__ __attribute__((aligned(16))) char lds[2 * kTile];
+    char* const ktile = lds;
+    char* const vtile = lds + kTile;
+    const AttnGeom& g = a.g;
+    const uint32_t item = attn_item(g, (blockIdx.y << kAttnGridLog) + blockIdx.x);
+    if (item >= g.items) return;
+    const AttnPlace at = attn_place(g, item);
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const uint32_t half = lane >> 5, col = lane & 31;
+    const AttnSeq seq = attn_seq(g, 0, a.counts != nullptr ? static_cast<int64_t>(a.counts[at.i]) : static_cast<int64_t>(g.n));
+    const uint32_t first = at.tile * kAttnRows, past = umin32(first + kAttnRows, g.rows);
+    const uint32_t wfirst = first + wave * kAttnWaveRows, row = wfirst + col;
+    const bool in = row < past, rows = wfirst < past;
+    const RowPlace place = row_place(g, at, in ? row : past - 1);
+    const bool live = in && place.t < seq.last;
+    f32x16v dq[DP / 32];
+    zero(dq);
+    if (static_cast<int32_t>(fdiv(first, g.d_group)) < seq.last) {
+        const Seen top = seen_by_row(g, seq, first), bottom = seen_by_row(g, seq, past - 1);
+        const KeyWalk walk = key_walk(top, bottom, KEYS);
+        const uint32_t wlast = umin32(wfirst + kAttnWaveRows, past) - 1;
+        const Seen wtop = rows ? seen_by_row(g, seq, wfirst) : bottom, wbottom = rows ? seen_by_row(g, seq, wlast) : bottom;
+        const Seen seen = seen_by_row(g, seq, place.row);
+        u32x4v q[DP / 16], go[DP / 16];
+        float delta = 0.f;
+        {
+            u32x4v o[DP / 16];
+            row_operands<DP>(static_cast<const uint16_t*>(a.dout) + place.at, g.D, half, live, go);
+            row_operands<DP>(static_cast<const uint16_t*>(a.out) + place.at, g.D, half, live, o);
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) delta = dot2_sum(go[ks], o[ks], delta, T{});
+            delta += other_half(delta);
+        }
+        if (live && half == 0) a.delta[static_cast<int64_t>(at.unit) * g.rows + row] = delta;
+        row_operands<DP>(static_cast<const uint16_t*>(a.q) + place.at, g.D, half, live, q);
+        const float lse2 = live ? lse2_of(a.lse[place.stat]) : __builtin_inff();
+        const int64_t base = static_cast<int64_t>(at.seq) * g.keys * g.kvl + at.kvh;
+        PairLoads<DP, KEYS> loads;
+        const auto load = [&](uint32_t i) {
+            const int32_t k0 = static_cast<int32_t>(walk_tile(walk, i) * KEYS);
+            loads.load(a.k, a.v, g.D, [&](uint32_t r) {
+                const int32_t j = k0 + static_cast<int32_t>(r);
+                return j < seq.end ? (base + static_cast<int64_t>(j) * g.kvl) * g.D : int64_t(-1);
+            });
+        };
+        load(0);
+        for (uint32_t i = 0; i < walk.total; ++i) {
+            const int32_t k0 = static_cast<int32_t>(walk_tile(walk, i) * KEYS);
+            __syncthreads();                                     // the last tile has been read
+            loads.store(ktile, vtile);
+            if (i + 1 < walk.total) load(i + 1);
+            __syncthreads();
+#pragma unroll
+            for (int b = 0; b < NK; ++b) {
+                const int32_t bk0 = k0 + b * 32;
+                if (!rows || none_seen(wtop, wbottom, bk0, bk0 + 32)) continue;
+                const bool masked = !all_seen(wtop, wbottom, bk0, bk0 + 32);
+                f32x16v s, dp;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    s[x] = 0.f;
+                    dp[x] = -delta;
+                }
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks) s = mfma<T>(along<DP>(ktile, b * 32 + col, half, ks), q[ks], s);
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks) dp = mfma<T>(along<DP>(vtile, b * 32 + col, half, ks), go[ks], dp);
+#pragma unroll
+                for (int x = 0; x < 16; ++x) dp[x] *= __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], a.scale2, -lse2));
+                if (masked) {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        if (!sees(seen, bk0 + static_cast<int32_t>((x / 4) * 8 + half * 4 + x % 4))) dp[x] = 0.f;
+                }
+                const u32x4v ds[2] = {operand_of<T>(dp, 0), operand_of<T>(dp, 1)};
+#pragma unroll
+                for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) dq[db] = mfma<T>(transposed<DP>(ktile, b * 32, t, db), ds[t], dq[db]);
+            }
+        }
+    }
+    if (in) store_row<T, DP>(a.dq, place.at, g.D, dq, a.scale, live);
+}
+
+// dk and dv.  A wave has 32 keys as columns of its matrix tiles and walks the
+// rows that see one of the workgroup's 128 keys in tiles of 32: scores and
+// dout v^T come as rows x keys, and P and dS go on from their registers to the
+// products with dout and q.  The first tiles of keys, which see all rows (sinks),
+// or all tiles of a small call, are walked in `splits` parts by workgroups of
+// their own, whose sums a third kernel joins in order.
+template <class T, int DP>
+__global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(AttnGradArgs a)
+{
+    constexpr int ROWS = 32;
+    constexpr uint32_t kTile = ROWS * row_stride<DP>();
+    __shared__ __attribute__((aligned(16))) char lds[2 * kTile];
+    __shared__ __attribute__((aligned(16))) float stat[2 * ROWS];
+    char* const qtile = lds;
+    char* const gtile = lds + kTile;
+    const AttnGeom& g = a.g;
+    const uint32_t item = attn_item(g, (blockIdx.y << kAttnGridLog) + blockIdx.x);
+    if (item >= g.items) return;
+    const KeyPlace at = key_place(g, a.keys, item);
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const uint32_t half = lane >> 5, col = lane & 31;
+    const AttnSeq seq = attn_seq(g, 0, a.counts != nullptr ? static_cast<int64_t>(a.counts[at.at.i]) : static_cast<int64_t>(g.n));
+    const uint32_t first = at.at.tile * kAttnGradKeys, past = umin32(first + kAttnGradKeys, g.keys);
+    const uint32_t j = first + wave * 32 + col;
+    const bool in = j < past, live = in && static_cast<int32_t>(j) < seq.end;
+    const int64_t to = ((static_cast<int64_t>(at.at.seq) * g.keys + (in ? j : first)) * g.kvl + at.at.kvh) * g.D;
+    f32x16v dk[DP / 32], dv[DP / 32];
+    zero(dk);
+    zero(dv);
+    if (static_cast<int32_t>(first) < seq.end) {
+        u32x4v k[DP / 16], v[DP / 16];
+        row_operands<DP>(static_cast<const uint16_t*>(a.k) + to, g.D, half, live, k);
+        row_operands<DP>(static_cast<const uint16_t*>(a.v) + to, g.D, half, live, v);
+        // the rows that see this lane's key, and those that see one of the workgroup's
+        const Span32 mine = live ? seers_of(g.win, static_cast<int32_t>(j), static_cast<int32_t>(j) + 1, seq.end) : Span32{0, 0};
+        const uint32_t ra = static_cast<uint32_t>(mine.first) * g.group, rb = static_cast<uint32_t>(mine.last) * g.group;
+        const int32_t end = static_cast<int32_t>(past) < seq.end ? static_cast<int32_t>(past) : seq.end;
+        const RowWalk walk = row_walk(g, seers_of(g.win, static_cast<int32_t>(first), end, seq.end), ROWS);
+        const uint32_t from = split_at(walk.total, at.parts, at.at.split), upto = split_at(walk.total, at.parts, at.at.split + 1);
+        const uint32_t live_rows = static_cast<uint32_t>(seq.last) * g.group;
+        PairLoads<DP, ROWS> loads;
+        float next_stat = 0.f;
+        const auto load = [&](uint32_t i) {
+            const uint32_t r0 = (walk.from + i) * ROWS;
+            loads.load(a.q, a.dout, g.D, [&](uint32_t r) {
+                return r0 + r < live_rows ? row_place(g, at.at, r0 + r).at : int64_t(-1);
+            });
+            if (threadIdx.x < 2 * ROWS) {
+                const uint32_t r = r0 + (threadIdx.x & (ROWS - 1));
+                const bool is_lse = threadIdx.x < ROWS;
+                next_stat = is_lse ? __builtin_inff() : 0.f;
+                if (r < live_rows)
+                    next_stat = is_lse ? lse2_of(a.lse[row_place(g, at.at, r).stat])
+                                       : -a.delta[static_cast<int64_t>(at.at.unit) * g.rows + r];
+            }
+        };
+        if (from < upto) load(from);
+        for (uint32_t i = from; i < upto; ++i) {
+            const uint32_t r0 = (walk.from + i) * ROWS;
+            __syncthreads();                                     // the last tile has been read
+            loads.store(qtile, gtile);
+            if (threadIdx.x < 2 * ROWS) stat[threadIdx.x] = next_stat;
+            if (i + 1 < upto) load(i + 1);
+            __syncthreads();
+            const bool none = r0 + ROWS <= ra || r0 >= rb, all = ra <= r0 && r0 + ROWS <= rb;
+            if (__builtin_amdgcn_ballot_w64(live && !none) == 0) continue;
+            const bool masked = __builtin_amdgcn_ballot_w64(live && !all) != 0;
+            f32x16v s, dp;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const f32x4v d = *reinterpret_cast<const f32x4v*>(stat + ROWS + b * 8 + half * 4);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    s[4 * b + x] = 0.f;
+                    dp[4 * b + x] = d[x];
+                }
+            }
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) s = mfma<T>(along<DP>(qtile, col, half, ks), k[ks], s);
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) dp = mfma<T>(along<DP>(gtile, col, half, ks), v[ks], dp);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const f32x4v l = *reinterpret_cast<const f32x4v*>(stat + b * 8 + half * 4);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    s[4 * b + x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * b + x], a.scale2, -l[x]));
+            }
+            if (masked) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const uint32_t r = r0 + (x / 4) * 8 + half * 4 + x % 4;
+                    if (!(r >= ra && r < rb)) s[x] = dp[x] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 16; ++x) dp[x] *= s[x];
+            const u32x4v p[2] = {operand_of<T>(s, 0), operand_of<T>(s, 1)};
+            const u32x4v ds[2] = {operand_of<T>(dp, 0), operand_of<T>(dp, 1)};
+#pragma unroll
+            for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) dv[db] = mfma<T>(transposed<DP>(gtile, 0, t, db), p[t], dv[db]);
+#pragma unroll
+            for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) dk[db] = mfma<T>(transposed<DP>(qtile, 0, t, db), ds[t], dk[db]);
+        }
+    }
+    if (!in) return;
+    if (at.parts > 1) {
+        float* line = a.partial + part_line(g, a.keys, at, j) * 2 * g.D;
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const uint32_t d = db * 32 + b * 8 + half * 4;
+                if (d >= g.D) continue;
+                f32x4v x, y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = live ? dk[db][4 * b + e] : 0.f;
+                    y[e] = live ? dv[db][4 * b + e] : 0.f;
+                }
+                *reinterpret_cast<f32x4v*>(line + d) = x;
+                *reinterpret_cast<f32x4v*>(line + g.D + d) = y;
+            }
+        return;
+    }
+    store_row<T, DP>(a.dk, to, g.D, dk, a.scale, live);
+    store_row<T, DP>(a.dv, to, g.D, dv, 1.f, live);
+}
+
+// The parts of keys whose rows were walked by several workgroups, joined in
+// order: 2 * D / 4 lanes a key.
+template <class T>
+__global__ __launch_bounds__(kAttnBlock) void ua2a_attention_keys_join_kernel(AttnGradArgs a)
+{
+    const AttnGeom& g = a.g;
+    const uint32_t per = g.D / 2;
+    const int64_t id = static_cast<int64_t>((blockIdx.y << kAttnGridLog) + blockIdx.x) * kAttnBlock + threadIdx.x;
+    const int64_t line = id / per;                               // of unit * span + key
+    const uint32_t span = a.keys.span;
+    const int64_t lines = static_cast<int64_t>(g.units) * span;
+    if (line >= lines) return;
+    const uint32_t c = static_cast<uint32_t>(id - line * per) * 4;          // of dk's and dv's D
+    const uint32_t unit = static_cast<uint32_t>(line / span), j = static_cast<uint32_t>(line - static_cast<int64_t>(unit) * span);
+    const uint32_t seq = fdiv(unit, g.d_kvl), kvh = unit - seq * g.kvl;
+    f32x4v x = {0.f, 0.f, 0.f, 0.f};
+    for (uint32_t s = 0; s < g.splits; ++s)
+        x += *reinterpret_cast<const f32x4v*>(a.partial + (s * lines + line) * 2 * g.D + c);
+    const bool is_v = c >= g.D;
+    const float f = is_v ? 1.f : a.scale;
+    const int64_t to = ((static_cast<int64_t>(seq) * g.keys + j) * g.kvl + kvh) * g.D + (is_v ? c - g.D : c);
+    *reinterpret_cast<u32x2v*>(static_cast<uint16_t*>(is_v ? a.dv : a.dk) + to) =
+        u32x2v{pack2<T>(x[0] * f, x[1] * f), pack2<T>(x[2] * f, x[3] * f)};
+}
+
+template <class T, int DP>
+const void* sized_fn(const AttnLaunch& L)
+{
+    return L.kernel == AttnKernel::GradRows ? reinterpret_cast<const void*>(&ua2a_attention_rows_kernel<T, DP>)
+                                            : reinterpret_cast<const void*>(&ua2a_attention_keys_kernel<T, DP>);
+}
+
+template <class T>
+const void* typed_fn(const AttnLaunch& L)
+{
+    if (L.kernel == AttnKernel::GradJoin) return reinterpret_cast<const void*>(&ua2a_attention_keys_join_kernel<T>);
+    switch (L.DP) {
+    case 32: return sized_fn<T, 32>(L);
+    case 64: return sized_fn<T, 64>(L);
+    case 96: return sized_fn<T, 96>(L);
+    case 128: return sized_fn<T, 128>(L);
+    }
+    return nullptr;
+}
+
+}  // namespace
+
+const void* attention_grad_kernel(const AttnLaunch& L)
+{
+    return L.type == UA2A_TYPE_BF16 ? typed_fn<__bf16>(L) : typed_fn<_Float16>(L);
+}
+
+}  // namespace ua2a

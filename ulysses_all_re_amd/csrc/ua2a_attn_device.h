@@ -1,0 +1,171 @@
+// Device functions that the attention kernels share: matrix tiles, their
+// operands in LDS, and rows of keys on their way there.
+//
+// Matrix tiles are 32 x 32, 16 deep (v_mfma_f32_32x32x16).  Lane l of a wave
+// has column l % 32 of B and of the result, row l % 32 of A; of the depth the
+// half h = l / 32 has eight places, and of the result's rows 8g + 4h .. + 3 in
+// its registers 4g .. 4g + 3.  A result goes into the next product as B
+// without leaving its lane: its registers 8s .. 8s + 7 are the depth places of
+// step s if A's depth runs in the order 16s + 4h + (0..3), 16s + 8 + 4h + (0..3),
+// and that is what `transposed` reads.
+#pragma once
+
+#include "ua2a_act_device.h"
+#include "ua2a_attn_internal.h"
+
+namespace ua2a {
+namespace {
+
+typedef float f32x16v __attribute__((ext_vector_type(16)));
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8v __attribute__((ext_vector_type(8)));
+typedef short s16x4v __attribute__((ext_vector_type(4)));
+
+template <class T>
+__device__ __forceinline__ f32x16v mfma(u32x4v a, u32x4v b, f32x16v c)
+{
+    if constexpr (__is_same(T, __bf16))
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8v, a), __builtin_bit_cast(bf16x8v, b), c,
+                                                       0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8v, a), __builtin_bit_cast(f16x8v, b), c, 0,
+                                                      0, 0);
+}
+
+// Two values in 32 bits rounded to the type, the first in the low half.
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    typedef T vec __attribute__((ext_vector_type(2)));
+    const vec v = {static_cast<T>(a), static_cast<T>(b)};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// Registers 8s .. 8s + 7 of a result, rounded to the type: B's operand of depth step s.
+template <class T>
+__device__ __forceinline__ u32x4v operand_of(const f32x16v& c, int s)
+{
+    u32x4v r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = pack2<T>(c[8 * s + 2 * i], c[8 * s + 2 * i + 1]);
+    return r;
+}
+
+// The value of the lane 32 places on (or back), joined by f.
+__device__ __forceinline__ float other_half(float x)
+{
+    return __shfl_xor(x, 32);
+}
+
+// A tile of rows in LDS: 16-byte chunks of a row side by side, rows a chunk
+// more than their values apart, so that eight lanes' chunks of eight rows lie
+// in different banks.
+template <int DP>
+constexpr int row_stride()
+{
+    return DP * 2 + 16;                      // bytes
+}
+
+// A's operand with a row of the tile per lane: row `row`, depth step ks along the row.
+template <int DP>
+__device__ __forceinline__ u32x4v along(const char* tile, uint32_t row, uint32_t half, int ks)
+{
+    return *reinterpret_cast<const u32x4v*>(tile + row * row_stride<DP>() + ks * 32 + half * 16);
+}
+
+// A's operand with a column of the tile per lane, the depth along the rows in
+// the order above: rows row0 + 16s .. + 15, columns 32 * db ...
+// ds_read_b64_tr_b16 hands lane i of 16 lanes value i of the four rows whose
+// 32 bytes their addresses name, four lanes a row.
+template <int DP>
+__device__ __forceinline__ u32x4v transposed(const char* tile, uint32_t row0, int s, int db)
+{
+    const uint32_t lane = threadIdx.x & 63;
+    const uint32_t at = (row0 + (lane >> 5) * 4 + ((lane & 15) >> 2)) * row_stride<DP>() + ((lane >> 4) & 1) * 32 +
+                        (lane & 3) * 8 + s * (16 * row_stride<DP>()) + db * 64;
+    typedef __attribute__((address_space(3))) s16x4v lds4;
+    const char* p = tile + at;
+    const s16x4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(const_cast<char*>(p)));
+    const s16x4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(const_cast<char*>(p + 8 * row_stride<DP>())));
+    const u32x2v x = __builtin_bit_cast(u32x2v, a), y = __builtin_bit_cast(u32x2v, b);
+    return u32x4v{x[0], x[1], y[0], y[1]};
+}
+
+// B's operands of a row per lane, straight from memory: chunk ks * 2 + half.
+// Values past D are zeros.
+template <int DP>
+__device__ __forceinline__ void row_operands(const void* row, uint32_t D, uint32_t half, bool live, u32x4v (&r)[DP / 16])
+{
+#pragma unroll
+    for (int ks = 0; ks < DP / 16; ++ks) {
+        const uint32_t d = ks * 16 + half * 8;
+        r[ks] = u32x4v{0, 0, 0, 0};
+        if (live && d < D) r[ks] = *reinterpret_cast<const u32x4v*>(static_cast<const uint16_t*>(row) + d);
+    }
+}
+
+// Where a row's values start: of q and out, and its place among the statistics.
+struct RowPlace {
+    int64_t at;                  // elements
+    int64_t stat;                // lse
+    uint32_t row;
+    int32_t t;
+};
+
+__device__ __forceinline__ RowPlace row_place(const AttnGeom& g, const AttnPlace& p, uint32_t row)
+{
+    RowPlace r;
+    const uint32_t t = fdiv(row, g.d_group);
+    const uint32_t head = p.kvh * g.group + (row - t * g.group);
+    r.row = row;
+    r.t = static_cast<int32_t>(t);
+    r.at = ((static_cast<int64_t>(p.seq) * g.n + t) * g.hl + head) * g.D;
+    r.stat = (static_cast<int64_t>(p.seq) * g.hl + head) * g.n + t;
+    return r;
+}
+
+// Infinities and NaN among eight values: whether there are any, the values with
+// zeros in their places, and a bit for each that is NaN or the infinity of a
+// sign (0 or 0x8000).
+template <class T>
+__device__ __forceinline__ constexpr uint32_t exponent_bits()
+{
+    return __is_same(T, __bf16) ? 0x7f80u : 0x7c00u;
+}
+template <class T>
+__device__ __forceinline__ bool unbounded(u32x4v r)
+{
+    constexpr uint32_t kExp = exponent_bits<T>() * 0x10001u;
+    constexpr uint32_t kOne = __is_same(T, __bf16) ? 0x00800080u : 0x04000400u;
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) any |= (r[i] & kExp) + kOne;
+    return (any & 0x80008000u) != 0;
+}
+template <class T>
+__device__ __forceinline__ u32x4v finite_part(u32x4v v)
+{
+    constexpr uint32_t kExp = exponent_bits<T>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((v[i] & kExp) == kExp) v[i] &= 0xffff0000u;
+        if ((v[i] >> 16 & kExp) == kExp) v[i] &= 0xffffu;
+    }
+    return v;
+}
+template <class T>
+__device__ __forceinline__ uint32_t unbounded_bits(u32x4v v, uint32_t sign)
+{
+    constexpr uint32_t kExp = exponent_bits<T>();
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w = v[i / 2] >> (i % 2 * 16) & 0xffffu;
+        if (w == (kExp | sign) || (w & 0x7fffu) > kExp) bits |= 1u << i;
+    }
+    return bits;
+}
+
+}  // namespace
+}  // namespace ua2a

@@ -1,0 +1,461 @@
+// gfx950 kernels of windowed attention (ua2a_attn.h): of gathered heads, and of
+// new tokens over the 8-bit cache.
+//
+// One pass over the keys with the running maximum m and sum l of each row's
+// softmax, in 32 bits: o = sum exp(s - m) v, rescaled when m grows.  A row is
+// a query token and head; heads that share a key head lie in one tile, so its
+// keys are read once for all of them.  A wave has 32 rows as the columns of its
+// matrix tiles: scores come as keys x rows, so a row's maximum and sum are a
+// lane's own work but for the other half's, and the weights go on to the
+// product with the values from the registers they are in.
+#include "ua2a_attn_device.h"
+
+namespace ua2a {
+namespace {
+
+// The rows of keys and values of a tile on their way from memory to LDS: CH
+// chunks of eight values per lane of each.
+template <class T, int DP, int KEYS, bool CODES>
+struct KeyLoads {
+    static constexpr int kAcross = DP / 8;                       // chunks of a row
+    static constexpr int CH = KEYS * kAcross / kAttnBlock;
+    u32x4v k[CODES ? 1 : CH], v[CODES ? 1 : CH];
+    u32x2v kc[CODES ? CH : 1], vc[CODES ? CH : 1];
+    uint32_t ks[CODES ? CH : 1], vs[CODES ? CH : 1];
+
+    // base: the sequence's position 0 of this key head.  Positions at or past
+    // `end`, and values past D, are zeros.
+    __device__ __forceinline__ void load(const AttnArgs& a, const char* kbase, const char* vbase, const uint8_t* kscale,
+                                         const uint8_t* vscale, int32_t k0)
+    {
+        const AttnGeom& g = a.g;
+        const int64_t row_values = static_cast<int64_t>(g.kvl) * g.D;
+        const int64_t row_scales = static_cast<int64_t>(g.kvl) * g.nb;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const uint32_t i = threadIdx.x + c * kAttnBlock;
+            const uint32_t row = i / kAcross, d = i % kAcross * 8;
+            const bool ok = static_cast<int32_t>(k0 + row) < end && d < g.D;
+            const int64_t at = (k0 + static_cast<int64_t>(row)) * row_values + d;
+            if constexpr (CODES) {
+                kc[c] = vc[c] = u32x2v{0, 0};
+                ks[c] = vs[c] = 0;
+                if (ok) {
+                    const int64_t sat = (k0 + static_cast<int64_t>(row)) * row_scales + d / kBlockValues;
+                    kc[c] = *reinterpret_cast<const u32x2v*>(kbase + at);
+                    vc[c] = *reinterpret_cast<const u32x2v*>(vbase + at);
+                    ks[c] = kscale[sat];
+                    vs[c] = vscale[sat];
+                }
+            } else {
+                k[c] = v[c] = u32x4v{0, 0, 0, 0};
+                if (ok) {
+                    k[c] = *reinterpret_cast<const u32x4v*>(kbase + at * 2);
+                    v[c] = *reinterpret_cast<const u32x4v*>(vbase + at * 2);
+                }
+            }
+        }
+    }
+
+    // Into LDS.  look: values' infinities and NaN become zeros there, and a bit
+    // each in `wild` ([row][2][DP / 8] bytes: +inf or NaN, -inf or NaN); returns
+    // whether this lane had any.
+    __device__ __forceinline__ bool store(char* ktile, char* vtile, uint8_t* wild, int32_t format, bool look)
+    {
+        bool odd = false;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const uint32_t i = threadIdx.x + c * kAttnBlock;
+            const uint32_t at = i / kAcross * row_stride<DP>() + i % kAcross * 16;
+            u32x4v kk, vv;
+            if constexpr (CODES) {
+                kk = decode_raw<T, 8>(kc[c], ks[c], format);
+                vv = decode_raw<T, 8>(vc[c], vs[c], format);
+            } else {
+                kk = k[c];
+                vv = v[c];
+            }
+            *reinterpret_cast<u32x4v*>(ktile + at) = kk;
+            if (look) {
+                const bool mine = unbounded<T>(vv);
+                uint32_t up = 0, down = 0;
+                if (mine) {
+                    up = unbounded_bits<T>(vv, 0);
+                    down = unbounded_bits<T>(vv, 0x8000u);
+                    vv = finite_part<T>(vv);
+                }
+                uint8_t* bits = wild + i / kAcross * (2 * kAcross) + i % kAcross;
+                bits[0] = static_cast<uint8_t>(up);
+                bits[kAcross] = static_cast<uint8_t>(down);
+                odd = odd || mine;
+            }
+            *reinterpret_cast<u32x4v*>(vtile + at) = vv;
+        }
+        return odd;
+    }
+
+    int32_t end;
+};
+
+// The running softmax of a wave's 32 rows and their sums over the values.
+template <class T, int DP>
+struct Rows {
+    f32x16v o[DP / 32];
+    float m;                     // times log2(e); -inf until the row has seen a key
+    float l;                     // of this half's keys
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
+        m = -__builtin_inff();
+        l = 0.f;
+    }
+};
+
+// One tile of 32 * NK keys for a wave: scores, softmax, sums.  k0: position of
+// the tile's row `row0`.  masked: some row does not see some key.  odd: the
+// tile's values had infinities or NaN, which a row must take only of keys it
+// sees (zero times them is NaN): zeros are in their places, and `wild` says
+// where they were.
+//
+// The maximum may lag by 2^8: exp2 then gives up to 256, which costs no
+// precision, and a row's sums are rescaled a few times in all.  The weights are
+// rounded to the type for the product (relative half a step of it, as its
+// operands are), their sum is not.
+template <class T, int DP, int NK>
+__device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16], const char* ktile, const char* vtile,
+                                       const uint8_t* wild, uint32_t row0, int32_t k0, const Seen& seen, float scale2,
+                                       bool masked, bool odd)
+{
+    const uint32_t lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
+    f32x16v s[NK];
+#pragma unroll
+    for (int b = 0; b < NK; ++b) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks)
+            s[b] = mfma<T>(along<DP>(ktile, row0 + b * 32 + col, half, ks), q[ks], s[b]);
+    }
+    const auto key = [&](int b, int i) {
+        return k0 + static_cast<int32_t>(b * 32 + (i / 4) * 8 + half * 4 + i % 4);
+    };
+    if (masked) {
+#pragma unroll
+        for (int b = 0; b < NK; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (!sees(seen, key(b, i))) s[b][i] = -__builtin_inff();
+    }
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int b = 0; b < NK; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+    top = fmaxf(top, other_half(top)) * scale2;
+    const bool grow = top > r.m + 8.f || (r.m == -__builtin_inff() && top > r.m);
+    if (__builtin_amdgcn_ballot_w64(grow) != 0) {
+        const float next = fmaxf(r.m, top);
+        const float f = next == r.m ? 1.f : __builtin_amdgcn_exp2f(r.m - next);
+        r.m = next;
+        r.l *= f;
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r.o[db][i] *= f;
+    }
+    const float m = r.m == -__builtin_inff() ? 0.f : r.m;
+    float sum = 0.f;
+#pragma unroll
+    for (int b = 0; b < NK; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], scale2, -m));
+            sum += s[b][i];
+        }
+    r.l += sum;
+    u32x4v p[2 * NK];
+#pragma unroll
+    for (int b = 0; b < NK; ++b)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) p[2 * b + t] = operand_of<T>(s[b], t);
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int t = 0; t < 2 * NK; ++t) r.o[db] = mfma<T>(transposed<DP>(vtile, row0, t, db), p[t], r.o[db]);
+    if (!odd) return;
+    // the tile's infinities and NaN: of the keys that the row sees, one bit per value
+    uint32_t up[DP / 32], down[DP / 32];
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db) up[db] = down[db] = 0;
+#pragma unroll 1
+    for (uint32_t j = 0; j < 32 * NK; ++j) {
+        const bool see = sees(seen, k0 + static_cast<int32_t>(j));
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db) {
+            const uint32_t* bits = reinterpret_cast<const uint32_t*>(wild + (row0 + j) * (DP / 4)) + db;
+            up[db] |= see ? bits[0] : 0u;
+            down[db] |= see ? bits[DP / 32] : 0u;
+        }
+    }
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t bit = (i / 4) * 8 + half * 4 + i % 4;
+            if (up[db] >> bit & 1) r.o[db][i] += __builtin_inff();
+            if (down[db] >> bit & 1) r.o[db][i] -= __builtin_inff();
+        }
+}
+
+// SHARED false: each wave has 32 rows of the workgroup's 128, and all walk tiles
+// of 64 keys.  SHARED true (at most 32 rows: single tokens): the waves have the
+// same rows and a quarter of each tile of 128 keys, and their sums are joined in
+// LDS.
+template <class T, int DP, bool CODES, bool SHARED>
+__global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs a)
+{
+    constexpr int KEYS = SHARED ? kAttnSplitKeys : kAttnKeys;
+    constexpr int NK = SHARED ? 1 : KEYS / 32;
+    constexpr uint32_t kTile = KEYS * row_stride<DP>();
+    __shared__ __attribute__((aligned(16))) char lds[2 * kTile];
+    __shared__ __attribute__((aligned(16))) uint8_t wild[KEYS * (DP / 4)];
+    __shared__ uint32_t odd_tile;
+    __shared__ float stat[SHARED ? 5 * 32 * 2 : 1];            // the waves', then joined
+    char* const ktile = lds;
+    char* const vtile = lds + kTile;
+    const AttnGeom& g = a.g;
+    const uint32_t item = attn_item(g, (blockIdx.y << kAttnGridLog) + blockIdx.x);
+    if (item >= g.items) return;
+    const AttnPlace at = attn_place(g, item);
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const uint32_t half = lane >> 5, col = lane & 31;
+    const AttnSeq seq = attn_seq(g, a.starts != nullptr ? static_cast<int64_t>(a.starts[at.i]) : 0,
+                                 a.counts != nullptr ? static_cast<int64_t>(a.counts[at.i]) : static_cast<int64_t>(g.n));
+    const uint32_t first = at.tile * (SHARED ? kAttnWaveRows : kAttnRows);
+    const uint32_t past = umin32(first + (SHARED ? kAttnWaveRows : kAttnRows), g.rows);
+    const uint32_t wfirst = SHARED ? first : first + wave * kAttnWaveRows;
+    const uint32_t row = wfirst + col;
+    const bool in = row < past;
+    const RowPlace place = row_place(g, at, in ? row : past - 1);
+    const bool live = in && place.t >= seq.first && place.t < seq.last;
+
+    Rows<T, DP> r;
+    r.clear();
+    // no query of the tile exists: nothing to walk
+    const bool some = static_cast<int32_t>(fdiv(first, g.d_group)) < seq.last &&
+                      static_cast<int32_t>(fdiv(past - 1, g.d_group)) >= seq.first;
+    if (some) {
+        const Seen top = seen_by_row(g, seq, first), bottom = seen_by_row(g, seq, past - 1);
+        const KeyWalk walk = key_walk(top, bottom, KEYS);
+        const uint32_t from = split_at(walk.total, g.splits, at.split), to = split_at(walk.total, g.splits, at.split + 1);
+        const uint32_t wlast = umin32(wfirst + kAttnWaveRows, past) - 1;
+        const bool rows = wfirst < past;                         // of the wave
+        const Seen wtop = rows ? seen_by_row(g, seq, wfirst) : bottom, wbottom = rows ? seen_by_row(g, seq, wlast) : bottom;
+        const Seen seen = seen_by_row(g, seq, place.row);
+        u32x4v q[DP / 16];
+        row_operands<DP>(static_cast<const uint16_t*>(a.q) + place.at, g.D, half, live, q);
+
+        const int64_t base = static_cast<int64_t>(at.seq) * g.keys * g.kvl + at.kvh;
+        const char *kbase, *vbase;
+        const uint8_t *kscale = nullptr, *vscale = nullptr;
+        if constexpr (CODES) {
+            kbase = reinterpret_cast<const char*>(a.codes + base * g.D);
+            vbase = kbase + a.part;
+            kscale = a.scales + base * g.nb;
+            vscale = kscale + a.part_scales;
+        } else {
+            kbase = static_cast<const char*>(a.k) + base * g.D * 2;
+            vbase = static_cast<const char*>(a.v) + base * g.D * 2;
+        }
+        KeyLoads<T, DP, KEYS, CODES> loads;
+        loads.end = seq.end;
+        if (from < to) loads.load(a, kbase, vbase, kscale, vscale, static_cast<int32_t>(walk_tile(walk, from) * KEYS));
+        if (threadIdx.x == 0) odd_tile = ~0u;
+        for (uint32_t i = from; i < to; ++i) {
+            const int32_t k0 = static_cast<int32_t>(walk_tile(walk, i) * KEYS);
+            const bool look = !all_seen(top, bottom, k0, k0 + KEYS);
+            __syncthreads();                                     // the last tile has been read
+            if (loads.store(ktile, vtile, wild, a.format, look)) odd_tile = i;
+            if (i + 1 < to)
+                loads.load(a, kbase, vbase, kscale, vscale, static_cast<int32_t>(walk_tile(walk, i + 1) * KEYS));
+            __syncthreads();
+            const uint32_t row0 = SHARED ? wave * 32 : 0;
+            const int32_t wk0 = k0 + static_cast<int32_t>(row0);
+            if (!rows || none_seen(wtop, wbottom, wk0, wk0 + 32 * NK)) continue;
+            attend<T, DP, NK>(r, q, ktile, vtile, wild, row0, wk0, seen, a.scale2,
+                              !all_seen(wtop, wbottom, wk0, wk0 + 32 * NK), look && odd_tile == i);
+        }
+    }
+    r.l += other_half(r.l);
+    if constexpr (SHARED) {
+        // the four waves' maxima and sums, then their values' sums, 32 rows of DP each
+        if (half == 0) {
+            stat[(wave * 32 + col) * 2] = r.m;
+            stat[(wave * 32 + col) * 2 + 1] = r.l;
+        }
+        __syncthreads();
+        float m = -__builtin_inff(), l = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m = fmaxf(m, stat[(w * 32 + col) * 2]);
+        const float mm = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            l += stat[(w * 32 + col) * 2 + 1] * __builtin_amdgcn_exp2f(stat[(w * 32 + col) * 2] - mm);
+        const float f = __builtin_amdgcn_exp2f(r.m - mm);
+        float* sums = reinterpret_cast<float*>(lds);             // [wave][row][DP]: no more than the tiles take
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                f32x4v x;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = r.o[db][4 * b + i] * f;
+                *reinterpret_cast<f32x4v*>(sums + (wave * 32 + col) * DP + db * 32 + b * 8 + half * 4) = x;
+            }
+        if (half == 0 && wave == 0) {
+            stat[(128 + col) * 2] = m;
+            stat[(128 + col) * 2 + 1] = l;
+        }
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < 32 * (DP / 4); i += kAttnBlock) {
+            const uint32_t c = i / (DP / 4), d = i % (DP / 4) * 4;
+            if (first + c >= past || d >= g.D) continue;
+            f32x4v x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) x += *reinterpret_cast<const f32x4v*>(sums + (w * 32 + c) * DP + d);
+            const RowPlace pl = row_place(g, at, first + c);
+            const bool alive = pl.t >= seq.first && pl.t < seq.last;
+            const float cm = stat[(128 + c) * 2], cl = stat[(128 + c) * 2 + 1];
+            if (g.splits > 1) {
+                const int64_t line = static_cast<int64_t>(at.split) * g.units * g.rows + static_cast<int64_t>(at.unit) * g.rows +
+                                     pl.row;
+                *reinterpret_cast<f32x4v*>(a.partial + line * g.D + d) = x;
+                if (d == 0) {
+                    a.stats[line * 2] = alive ? cm : -__builtin_inff();
+                    a.stats[line * 2 + 1] = alive ? cl : 0.f;
+                }
+                continue;
+            }
+            if (!alive && a.keep) continue;
+            const float inv = alive && cl != 0.f ? 1.f / cl : 0.f;
+            u32x2v y = {0, 0};
+            if (alive) y = u32x2v{pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv)};
+            *reinterpret_cast<u32x2v*>(static_cast<uint16_t*>(a.out) + pl.at + d) = y;
+            if (d == 0 && a.lse != nullptr)
+                a.lse[pl.stat] = alive && cl != 0.f ? cm * kLn2 + logf(cl) : -__builtin_inff();
+        }
+        return;
+    }
+    if (!in) return;
+    if (g.splits > 1) {
+        const int64_t line = static_cast<int64_t>(at.split) * g.units * g.rows + static_cast<int64_t>(at.unit) * g.rows + row;
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const uint32_t d = db * 32 + b * 8 + half * 4;
+                if (d < g.D)
+                    *reinterpret_cast<f32x4v*>(a.partial + line * g.D + d) =
+                        f32x4v{r.o[db][4 * b], r.o[db][4 * b + 1], r.o[db][4 * b + 2], r.o[db][4 * b + 3]};
+            }
+        if (half == 0) {
+            a.stats[line * 2] = live ? r.m : -__builtin_inff();
+            a.stats[line * 2 + 1] = live ? r.l : 0.f;
+        }
+        return;
+    }
+    if (!live && a.keep) return;
+    const float inv = live && r.l != 0.f ? 1.f / r.l : 0.f;
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t d = db * 32 + b * 8 + half * 4;
+            u32x2v y = {0, 0};
+            if (live)
+                y = u32x2v{pack2<T>(r.o[db][4 * b] * inv, r.o[db][4 * b + 1] * inv),
+                           pack2<T>(r.o[db][4 * b + 2] * inv, r.o[db][4 * b + 3] * inv)};
+            if (d < g.D) *reinterpret_cast<u32x2v*>(static_cast<uint16_t*>(a.out) + place.at + d) = y;
+        }
+    if (half == 0 && a.lse != nullptr)
+        a.lse[place.stat] = live && r.l != 0.f ? r.m * kLn2 + logf(r.l) : -__builtin_inff();
+}
+
+// The parts of rows whose keys were walked by several workgroups, joined: D / 4
+// lanes a row.
+template <class T>
+__global__ __launch_bounds__(kAttnBlock) void ua2a_attention_join_kernel(AttnArgs a)
+{
+    const AttnGeom& g = a.g;
+    const uint32_t per = g.D / 4;
+    const int64_t id = static_cast<int64_t>((blockIdx.y << kAttnGridLog) + blockIdx.x) * kAttnBlock + threadIdx.x;
+    const int64_t lines = static_cast<int64_t>(g.units) * g.rows;
+    const int64_t line = id / per;
+    const uint32_t d = static_cast<uint32_t>(id - line * per) * 4;
+    if (line >= lines) return;
+    AttnPlace at;
+    at.unit = static_cast<uint32_t>(line / g.rows);
+    at.seq = fdiv(at.unit, g.d_kvl);
+    at.kvh = at.unit - at.seq * g.kvl;
+    at.i = at.seq - fdiv(at.seq, g.d_seqs) * g.seqs;
+    const RowPlace pl = row_place(g, at, static_cast<uint32_t>(line - static_cast<int64_t>(at.unit) * g.rows));
+    const AttnSeq seq = attn_seq(g, a.starts != nullptr ? static_cast<int64_t>(a.starts[at.i]) : 0,
+                                 a.counts != nullptr ? static_cast<int64_t>(a.counts[at.i]) : static_cast<int64_t>(g.n));
+    const bool live = pl.t >= seq.first && pl.t < seq.last;
+    if (!live && a.keep) return;
+    float m = -__builtin_inff(), l = 0.f;
+    f32x4v x = {0.f, 0.f, 0.f, 0.f};
+    if (live) {
+        for (uint32_t s = 0; s < g.splits; ++s) m = fmaxf(m, a.stats[(s * lines + line) * 2]);
+        const float mm = m == -__builtin_inff() ? 0.f : m;
+        for (uint32_t s = 0; s < g.splits; ++s) {
+            const float sm = a.stats[(s * lines + line) * 2], sl = a.stats[(s * lines + line) * 2 + 1];
+            const float f = __builtin_amdgcn_exp2f(sm - mm);
+            const f32x4v p = *reinterpret_cast<const f32x4v*>(a.partial + (s * lines + line) * g.D + d);
+            l += sl * f;
+            x += p * f;
+        }
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    u32x2v y = {0, 0};
+    if (live) y = u32x2v{pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv)};
+    *reinterpret_cast<u32x2v*>(static_cast<uint16_t*>(a.out) + pl.at + d) = y;
+    if (d == 0 && a.lse != nullptr) a.lse[pl.stat] = live && l != 0.f ? m * kLn2 + logf(l) : -__builtin_inff();
+}
+
+template <class T, int DP>
+const void* sized_fn(const AttnLaunch& L)
+{
+    const bool codes = L.attn.codes != nullptr;
+    if (codes)
+        return L.shared ? reinterpret_cast<const void*>(&ua2a_attention_kernel<T, DP, true, true>)
+                        : reinterpret_cast<const void*>(&ua2a_attention_kernel<T, DP, true, false>);
+    return L.shared ? reinterpret_cast<const void*>(&ua2a_attention_kernel<T, DP, false, true>)
+                    : reinterpret_cast<const void*>(&ua2a_attention_kernel<T, DP, false, false>);
+}
+
+template <class T>
+const void* typed_fn(const AttnLaunch& L)
+{
+    if (L.kernel == AttnKernel::Join) return reinterpret_cast<const void*>(&ua2a_attention_join_kernel<T>);
+    switch (L.DP) {
+    case 32: return sized_fn<T, 32>(L);
+    case 64: return sized_fn<T, 64>(L);
+    case 96: return sized_fn<T, 96>(L);
+    case 128: return sized_fn<T, 128>(L);
+    }
+    return nullptr;
+}
+
+}  // namespace
+
+const void* attention_kernel(const AttnLaunch& L)
+{
+    return L.type == UA2A_TYPE_BF16 ? typed_fn<__bf16>(L) : typed_fn<_Float16>(L);
+}
+
+}  // namespace ua2a
