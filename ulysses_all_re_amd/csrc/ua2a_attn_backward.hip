@@ -11,50 +11,6 @@
 namespace ua2a {
 namespace {
 
-// Rows of two tensors on their way from memory to LDS, CH chunks of eight values
-// per lane of each.
-template <int DP, int ROWS>
-struct PairLoads {
-    static constexpr int kAcross = DP / 8;
-    static constexpr int kChunks = ROWS * kAcross;
-    static constexpr int CH = (kChunks + static_cast<int>(kAttnBlock) - 1) / static_cast<int>(kAttnBlock);
-    u32x4v a[CH], b[CH];
-
-    // whether the lane's chunk c is one of the tile's
-    __device__ __forceinline__ static bool has(int c)
-    {
-        return kChunks % kAttnBlock == 0 || threadIdx.x + c * kAttnBlock < static_cast<uint32_t>(kChunks);
-    }
-
-    // at(row): elements from the tensors' starts, or -1 for zeros
-    template <class F>
-    __device__ __forceinline__ void load(const void* pa, const void* pb, uint32_t D, F at)
-    {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const uint32_t i = threadIdx.x + c * kAttnBlock, d = i % kAcross * 8;
-            a[c] = b[c] = u32x4v{0, 0, 0, 0};
-            if (!has(c)) continue;
-            const int64_t e = at(i / kAcross);
-            if (e >= 0 && d < D) {
-                a[c] = *reinterpret_cast<const u32x4v*>(static_cast<const uint16_t*>(pa) + e + d);
-                b[c] = *reinterpret_cast<const u32x4v*>(static_cast<const uint16_t*>(pb) + e + d);
-            }
-        }
-    }
-    __device__ __forceinline__ void store(char* ta, char* tb) const
-    {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const uint32_t i = threadIdx.x + c * kAttnBlock;
-            if (!has(c)) continue;
-            const uint32_t to = i / kAcross * row_stride<DP>() + i % kAcross * 16;
-            *reinterpret_cast<u32x4v*>(ta + to) = a[c];
-            *reinterpret_cast<u32x4v*>(tb + to) = b[c];
-        }
-    }
-};
-
 __device__ __forceinline__ float dot2_sum(u32x4v a, u32x4v b, float sum, __bf16)
 {
 #pragma unroll
@@ -110,10 +66,8 @@ template <class T, int DP>
 __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(AttnGradArgs a)
 {
     constexpr int KEYS = kAttnKeys, NK = KEYS / 32;
-    constexpr uint32_t kTile = KEYS * row_stride<DP>();
-    __shared__ __attribute__((aligned(16))) char lds[2 * kTile];
-    char* const ktile = lds;
-    char* const vtile = lds + kTile;
+    constexpr uint32_t kTile = KEYS * kRow<DP>;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * kTile];           // two buffers of keys and values
     const AttnGeom& g = a.g;
     const uint32_t item = attn_item(g, (blockIdx.y << kAttnGridLog) + blockIdx.x);
     if (item >= g.items) return;
@@ -148,21 +102,36 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
         row_operands<DP>(static_cast<const uint16_t*>(a.q) + place.at, g.D, half, live, q);
         const float lse2 = live ? lse2_of(a.lse[place.stat]) : __builtin_inff();
         const int64_t base = static_cast<int64_t>(at.seq) * g.keys * g.kvl + at.kvh;
-        PairLoads<DP, KEYS> loads;
-        const auto load = [&](uint32_t i) {
-            const int32_t k0 = static_cast<int32_t>(walk_tile(walk, i) * KEYS);
-            loads.load(a.k, a.v, g.D, [&](uint32_t r) {
-                const int32_t j = k0 + static_cast<int32_t>(r);
-                return j < seq.end ? (base + static_cast<int64_t>(j) * g.kvl) * g.D : int64_t(-1);
-            });
+        typedef TileLoads<DP, KEYS> Loads;
+        uint32_t offset[Loads::N];
+        const uint32_t row_bytes = g.kvl * g.D * 2;
+#pragma unroll
+        for (int n = 0; n < Loads::N; ++n) {
+            const uint32_t bytes = Loads::bytes(n, wave, g.D);
+            offset[n] = bytes == kNowhere ? kNowhere : Loads::row(n, wave) * row_bytes + bytes;
+        }
+        const auto position = [&](uint32_t i) { return static_cast<int32_t>(walk_tile(walk, i) * KEYS); };
+        const auto load = [&](uint32_t i, char* tile) {
+            const int32_t k0 = position(i);
+            const int64_t start = (base + static_cast<int64_t>(k0) * g.kvl) * g.D * 2;
+            const uint32_t bytes = static_cast<uint32_t>(seq.end - k0 < KEYS ? seq.end - k0 : KEYS) * row_bytes;
+            const u32x4v k = descriptor(static_cast<const char*>(a.k) + start, bytes),
+                         v = descriptor(static_cast<const char*>(a.v) + start, bytes);
+#pragma unroll
+            for (int n = 0; n < Loads::N; ++n) {
+                if (!Loads::has(n, wave)) continue;
+                char* const to_lds = tile + (n * 4 + wave) * 1024;
+                load_to_lds(k, offset[n], to_lds);
+                load_to_lds(v, offset[n], to_lds + kTile);
+            }
         };
-        load(0);
+        char *ktile = lds, *other = lds + 2 * kTile;
+        load(0, ktile);
         for (uint32_t i = 0; i < walk.total; ++i) {
-            const int32_t k0 = static_cast<int32_t>(walk_tile(walk, i) * KEYS);
-            __syncthreads();                                     // the last tile has been read
-            loads.store(ktile, vtile);
-            if (i + 1 < walk.total) load(i + 1);
-            __syncthreads();
+            const int32_t k0 = position(i);
+            char* const vtile = ktile + kTile;
+            arrived();
+            if (i + 1 < walk.total) load(i + 1, other);
 #pragma unroll
             for (int b = 0; b < NK; ++b) {
                 const int32_t bk0 = k0 + b * 32;
@@ -175,9 +144,9 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
                     dp[x] = -delta;
                 }
 #pragma unroll
-                for (int ks = 0; ks < DP / 16; ++ks) s = mfma<T>(along<DP>(ktile, b * 32 + col, half, ks), q[ks], s);
+                for (int ks = 0; ks < DP / 16; ++ks) s = mfma<T>(along<DP>(ktile, b * 32, ks), q[ks], s);
 #pragma unroll
-                for (int ks = 0; ks < DP / 16; ++ks) dp = mfma<T>(along<DP>(vtile, b * 32 + col, half, ks), go[ks], dp);
+                for (int ks = 0; ks < DP / 16; ++ks) dp = mfma<T>(along<DP>(vtile, b * 32, ks), go[ks], dp);
 #pragma unroll
                 for (int x = 0; x < 16; ++x) dp[x] *= __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], a.scale2, -lse2));
                 if (masked) {
@@ -191,13 +160,16 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
 #pragma unroll
                     for (int t = 0; t < 2; ++t) dq[db] = mfma<T>(transposed<DP>(ktile, b * 32, t, db), ds[t], dq[db]);
             }
+            char* const t = ktile;
+            ktile = other;
+            other = t;
         }
     }
     if (in) store_row<T, DP>(a.dq, place.at, g.D, dq, a.scale, live);
 }
 
 // dk and dv.  A wave has 32 keys as columns of its matrix tiles and walks the
-// rows that see one of the workgroup's 128 keys in tiles of 32: scores and
+// rows that see one of the workgroup's 128 keys in tiles of 64: scores and
 // dout v^T come as rows x keys, and P and dS go on from their registers to the
 // products with dout and q.  The first tiles of keys, which see all rows (sinks),
 // or all tiles of a small call, are walked in `splits` parts by workgroups of
@@ -205,12 +177,10 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
 template <class T, int DP>
 __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(AttnGradArgs a)
 {
-    constexpr int ROWS = 32;
-    constexpr uint32_t kTile = ROWS * row_stride<DP>();
-    __shared__ __attribute__((aligned(16))) char lds[2 * kTile];
-    __shared__ __attribute__((aligned(16))) float stat[2 * ROWS];
-    char* const qtile = lds;
-    char* const gtile = lds + kTile;
+    constexpr int ROWS = kAttnGradRows;
+    constexpr uint32_t kTile = ROWS * kRow<DP>;
+    __shared__ __attribute__((aligned(1024))) char lds[4 * kTile];           // two buffers of q and dout
+    __shared__ __attribute__((aligned(16))) float stats[2 * 2 * ROWS];       // ... of lse and -delta
     const AttnGeom& g = a.g;
     const uint32_t item = attn_item(g, (blockIdx.y << kAttnGridLog) + blockIdx.x);
     if (item >= g.items) return;
@@ -236,73 +206,96 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(Attn
         const RowWalk walk = row_walk(g, seers_of(g.win, static_cast<int32_t>(first), end, seq.end), ROWS);
         const uint32_t from = split_at(walk.total, at.parts, at.at.split), upto = split_at(walk.total, at.parts, at.at.split + 1);
         const uint32_t live_rows = static_cast<uint32_t>(seq.last) * g.group;
-        PairLoads<DP, ROWS> loads;
-        float next_stat = 0.f;
-        const auto load = [&](uint32_t i) {
-            const uint32_t r0 = (walk.from + i) * ROWS;
-            loads.load(a.q, a.dout, g.D, [&](uint32_t r) {
-                return r0 + r < live_rows ? row_place(g, at.at, r0 + r).at : int64_t(-1);
-            });
+        typedef TileLoads<DP, ROWS> Loads;
+        uint32_t bytes[Loads::N];
+#pragma unroll
+        for (int n = 0; n < Loads::N; ++n) bytes[n] = Loads::bytes(n, wave, g.D);
+        const uint32_t token_bytes = g.hl * g.D * 2, head_bytes = g.D * 2;
+        const auto load = [&](uint32_t i, char* tile, float* stat) {
+            const uint32_t r0 = (walk.from + i) * ROWS, t0 = fdiv(r0, g.d_group);
+            const int64_t start = row_place(g, at.at, t0 * g.group).at * 2;
+            const u32x4v q = descriptor(static_cast<const char*>(a.q) + start, kNowhere),
+                         go = descriptor(static_cast<const char*>(a.dout) + start, kNowhere);
+#pragma unroll
+            for (int n = 0; n < Loads::N; ++n) {
+                if (!Loads::has(n, wave)) continue;
+                const uint32_t r = r0 + Loads::row(n, wave), t = fdiv(r, g.d_group);
+                const uint32_t off = (t - t0) * token_bytes + (r - t * g.group) * head_bytes + bytes[n];
+                const uint32_t from_row = bytes[n] == kNowhere || r >= live_rows ? kNowhere : off;
+                char* const to_lds = tile + (n * 4 + wave) * 1024;
+                load_to_lds(q, from_row, to_lds);
+                load_to_lds(go, from_row, to_lds + kTile);
+            }
             if (threadIdx.x < 2 * ROWS) {
                 const uint32_t r = r0 + (threadIdx.x & (ROWS - 1));
                 const bool is_lse = threadIdx.x < ROWS;
-                next_stat = is_lse ? __builtin_inff() : 0.f;
+                float x = is_lse ? __builtin_inff() : 0.f;
                 if (r < live_rows)
-                    next_stat = is_lse ? lse2_of(a.lse[row_place(g, at.at, r).stat])
-                                       : -a.delta[static_cast<int64_t>(at.at.unit) * g.rows + r];
+                    x = is_lse ? lse2_of(a.lse[row_place(g, at.at, r).stat])
+                               : -a.delta[static_cast<int64_t>(at.at.unit) * g.rows + r];
+                stat[threadIdx.x] = x;
             }
         };
-        if (from < upto) load(from);
+        char *tile = lds, *other = lds + 2 * kTile;
+        float *stat = stats, *other_stat = stats + 2 * ROWS;
+        if (from < upto) load(from, tile, stat);
         for (uint32_t i = from; i < upto; ++i) {
-            const uint32_t r0 = (walk.from + i) * ROWS;
-            __syncthreads();                                     // the last tile has been read
-            loads.store(qtile, gtile);
-            if (threadIdx.x < 2 * ROWS) stat[threadIdx.x] = next_stat;
-            if (i + 1 < upto) load(i + 1);
-            __syncthreads();
-            const bool none = r0 + ROWS <= ra || r0 >= rb, all = ra <= r0 && r0 + ROWS <= rb;
-            if (__builtin_amdgcn_ballot_w64(live && !none) == 0) continue;
-            const bool masked = __builtin_amdgcn_ballot_w64(live && !all) != 0;
-            f32x16v s, dp;
+            const char *qtile = tile, *gtile = tile + kTile;
+            arrived();
+            if (i + 1 < upto) load(i + 1, other, other_stat);
+#pragma unroll 1
+            for (uint32_t half_tile = 0; half_tile < ROWS / 32; ++half_tile) {
+                const uint32_t row0 = half_tile * 32, r0 = (walk.from + i) * ROWS + row0;
+                const bool none = r0 + 32 <= ra || r0 >= rb, all = ra <= r0 && r0 + 32 <= rb;
+                if (__builtin_amdgcn_ballot_w64(live && !none) == 0) continue;
+                const bool masked = __builtin_amdgcn_ballot_w64(live && !all) != 0;
+                f32x16v s, dp;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const f32x4v d = *reinterpret_cast<const f32x4v*>(stat + ROWS + b * 8 + half * 4);
+                for (int b = 0; b < 4; ++b) {
+                    const f32x4v d = *reinterpret_cast<const f32x4v*>(stat + ROWS + row0 + b * 8 + half * 4);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    s[4 * b + x] = 0.f;
-                    dp[4 * b + x] = d[x];
+                    for (int x = 0; x < 4; ++x) {
+                        s[4 * b + x] = 0.f;
+                        dp[4 * b + x] = d[x];
+                    }
                 }
-            }
 #pragma unroll
-            for (int ks = 0; ks < DP / 16; ++ks) s = mfma<T>(along<DP>(qtile, col, half, ks), k[ks], s);
+                for (int ks = 0; ks < DP / 16; ++ks) s = mfma<T>(along<DP>(qtile, row0, ks), k[ks], s);
 #pragma unroll
-            for (int ks = 0; ks < DP / 16; ++ks) dp = mfma<T>(along<DP>(gtile, col, half, ks), v[ks], dp);
+                for (int ks = 0; ks < DP / 16; ++ks) dp = mfma<T>(along<DP>(gtile, row0, ks), v[ks], dp);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const f32x4v l = *reinterpret_cast<const f32x4v*>(stat + b * 8 + half * 4);
+                for (int b = 0; b < 4; ++b) {
+                    const f32x4v l = *reinterpret_cast<const f32x4v*>(stat + row0 + b * 8 + half * 4);
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    s[4 * b + x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * b + x], a.scale2, -l[x]));
-            }
-            if (masked) {
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const uint32_t r = r0 + (x / 4) * 8 + half * 4 + x % 4;
-                    if (!(r >= ra && r < rb)) s[x] = dp[x] = 0.f;
+                    for (int x = 0; x < 4; ++x)
+                        s[4 * b + x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * b + x], a.scale2, -l[x]));
                 }
+                if (masked) {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const uint32_t r = r0 + (x / 4) * 8 + half * 4 + x % 4;
+                        if (!(r >= ra && r < rb)) s[x] = dp[x] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 16; ++x) dp[x] *= s[x];
+                const u32x4v p[2] = {operand_of<T>(s, 0), operand_of<T>(s, 1)};
+                const u32x4v ds[2] = {operand_of<T>(dp, 0), operand_of<T>(dp, 1)};
+#pragma unroll
+                for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) dv[db] = mfma<T>(transposed<DP>(gtile, row0, t, db), p[t], dv[db]);
+#pragma unroll
+                for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) dk[db] = mfma<T>(transposed<DP>(qtile, row0, t, db), ds[t], dk[db]);
             }
-#pragma unroll
-            for (int x = 0; x < 16; ++x) dp[x] *= s[x];
-            const u32x4v p[2] = {operand_of<T>(s, 0), operand_of<T>(s, 1)};
-            const u32x4v ds[2] = {operand_of<T>(dp, 0), operand_of<T>(dp, 1)};
-#pragma unroll
-            for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) dv[db] = mfma<T>(transposed<DP>(gtile, 0, t, db), p[t], dv[db]);
-#pragma unroll
-            for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) dk[db] = mfma<T>(transposed<DP>(qtile, 0, t, db), ds[t], dk[db]);
+            char* const t = tile;
+            tile = other;
+            other = t;
+            float* const u = stat;
+            stat = other_stat;
+            other_stat = u;
         }
     }
     if (!in) return;

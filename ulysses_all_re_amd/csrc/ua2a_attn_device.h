@@ -58,38 +58,116 @@ __device__ __forceinline__ float other_half(float x)
     return __shfl_xor(x, 32);
 }
 
-// A tile of rows in LDS: 16-byte chunks of a row side by side, rows a chunk
-// more than their values apart, so that eight lanes' chunks of eight rows lie
-// in different banks.
+// A tile of rows in LDS, DP values each, in chunks of 16 bytes.  Row r keeps its
+// chunk c in place c ^ f(r), so that what lanes read together lies in different
+// banks: eight rows' chunks of one place (`along`), and four rows' pairs of
+// neighbouring chunks (`transposed`).  Offsets in bytes; f does not change with
+// multiples of 16 rows, and xor takes the depth step apart from the lane's part.
 template <int DP>
-constexpr int row_stride()
+constexpr uint32_t kRow = DP * 2;
+template <int DP>
+__device__ __forceinline__ uint32_t swizzle(uint32_t row)
 {
-    return DP * 2 + 16;                      // bytes
+    if constexpr (DP % 64 == 0)
+        return ((row & 3) << 1 | (row >> 2 & 1) | (DP == 128 ? row & 8 : 0)) << 4;
+    else
+        return (row >> 1 & 3) << 4;
+}
+// Where chunk c (a multiple of 16 bytes along the row) of a row is kept.
+template <int DP>
+__device__ __forceinline__ uint32_t place_of(uint32_t row, uint32_t bytes)
+{
+    return row * kRow<DP> + (bytes ^ swizzle<DP>(row));
 }
 
-// A's operand with a row of the tile per lane: row `row`, depth step ks along the row.
+// A's operand with a row of the tile per lane: rows row0 .. + 31 (row0 a multiple
+// of 32), depth step ks along the row.
 template <int DP>
-__device__ __forceinline__ u32x4v along(const char* tile, uint32_t row, uint32_t half, int ks)
+__device__ __forceinline__ u32x4v along(const char* tile, uint32_t row0, int ks)
 {
-    return *reinterpret_cast<const u32x4v*>(tile + row * row_stride<DP>() + ks * 32 + half * 16);
+    constexpr uint32_t kMask = DP % 64 == 0 ? ~0u : 63u;
+    const uint32_t lane = threadIdx.x & 63;
+    const uint32_t mine = place_of<DP>(lane & 31, (lane >> 5) * 16);
+    return *reinterpret_cast<const u32x4v*>(tile + row0 * kRow<DP> + (ks * 32 & ~kMask) + (mine ^ (ks * 32 & kMask)));
 }
 
 // A's operand with a column of the tile per lane, the depth along the rows in
-// the order above: rows row0 + 16s .. + 15, columns 32 * db ...
+// the order above: rows row0 + 16s .. + 15 (row0 a multiple of 16), columns 32 * db ...
 // ds_read_b64_tr_b16 hands lane i of 16 lanes value i of the four rows whose
 // 32 bytes their addresses name, four lanes a row.
 template <int DP>
 __device__ __forceinline__ u32x4v transposed(const char* tile, uint32_t row0, int s, int db)
 {
     const uint32_t lane = threadIdx.x & 63;
-    const uint32_t at = (row0 + (lane >> 5) * 4 + ((lane & 15) >> 2)) * row_stride<DP>() + ((lane >> 4) & 1) * 32 +
-                        (lane & 3) * 8 + s * (16 * row_stride<DP>()) + db * 64;
+    const uint32_t row = (lane >> 5) * 4 + ((lane & 15) >> 2);
+    const uint32_t mine = place_of<DP>(row, (lane >> 4 & 1) * 32 + (lane >> 1 & 1) * 16) + (lane & 1) * 8;
+    uint32_t at = mine + db * 64;
+    if constexpr (DP % 64 == 0) at = mine ^ (db * 64);
     typedef __attribute__((address_space(3))) s16x4v lds4;
-    const char* p = tile + at;
-    const s16x4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(const_cast<char*>(p)));
-    const s16x4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(const_cast<char*>(p + 8 * row_stride<DP>())));
+    char* const p = const_cast<char*>(tile) + (row0 + 16 * s) * kRow<DP>;
+    const s16x4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + at));
+    const s16x4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 8 * kRow<DP> + (DP == 128 ? at ^ 128u : at)));
     const u32x2v x = __builtin_bit_cast(u32x2v, a), y = __builtin_bit_cast(u32x2v, b);
     return u32x4v{x[0], x[1], y[0], y[1]};
+}
+
+// A tile of ROWS rows from memory straight into LDS: a wave's load moves 64
+// chunks, 16 bytes a lane, to consecutive places; lanes fetch the chunks that
+// belong there.  Reads past the descriptor's bytes give zeros: rows that do not
+// exist, and chunks past D (kNowhere).  The loads are outstanding until
+// `arrived`, which the compiler does not know: nothing may read the tile before.
+constexpr uint32_t kNowhere = 0x80000000u;
+
+template <int DP, int ROWS>
+struct TileLoads {
+    static constexpr int kAcross = DP / 8;
+    static constexpr int kTotal = ROWS * kAcross / 64;           // loads of all waves
+    static constexpr int N = (kTotal + 3) / 4;
+    static constexpr uint32_t kBytes = ROWS * DP * 2;
+
+    // the tile's row of this lane's load n, and which bytes of it
+    __device__ __forceinline__ static uint32_t row(int n, uint32_t wave)
+    {
+        return ((n * 4 + wave) * 64 + (threadIdx.x & 63)) / kAcross;
+    }
+    __device__ __forceinline__ static uint32_t bytes(int n, uint32_t wave, uint32_t D)
+    {
+        const uint32_t r = row(n, wave), place = ((n * 4 + wave) * 64 + (threadIdx.x & 63)) % kAcross;
+        const uint32_t at = (place * 16) ^ swizzle<DP>(r);
+        return at < D * 2 ? at : kNowhere;
+    }
+    // uniform: whether the wave has a load n
+    __device__ __forceinline__ static bool has(int n, uint32_t wave) { return n * 4 + 3 < kTotal || n * 4 + wave < kTotal; }
+};
+
+// What a descriptor's reads start from and how many bytes there are (uniform).
+__device__ __forceinline__ u32x4v descriptor(const void* base, uint32_t bytes)
+{
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    return u32x4v{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b))),
+                  static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32) & 0xffffu)),
+                  static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
+}
+
+// One load of a wave: 16 bytes from `offset` of each lane to consecutive places
+// from `to` on.  The destination comes in m0, which is put back.
+__device__ __forceinline__ void load_to_lds(u32x4v from, uint32_t offset, const char* to)
+{
+    typedef __attribute__((address_space(3))) const char lds;
+    const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds*)to)));
+    uint32_t m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0)
+                 : "s"(at), "v"(offset), "s"(from)
+                 : "memory");
+}
+
+// This wave's loads have arrived; after the barrier everyone's have, and what
+// was read before it may be overwritten.
+__device__ __forceinline__ void arrived()
+{
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
 }
 
 // B's operands of a row per lane, straight from memory: chunk ks * 2 + half.

@@ -13,88 +13,71 @@
 namespace ua2a {
 namespace {
 
-// The rows of keys and values of a tile on their way from memory to LDS: CH
-// chunks of eight values per lane of each.
-template <class T, int DP, int KEYS, bool CODES>
-struct KeyLoads {
-    static constexpr int kAcross = DP / 8;                       // chunks of a row
-    static constexpr int CH = KEYS * kAcross / kAttnBlock;
-    u32x4v k[CODES ? 1 : CH], v[CODES ? 1 : CH];
-    u32x2v kc[CODES ? CH : 1], vc[CODES ? CH : 1];
-    uint32_t ks[CODES ? CH : 1], vs[CODES ? CH : 1];
+// Infinities and NaN of a tile's values become zeros, and a bit each in `wild`
+// ([row][2][DP / 8] bytes: +inf or NaN, -inf or NaN).  Returns whether this chunk
+// had any.
+template <class T, int DP>
+__device__ __forceinline__ bool tame(u32x4v& v, uint8_t* wild, uint32_t row, uint32_t chunk)
+{
+    const bool mine = unbounded<T>(v);
+    uint32_t up = 0, down = 0;
+    if (mine) {
+        up = unbounded_bits<T>(v, 0);
+        down = unbounded_bits<T>(v, 0x8000u);
+        v = finite_part<T>(v);
+    }
+    uint8_t* bits = wild + row * (DP / 4) + chunk;
+    bits[0] = static_cast<uint8_t>(up);
+    bits[DP / 8] = static_cast<uint8_t>(down);
+    return mine;
+}
 
-    // base: the sequence's position 0 of this key head.  Positions at or past
-    // `end`, and values past D, are zeros.
-    __device__ __forceinline__ void load(const AttnArgs& a, const char* kbase, const char* vbase, const uint8_t* kscale,
-                                         const uint8_t* vscale, int32_t k0)
+// The keys and values of a tile of a cache on their way to LDS: CH chunks of
+// eight codes per lane of each, decoded when they are stored.
+template <class T, int DP, int KEYS>
+struct CodeLoads {
+    static constexpr int kAcross = DP / 8;                       // chunks of a row
+    static constexpr int CH = KEYS * kAcross / static_cast<int>(kAttnBlock);
+    u32x2v k[CH], v[CH];
+    uint32_t ks[CH], vs[CH];
+
+    // from the sequence's position 0 of this key head; positions at or past
+    // `end`, and values past D, are zeros
+    __device__ __forceinline__ void load(const AttnArgs& a, const uint8_t* codes, const uint8_t* scales, int32_t k0,
+                                         int32_t end)
     {
         const AttnGeom& g = a.g;
-        const int64_t row_values = static_cast<int64_t>(g.kvl) * g.D;
-        const int64_t row_scales = static_cast<int64_t>(g.kvl) * g.nb;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const uint32_t i = threadIdx.x + c * kAttnBlock;
             const uint32_t row = i / kAcross, d = i % kAcross * 8;
-            const bool ok = static_cast<int32_t>(k0 + row) < end && d < g.D;
-            const int64_t at = (k0 + static_cast<int64_t>(row)) * row_values + d;
-            if constexpr (CODES) {
-                kc[c] = vc[c] = u32x2v{0, 0};
-                ks[c] = vs[c] = 0;
-                if (ok) {
-                    const int64_t sat = (k0 + static_cast<int64_t>(row)) * row_scales + d / kBlockValues;
-                    kc[c] = *reinterpret_cast<const u32x2v*>(kbase + at);
-                    vc[c] = *reinterpret_cast<const u32x2v*>(vbase + at);
-                    ks[c] = kscale[sat];
-                    vs[c] = vscale[sat];
-                }
-            } else {
-                k[c] = v[c] = u32x4v{0, 0, 0, 0};
-                if (ok) {
-                    k[c] = *reinterpret_cast<const u32x4v*>(kbase + at * 2);
-                    v[c] = *reinterpret_cast<const u32x4v*>(vbase + at * 2);
-                }
-            }
+            k[c] = v[c] = u32x2v{0, 0};
+            ks[c] = vs[c] = 0;
+            if (static_cast<int32_t>(k0 + row) >= end || d >= g.D) continue;
+            const int64_t j = (k0 + static_cast<int64_t>(row)) * g.kvl;
+            const uint8_t* at = codes + j * g.D + d;
+            const uint8_t* sat = scales + j * g.nb + d / kBlockValues;
+            k[c] = *reinterpret_cast<const u32x2v*>(at);
+            v[c] = *reinterpret_cast<const u32x2v*>(at + a.part);
+            ks[c] = sat[0];
+            vs[c] = sat[a.part_scales];
         }
     }
-
-    // Into LDS.  look: values' infinities and NaN become zeros there, and a bit
-    // each in `wild` ([row][2][DP / 8] bytes: +inf or NaN, -inf or NaN); returns
-    // whether this lane had any.
-    __device__ __forceinline__ bool store(char* ktile, char* vtile, uint8_t* wild, int32_t format, bool look)
+    // Returns whether this lane's values had an infinity or NaN (where `look`).
+    __device__ __forceinline__ bool store(char* ktile, char* vtile, uint8_t* wild, int32_t format, bool look) const
     {
         bool odd = false;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const uint32_t i = threadIdx.x + c * kAttnBlock;
-            const uint32_t at = i / kAcross * row_stride<DP>() + i % kAcross * 16;
-            u32x4v kk, vv;
-            if constexpr (CODES) {
-                kk = decode_raw<T, 8>(kc[c], ks[c], format);
-                vv = decode_raw<T, 8>(vc[c], vs[c], format);
-            } else {
-                kk = k[c];
-                vv = v[c];
-            }
-            *reinterpret_cast<u32x4v*>(ktile + at) = kk;
-            if (look) {
-                const bool mine = unbounded<T>(vv);
-                uint32_t up = 0, down = 0;
-                if (mine) {
-                    up = unbounded_bits<T>(vv, 0);
-                    down = unbounded_bits<T>(vv, 0x8000u);
-                    vv = finite_part<T>(vv);
-                }
-                uint8_t* bits = wild + i / kAcross * (2 * kAcross) + i % kAcross;
-                bits[0] = static_cast<uint8_t>(up);
-                bits[kAcross] = static_cast<uint8_t>(down);
-                odd = odd || mine;
-            }
-            *reinterpret_cast<u32x4v*>(vtile + at) = vv;
+            const uint32_t i = threadIdx.x + c * kAttnBlock, row = i / kAcross, chunk = i % kAcross;
+            const uint32_t at = place_of<DP>(row, chunk * 16);
+            *reinterpret_cast<u32x4v*>(ktile + at) = decode_raw<T, 8>(k[c], ks[c], format);
+            u32x4v x = decode_raw<T, 8>(v[c], vs[c], format);
+            if (look) odd |= tame<T, DP>(x, wild, row, chunk);
+            *reinterpret_cast<u32x4v*>(vtile + at) = x;
         }
         return odd;
     }
-
-    int32_t end;
 };
 
 // The running softmax of a wave's 32 rows and their sums over the values.
@@ -130,7 +113,7 @@ __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16
                                        const uint8_t* wild, uint32_t row0, int32_t k0, const Seen& seen, float scale2,
                                        bool masked, bool odd)
 {
-    const uint32_t lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
+    const uint32_t half = (threadIdx.x & 63) >> 5;
     f32x16v s[NK];
 #pragma unroll
     for (int b = 0; b < NK; ++b) {
@@ -138,7 +121,7 @@ __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16
         for (int i = 0; i < 16; ++i) s[b][i] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < DP / 16; ++ks)
-            s[b] = mfma<T>(along<DP>(ktile, row0 + b * 32 + col, half, ks), q[ks], s[b]);
+            s[b] = mfma<T>(along<DP>(ktile, row0 + b * 32, ks), q[ks], s[b]);
     }
     const auto key = [&](int b, int i) {
         return k0 + static_cast<int32_t>(b * 32 + (i / 4) * 8 + half * 4 + i % 4);
@@ -220,13 +203,14 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
 {
     constexpr int KEYS = SHARED ? kAttnSplitKeys : kAttnKeys;
     constexpr int NK = SHARED ? 1 : KEYS / 32;
-    constexpr uint32_t kTile = KEYS * row_stride<DP>();
-    __shared__ __attribute__((aligned(16))) char lds[2 * kTile];
+    constexpr uint32_t kTile = KEYS * kRow<DP>;
+    // two buffers of keys and values where loads go straight to LDS; a wave's
+    // sums (SHARED) take the place of one
+    constexpr uint32_t kBuffers = CODES || SHARED ? 1 : 2;
+    __shared__ __attribute__((aligned(1024))) char lds[kBuffers * 2 * kTile];
     __shared__ __attribute__((aligned(16))) uint8_t wild[KEYS * (DP / 4)];
     __shared__ uint32_t odd_tile;
     __shared__ float stat[SHARED ? 5 * 32 * 2 : 1];            // the waves', then joined
-    char* const ktile = lds;
-    char* const vtile = lds + kTile;
     const AttnGeom& g = a.g;
     const uint32_t item = attn_item(g, (blockIdx.y << kAttnGridLog) + blockIdx.x);
     if (item >= g.items) return;
@@ -260,36 +244,88 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
         row_operands<DP>(static_cast<const uint16_t*>(a.q) + place.at, g.D, half, live, q);
 
         const int64_t base = static_cast<int64_t>(at.seq) * g.keys * g.kvl + at.kvh;
-        const char *kbase, *vbase;
-        const uint8_t *kscale = nullptr, *vscale = nullptr;
-        if constexpr (CODES) {
-            kbase = reinterpret_cast<const char*>(a.codes + base * g.D);
-            vbase = kbase + a.part;
-            kscale = a.scales + base * g.nb;
-            vscale = kscale + a.part_scales;
-        } else {
-            kbase = static_cast<const char*>(a.k) + base * g.D * 2;
-            vbase = static_cast<const char*>(a.v) + base * g.D * 2;
-        }
-        KeyLoads<T, DP, KEYS, CODES> loads;
-        loads.end = seq.end;
-        if (from < to) loads.load(a, kbase, vbase, kscale, vscale, static_cast<int32_t>(walk_tile(walk, from) * KEYS));
         if (threadIdx.x == 0) odd_tile = ~0u;
-        for (uint32_t i = from; i < to; ++i) {
-            const int32_t k0 = static_cast<int32_t>(walk_tile(walk, i) * KEYS);
-            const bool look = !all_seen(top, bottom, k0, k0 + KEYS);
-            __syncthreads();                                     // the last tile has been read
-            if (loads.store(ktile, vtile, wild, a.format, look)) odd_tile = i;
-            if (i + 1 < to)
-                loads.load(a, kbase, vbase, kscale, vscale, static_cast<int32_t>(walk_tile(walk, i + 1) * KEYS));
-            __syncthreads();
+        const auto position = [&](uint32_t i) { return static_cast<int32_t>(walk_tile(walk, i) * KEYS); };
+        // whether some row of the workgroup does not see some key of tile i
+        const auto part_seen = [&](int32_t k0) { return !all_seen(top, bottom, k0, k0 + KEYS); };
+        const auto work = [&](uint32_t i, int32_t k0, const char* ktile, const char* vtile, bool look) {
             const uint32_t row0 = SHARED ? wave * 32 : 0;
             const int32_t wk0 = k0 + static_cast<int32_t>(row0);
-            if (!rows || none_seen(wtop, wbottom, wk0, wk0 + 32 * NK)) continue;
+            if (!rows || none_seen(wtop, wbottom, wk0, wk0 + 32 * NK)) return;
             attend<T, DP, NK>(r, q, ktile, vtile, wild, row0, wk0, seen, a.scale2,
                               !all_seen(wtop, wbottom, wk0, wk0 + 32 * NK), look && odd_tile == i);
+        };
+        if constexpr (CODES) {
+            CodeLoads<T, DP, KEYS> loads;
+            const uint8_t *codes = a.codes + base * g.D, *scales = a.scales + base * g.nb;
+            if (from < to) loads.load(a, codes, scales, position(from), seq.end);
+            for (uint32_t i = from; i < to; ++i) {
+                const int32_t k0 = position(i);
+                const bool look = part_seen(k0);
+                __syncthreads();                                 // the last tile has been read
+                if (loads.store(lds, lds + kTile, wild, a.format, look)) odd_tile = i;
+                if (i + 1 < to) loads.load(a, codes, scales, position(i + 1), seq.end);
+                __syncthreads();
+                work(i, k0, lds, lds + kTile, look);
+            }
+        } else {
+            typedef TileLoads<DP, KEYS> Loads;
+            uint32_t offset[Loads::N];
+            const uint32_t row_bytes = g.kvl * g.D * 2;
+#pragma unroll
+            for (int n = 0; n < Loads::N; ++n) {
+                const uint32_t bytes = Loads::bytes(n, wave, g.D);
+                offset[n] = bytes == kNowhere ? kNowhere : Loads::row(n, wave) * row_bytes + bytes;
+            }
+            const auto load = [&](uint32_t i, char* tile) {
+                const int32_t k0 = position(i);
+                const int64_t start = (base + static_cast<int64_t>(k0) * g.kvl) * g.D * 2;
+                const uint32_t bytes = static_cast<uint32_t>(seq.end - k0 < KEYS ? seq.end - k0 : KEYS) * row_bytes;
+                const u32x4v k = descriptor(static_cast<const char*>(a.k) + start, bytes),
+                             v = descriptor(static_cast<const char*>(a.v) + start, bytes);
+#pragma unroll
+                for (int n = 0; n < Loads::N; ++n) {
+                    if (!Loads::has(n, wave)) continue;
+                    char* const to_lds = tile + (n * 4 + wave) * 1024;
+                    load_to_lds(k, offset[n], to_lds);
+                    load_to_lds(v, offset[n], to_lds + kTile);
+                }
+            };
+            char* tile = lds;
+            char* other = lds + (kBuffers - 1) * 2 * kTile;
+            if (from < to && kBuffers == 2) load(from, tile);
+            for (uint32_t i = from; i < to; ++i) {
+                const int32_t k0 = position(i);
+                const bool look = part_seen(k0);
+                if constexpr (kBuffers == 1) {
+                    __syncthreads();                             // the last tile has been read
+                    load(i, tile);
+                }
+                arrived();
+                if (kBuffers == 2 && i + 1 < to) load(i + 1, other);
+                if (look) {
+#pragma unroll
+                    for (int n = 0; n < Loads::N; ++n) {
+                        const uint32_t x = threadIdx.x + n * kAttnBlock, row = x / (DP / 8), chunk = x % (DP / 8);
+                        char* const p = tile + kTile + place_of<DP>(row, chunk * 16);
+                        u32x4v v = *reinterpret_cast<const u32x4v*>(p);
+                        if (tame<T, DP>(v, wild, row, chunk)) {
+                            *reinterpret_cast<u32x4v*>(p) = v;
+                            odd_tile = i;
+                        }
+                    }
+                    __syncthreads();
+                }
+                work(i, k0, tile, tile + kTile, look);
+                if constexpr (kBuffers == 2) {
+                    char* const t = tile;
+                    tile = other;
+                    other = t;
+                }
+            }
         }
     }
+    __syncthreads();
     r.l += other_half(r.l);
     if constexpr (SHARED) {
         // the four waves' maxima and sums, then their values' sums, 32 rows of DP each
