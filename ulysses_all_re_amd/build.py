@@ -22,6 +22,7 @@ SOURCES = [os.path.join(CSRC, "ua2a_kernels.hip"), os.path.join(CSRC, "ua2a_host
            os.path.join(CSRC, "ua2a_act_cache.hip"), os.path.join(CSRC, "ua2a_act_launch.hip"),
            os.path.join(CSRC, "ua2a_act_host.cpp"), os.path.join(CSRC, "ua2a_rope.hip"),
            os.path.join(CSRC, "ua2a_attn_forward.hip"), os.path.join(CSRC, "ua2a_attn_backward.hip"),
+           os.path.join(CSRC, "ua2a_attn_decode.hip"),
            os.path.join(CSRC, "ua2a_attn_launch.hip"), os.path.join(CSRC, "ua2a_attn_host.cpp")]
 HEADERS = [os.path.join(INCLUDE, "ua2a.h"), os.path.join(INCLUDE, "ua2a_act.h"),
            os.path.join(CSRC, "ua2a_geometry.h"), os.path.join(CSRC, "ua2a_bodies.h"),

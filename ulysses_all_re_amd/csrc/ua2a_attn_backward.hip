@@ -171,9 +171,8 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
 // dk and dv.  A wave has 32 keys as columns of its matrix tiles and walks the
 // rows that see one of the workgroup's 128 keys in tiles of 64: scores and
 // dout v^T come as rows x keys, and P and dS go on from their registers to the
-// products with dout and q.  The first tiles of keys, which see all rows (sinks),
-// or all tiles of a small call, are walked in `splits` parts by workgroups of
-// their own, whose sums a third kernel joins in order.
+// products with dout and q.  Where a tile's walk is long for the call, workgroups of
+// their own walk parts of it, whose sums a third kernel joins in order.
 template <class T, int DP>
 __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(AttnGradArgs a)
 {
@@ -300,7 +299,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(Attn
     }
     if (!in) return;
     if (at.parts > 1) {
-        float* line = a.partial + part_line(g, a.keys, at, j) * 2 * g.D;
+        float* line = a.partial + part_line(g, a.keys, at.at.unit, at.at.split, j) * 2 * g.D;
 #pragma unroll
         for (int db = 0; db < DP / 32; ++db)
 #pragma unroll
@@ -330,16 +329,17 @@ __global__ __launch_bounds__(kAttnBlock) void ua2a_attention_keys_join_kernel(At
     const AttnGeom& g = a.g;
     const uint32_t per = g.D / 2;
     const int64_t id = static_cast<int64_t>((blockIdx.y << kAttnGridLog) + blockIdx.x) * kAttnBlock + threadIdx.x;
-    const int64_t line = id / per;                               // of unit * span + key
-    const uint32_t span = a.keys.span;
-    const int64_t lines = static_cast<int64_t>(g.units) * span;
-    if (line >= lines) return;
+    const uint32_t keys = a.keys.rest_parts > 1 ? g.keys : a.keys.span;      // of a unit that may have parts
+    const int64_t line = id / per;                               // unit * keys + key
+    if (line >= static_cast<int64_t>(g.units) * keys) return;
     const uint32_t c = static_cast<uint32_t>(id - line * per) * 4;          // of dk's and dv's D
-    const uint32_t unit = static_cast<uint32_t>(line / span), j = static_cast<uint32_t>(line - static_cast<int64_t>(unit) * span);
+    const uint32_t unit = static_cast<uint32_t>(line / keys), j = static_cast<uint32_t>(line - static_cast<int64_t>(unit) * keys);
+    const uint32_t parts = j < a.keys.span ? a.keys.lead_parts : a.keys.rest_parts;
+    if (parts <= 1) return;
     const uint32_t seq = fdiv(unit, g.d_kvl), kvh = unit - seq * g.kvl;
     f32x4v x = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t s = 0; s < g.splits; ++s)
-        x += *reinterpret_cast<const f32x4v*>(a.partial + (s * lines + line) * 2 * g.D + c);
+    for (uint32_t s = 0; s < parts; ++s)
+        x += *reinterpret_cast<const f32x4v*>(a.partial + part_line(g, a.keys, unit, s, j) * 2 * g.D + c);
     const bool is_v = c >= g.D;
     const float f = is_v ? 1.f : a.scale;
     const int64_t to = ((static_cast<int64_t>(seq) * g.keys + j) * g.kvl + kvh) * g.D + (is_v ? c - g.D : c);

@@ -149,6 +149,12 @@ __device__ __forceinline__ u32x4v descriptor(const void* base, uint32_t bytes)
                   static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(bytes)), 0x00020000u};
 }
 
+// The same for the compiler's own buffer loads.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* base, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(bytes), 0x00020000);
+}
+
 // One load of a wave: 16 bytes from `offset` of each lane to consecutive places
 // from `to` on.  The destination comes in m0, which is put back.
 __device__ __forceinline__ void load_to_lds(u32x4v from, uint32_t offset, const char* to)
@@ -243,6 +249,81 @@ __device__ __forceinline__ uint32_t unbounded_bits(u32x4v v, uint32_t sign)
         if (w == (kExp | sign) || (w & 0x7fffu) > kExp) bits |= 1u << i;
     }
     return bits;
+}
+
+// Infinities and NaN of a tile's values become zeros, and a bit each in `wild`
+// ([row][2][DP / 8] bytes: +inf or NaN, -inf or NaN).  Returns whether this chunk
+// had any.
+template <class T, int DP>
+__device__ __forceinline__ bool tame(u32x4v& v, uint8_t* wild, uint32_t row, uint32_t chunk)
+{
+    const bool mine = unbounded<T>(v);
+    uint32_t up = 0, down = 0;
+    if (mine) {
+        up = unbounded_bits<T>(v, 0);
+        down = unbounded_bits<T>(v, 0x8000u);
+        v = finite_part<T>(v);
+    }
+    uint8_t* bits = wild + row * (DP / 4) + chunk;
+    bits[0] = static_cast<uint8_t>(up);
+    bits[DP / 8] = static_cast<uint8_t>(down);
+    return mine;
+}
+
+// Eight codes in the type, code * scale rounded once, by the scaled conversions;
+// for scales at which no code passes what the type holds (decode_raw is for all).
+template <class T, bool E4M3>
+__device__ __forceinline__ u32x4v decode8(u32x2v c, uint32_t byte)
+{
+    const float s = read_scale_of(byte);
+    u32x4v r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (__is_same(T, __bf16)) {
+            if constexpr (E4M3) {
+                r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], s, false));
+                r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], s, true));
+            } else {
+                r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c[i], s, false));
+                r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c[i], s, true));
+            }
+        } else {
+            if constexpr (E4M3) {
+                r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[i], s, false));
+                r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c[i], s, true));
+            } else {
+                r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(c[i], s, false));
+                r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(c[i], s, true));
+            }
+        }
+    }
+    return r;
+}
+
+// Four values d .. of a row's sums, with its maximum and sum: the result, or a
+// part's place in the workspace.  The lane of d = 0 writes the statistics.
+template <class T>
+__device__ __forceinline__ void finish_row(const AttnArgs& a, const AttnPlace& at, const AttnSeq& seq, uint32_t row,
+                                           uint32_t d, f32x4v x, float m, float l)
+{
+    const AttnGeom& g = a.g;
+    const RowPlace pl = row_place(g, at, row);
+    const bool live = pl.t >= seq.first && pl.t < seq.last;
+    if (g.splits > 1) {
+        const int64_t line = (static_cast<int64_t>(at.split) * g.units + at.unit) * g.rows + row;
+        *reinterpret_cast<f32x4v*>(a.partial + line * g.D + d) = x;
+        if (d == 0) {
+            a.stats[line * 2] = live ? m : -__builtin_inff();
+            a.stats[line * 2 + 1] = live ? l : 0.f;
+        }
+        return;
+    }
+    if (!live && a.keep) return;
+    const float inv = live && l != 0.f ? 1.f / l : 0.f;
+    u32x2v y = {0, 0};
+    if (live) y = u32x2v{pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv)};
+    *reinterpret_cast<u32x2v*>(static_cast<uint16_t*>(a.out) + pl.at + d) = y;
+    if (d == 0 && a.lse != nullptr) a.lse[pl.stat] = live && l != 0.f ? m * kLn2 + logf(l) : -__builtin_inff();
 }
 
 }  // namespace

@@ -13,25 +13,6 @@
 namespace ua2a {
 namespace {
 
-// Infinities and NaN of a tile's values become zeros, and a bit each in `wild`
-// ([row][2][DP / 8] bytes: +inf or NaN, -inf or NaN).  Returns whether this chunk
-// had any.
-template <class T, int DP>
-__device__ __forceinline__ bool tame(u32x4v& v, uint8_t* wild, uint32_t row, uint32_t chunk)
-{
-    const bool mine = unbounded<T>(v);
-    uint32_t up = 0, down = 0;
-    if (mine) {
-        up = unbounded_bits<T>(v, 0);
-        down = unbounded_bits<T>(v, 0x8000u);
-        v = finite_part<T>(v);
-    }
-    uint8_t* bits = wild + row * (DP / 4) + chunk;
-    bits[0] = static_cast<uint8_t>(up);
-    bits[DP / 8] = static_cast<uint8_t>(down);
-    return mine;
-}
-
 // The keys and values of a tile of a cache on their way to LDS: CH chunks of
 // eight codes per lane of each, decoded when they are stored.
 template <class T, int DP, int KEYS>
@@ -41,42 +22,63 @@ struct CodeLoads {
     u32x2v k[CH], v[CH];
     uint32_t ks[CH], vs[CH];
 
-    // from the sequence's position 0 of this key head; positions at or past
-    // `end`, and values past D, are zeros
-    __device__ __forceinline__ void load(const AttnArgs& a, const uint8_t* codes, const uint8_t* scales, int32_t k0,
-                                         int32_t end)
+    __device__ __forceinline__ static uint32_t row(int c) { return (threadIdx.x + c * kAttnBlock) / kAcross; }
+    __device__ __forceinline__ static uint32_t chunk(int c) { return (threadIdx.x + c * kAttnBlock) % kAcross; }
+
+    // j0: the tile's first position of this key head, in heads of D codes.  What
+    // lies at or past `rows` positions, or past D, is zeros.
+    __device__ __forceinline__ void load(const AttnArgs& a, int64_t j0, int32_t rows)
     {
         const AttnGeom& g = a.g;
+        const uint32_t step = g.kvl * g.D, sstep = g.kvl * g.nb;
+        const uint32_t bytes = static_cast<uint32_t>(rows) * step, sbytes = static_cast<uint32_t>(rows) * sstep;
+        const auto kd = resource(a.codes + j0 * g.D, bytes), vd = resource(a.codes + a.part + j0 * g.D, bytes);
+        const auto ksd = resource(a.scales + j0 * g.nb, sbytes), vsd = resource(a.scales + a.part_scales + j0 * g.nb, sbytes);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const uint32_t i = threadIdx.x + c * kAttnBlock;
-            const uint32_t row = i / kAcross, d = i % kAcross * 8;
-            k[c] = v[c] = u32x2v{0, 0};
-            ks[c] = vs[c] = 0;
-            if (static_cast<int32_t>(k0 + row) >= end || d >= g.D) continue;
-            const int64_t j = (k0 + static_cast<int64_t>(row)) * g.kvl;
-            const uint8_t* at = codes + j * g.D + d;
-            const uint8_t* sat = scales + j * g.nb + d / kBlockValues;
-            k[c] = *reinterpret_cast<const u32x2v*>(at);
-            v[c] = *reinterpret_cast<const u32x2v*>(at + a.part);
-            ks[c] = sat[0];
-            vs[c] = sat[a.part_scales];
+            const uint32_t d = chunk(c) * 8;
+            const bool ok = d < g.D;
+            const uint32_t at = ok ? row(c) * step + d : kNowhere, sat = ok ? row(c) * sstep + d / kBlockValues : kNowhere;
+            k[c] = __builtin_bit_cast(u32x2v, __builtin_amdgcn_raw_buffer_load_b64(kd, at, 0, 0));
+            v[c] = __builtin_bit_cast(u32x2v, __builtin_amdgcn_raw_buffer_load_b64(vd, at, 0, 0));
+            ks[c] = __builtin_amdgcn_raw_buffer_load_b8(ksd, sat, 0, 0);
+            vs[c] = __builtin_amdgcn_raw_buffer_load_b8(vsd, sat, 0, 0);
         }
+    }
+    template <bool E4M3>
+    __device__ __forceinline__ bool put(char* ktile, char* vtile, uint8_t* wild, bool look) const
+    {
+        // from here on a code may pass the type's largest value
+        constexpr uint32_t kHigh = 127u + (__is_same(T, _Float16) ? 15u : 127u) - (E4M3 ? 8u : 15u) + 1u;
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) top = max(top, max(ks[c], vs[c]));
+        const bool high = __builtin_amdgcn_ballot_w64(top >= kHigh) != 0;
+        bool odd = false;
+        if (!high && !look) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const uint32_t at = place_of<DP>(row(c), chunk(c) * 16);
+                *reinterpret_cast<u32x4v*>(ktile + at) = decode8<T, E4M3>(k[c], ks[c]);
+                *reinterpret_cast<u32x4v*>(vtile + at) = decode8<T, E4M3>(v[c], vs[c]);
+            }
+            return false;
+        }
+        constexpr int32_t kFormat = E4M3 ? UA2A_FORMAT_E4M3 : UA2A_FORMAT_E5M2;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const uint32_t at = place_of<DP>(row(c), chunk(c) * 16);
+            *reinterpret_cast<u32x4v*>(ktile + at) = decode_raw<T, 8>(k[c], ks[c], kFormat);
+            u32x4v x = decode_raw<T, 8>(v[c], vs[c], kFormat);
+            if (look) odd |= tame<T, DP>(x, wild, row(c), chunk(c));
+            *reinterpret_cast<u32x4v*>(vtile + at) = x;
+        }
+        return odd;
     }
     // Returns whether this lane's values had an infinity or NaN (where `look`).
     __device__ __forceinline__ bool store(char* ktile, char* vtile, uint8_t* wild, int32_t format, bool look) const
     {
-        bool odd = false;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const uint32_t i = threadIdx.x + c * kAttnBlock, row = i / kAcross, chunk = i % kAcross;
-            const uint32_t at = place_of<DP>(row, chunk * 16);
-            *reinterpret_cast<u32x4v*>(ktile + at) = decode_raw<T, 8>(k[c], ks[c], format);
-            u32x4v x = decode_raw<T, 8>(v[c], vs[c], format);
-            if (look) odd |= tame<T, DP>(x, wild, row, chunk);
-            *reinterpret_cast<u32x4v*>(vtile + at) = x;
-        }
-        return odd;
+        return format == UA2A_FORMAT_E4M3 ? put<true>(ktile, vtile, wild, look) : put<false>(ktile, vtile, wild, look);
     }
 };
 
@@ -257,14 +259,17 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
         };
         if constexpr (CODES) {
             CodeLoads<T, DP, KEYS> loads;
-            const uint8_t *codes = a.codes + base * g.D, *scales = a.scales + base * g.nb;
-            if (from < to) loads.load(a, codes, scales, position(from), seq.end);
+            const auto load = [&](uint32_t i) {
+                const int32_t k0 = position(i);
+                loads.load(a, base + static_cast<int64_t>(k0) * g.kvl, seq.end - k0 < KEYS ? seq.end - k0 : KEYS);
+            };
+            if (from < to) load(from);
             for (uint32_t i = from; i < to; ++i) {
                 const int32_t k0 = position(i);
                 const bool look = part_seen(k0);
                 __syncthreads();                                 // the last tile has been read
                 if (loads.store(lds, lds + kTile, wild, a.format, look)) odd_tile = i;
-                if (i + 1 < to) loads.load(a, codes, scales, position(i + 1), seq.end);
+                if (i + 1 < to) load(i + 1);
                 __syncthreads();
                 work(i, k0, lds, lds + kTile, look);
             }
@@ -363,26 +368,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
             f32x4v x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < 4; ++w) x += *reinterpret_cast<const f32x4v*>(sums + (w * 32 + c) * DP + d);
-            const RowPlace pl = row_place(g, at, first + c);
-            const bool alive = pl.t >= seq.first && pl.t < seq.last;
-            const float cm = stat[(128 + c) * 2], cl = stat[(128 + c) * 2 + 1];
-            if (g.splits > 1) {
-                const int64_t line = static_cast<int64_t>(at.split) * g.units * g.rows + static_cast<int64_t>(at.unit) * g.rows +
-                                     pl.row;
-                *reinterpret_cast<f32x4v*>(a.partial + line * g.D + d) = x;
-                if (d == 0) {
-                    a.stats[line * 2] = alive ? cm : -__builtin_inff();
-                    a.stats[line * 2 + 1] = alive ? cl : 0.f;
-                }
-                continue;
-            }
-            if (!alive && a.keep) continue;
-            const float inv = alive && cl != 0.f ? 1.f / cl : 0.f;
-            u32x2v y = {0, 0};
-            if (alive) y = u32x2v{pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv)};
-            *reinterpret_cast<u32x2v*>(static_cast<uint16_t*>(a.out) + pl.at + d) = y;
-            if (d == 0 && a.lse != nullptr)
-                a.lse[pl.stat] = alive && cl != 0.f ? cm * kLn2 + logf(cl) : -__builtin_inff();
+            finish_row<T>(a, at, seq, first + c, d, x, stat[(128 + c) * 2], stat[(128 + c) * 2 + 1]);
         }
         return;
     }
@@ -421,17 +407,18 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
         a.lse[place.stat] = live && r.l != 0.f ? r.m * kLn2 + logf(r.l) : -__builtin_inff();
 }
 
-// The parts of rows whose keys were walked by several workgroups, joined: D / 4
-// lanes a row.
+// The parts of rows whose keys were walked by several workgroups, joined: a
+// workgroup a row.  D / 4 lanes (`wide`) have four values each of a part, so a
+// workgroup takes 8 to 32 parts at once, whose loads are all on their way
+// together (64 parts: 23 us with one wave a row, two parts at once).
 template <class T>
 __global__ __launch_bounds__(kAttnBlock) void ua2a_attention_join_kernel(AttnArgs a)
 {
+    __shared__ f32x4v sums[kAttnBlock];
+    __shared__ float tops[kAttnBlock], totals[kAttnBlock];
     const AttnGeom& g = a.g;
-    const uint32_t per = g.D / 4;
-    const int64_t id = static_cast<int64_t>((blockIdx.y << kAttnGridLog) + blockIdx.x) * kAttnBlock + threadIdx.x;
     const int64_t lines = static_cast<int64_t>(g.units) * g.rows;
-    const int64_t line = id / per;
-    const uint32_t d = static_cast<uint32_t>(id - line * per) * 4;
+    const int64_t line = static_cast<int64_t>((blockIdx.y << kAttnGridLog) + blockIdx.x);
     if (line >= lines) return;
     AttnPlace at;
     at.unit = static_cast<uint32_t>(line / g.rows);
@@ -443,18 +430,53 @@ __global__ __launch_bounds__(kAttnBlock) void ua2a_attention_join_kernel(AttnArg
                                  a.counts != nullptr ? static_cast<int64_t>(a.counts[at.i]) : static_cast<int64_t>(g.n));
     const bool live = pl.t >= seq.first && pl.t < seq.last;
     if (!live && a.keep) return;
+    const uint32_t wide = g.D > 64 ? 32 : g.D > 32 ? 16 : 8;
+    const uint32_t d = (threadIdx.x & (wide - 1)) * 4, mine = threadIdx.x / wide, step = kAttnBlock / wide;
     float m = -__builtin_inff(), l = 0.f;
     f32x4v x = {0.f, 0.f, 0.f, 0.f};
-    if (live) {
-        for (uint32_t s = 0; s < g.splits; ++s) m = fmaxf(m, a.stats[(s * lines + line) * 2]);
-        const float mm = m == -__builtin_inff() ? 0.f : m;
-        for (uint32_t s = 0; s < g.splits; ++s) {
-            const float sm = a.stats[(s * lines + line) * 2], sl = a.stats[(s * lines + line) * 2 + 1];
-            const float f = __builtin_amdgcn_exp2f(sm - mm);
-            const f32x4v p = *reinterpret_cast<const f32x4v*>(a.partial + (s * lines + line) * g.D + d);
-            l += sl * f;
-            x += p * f;
+    constexpr int kAtOnce = 8;
+    for (uint32_t s0 = mine; live && s0 < g.splits; s0 += step * kAtOnce) {
+        float sm[kAtOnce], sl[kAtOnce];
+        f32x4v sx[kAtOnce];
+#pragma unroll
+        for (int b = 0; b < kAtOnce; ++b) {
+            const uint32_t s = s0 + b * step;
+            sm[b] = -__builtin_inff();
+            sl[b] = 0.f;
+            sx[b] = f32x4v{0.f, 0.f, 0.f, 0.f};
+            if (s >= g.splits) continue;
+            sm[b] = a.stats[(s * lines + line) * 2];
+            sl[b] = a.stats[(s * lines + line) * 2 + 1];
+            if (d < g.D) sx[b] = *reinterpret_cast<const f32x4v*>(a.partial + (s * lines + line) * g.D + d);
         }
+        float now = m;
+#pragma unroll
+        for (int b = 0; b < kAtOnce; ++b) now = fmaxf(now, sm[b]);
+        const float mm = now == -__builtin_inff() ? 0.f : now;
+        const float f = __builtin_amdgcn_exp2f(m - mm);
+        l *= f;
+        x *= f;
+#pragma unroll
+        for (int b = 0; b < kAtOnce; ++b) {
+            const float w = __builtin_amdgcn_exp2f(sm[b] - mm);
+            l += sl[b] * w;
+            x += sx[b] * w;
+        }
+        m = now;
+    }
+    sums[threadIdx.x] = x;
+    tops[threadIdx.x] = m;
+    totals[threadIdx.x] = l;
+    __syncthreads();
+    if (mine != 0 || d >= g.D) return;
+    for (uint32_t b = 0; b < step; ++b) m = fmaxf(m, tops[b * wide + threadIdx.x]);
+    const float mm = m == -__builtin_inff() ? 0.f : m;
+    x = f32x4v{0.f, 0.f, 0.f, 0.f};
+    l = 0.f;
+    for (uint32_t b = 0; b < step; ++b) {
+        const float w = __builtin_amdgcn_exp2f(tops[b * wide + threadIdx.x] - mm);
+        l += totals[b * wide + threadIdx.x] * w;
+        x += sums[b * wide + threadIdx.x] * w;
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
     u32x2v y = {0, 0};

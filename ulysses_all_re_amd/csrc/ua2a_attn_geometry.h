@@ -195,13 +195,15 @@ UA2A_HD bool none_seen(const Seen& a, const Seen& b, int32_t k0, int32_t k1)
 }
 
 // ------------------------------------------------------------- keys' gradients
-// A unit's tiles of keys: the first `lead` are walked in g.splits parts each,
-// the others by one workgroup.
+// A unit's tiles of keys: the first `lead` (span keys) are walked in lead_parts
+// parts each, the others in rest_parts.  Parts' sums lie in the workspace, the
+// lead tiles' first, [parts][units][keys] each.
 struct KeyTiles {
-    uint32_t lead;
-    uint32_t span;               // keys of the lead tiles
-    uint32_t per_unit;           // lead * splits + (tiles - lead)
-    Div32 d_per_unit;
+    uint32_t lead, span;
+    uint32_t lead_parts, rest_parts;
+    uint32_t per_unit;           // lead * lead_parts + (tiles - lead) * rest_parts
+    Div32 d_per_unit, d_lead_parts, d_rest_parts;
+    int64_t rest_line;           // where the other tiles' sums start, in keys
 };
 
 struct KeyPlace {
@@ -213,15 +215,18 @@ UA2A_HD KeyPlace key_place(const AttnGeom& g, const KeyTiles& t, uint32_t item)
 {
     KeyPlace p;
     p.at.unit = fdiv(item, t.d_per_unit);
-    const uint32_t i = item - p.at.unit * t.per_unit, parted = t.lead * g.splits;
-    if (i < parted) {
-        p.at.tile = fdiv(i, g.d_splits);
-        p.at.split = i - p.at.tile * g.splits;
-        p.parts = g.splits;
+    uint32_t i = item - p.at.unit * t.per_unit;
+    const uint32_t leading = t.lead * t.lead_parts;
+    if (i < leading) {
+        p.at.tile = fdiv(i, t.d_lead_parts);
+        p.at.split = i - p.at.tile * t.lead_parts;
+        p.parts = t.lead_parts;
     } else {
-        p.at.tile = t.lead + (i - parted);
-        p.at.split = 0;
-        p.parts = 1;
+        i -= leading;
+        const uint32_t tile = fdiv(i, t.d_rest_parts);
+        p.at.split = i - tile * t.rest_parts;
+        p.at.tile = t.lead + tile;
+        p.parts = t.rest_parts;
     }
     p.at.seq = fdiv(p.at.unit, g.d_kvl);
     p.at.kvh = p.at.unit - p.at.seq * g.kvl;
@@ -229,10 +234,11 @@ UA2A_HD KeyPlace key_place(const AttnGeom& g, const KeyTiles& t, uint32_t item)
     return p;
 }
 
-// Where a part's sums of key j go, in lines of dk's and dv's values.
-UA2A_HD int64_t part_line(const AttnGeom& g, const KeyTiles& t, const KeyPlace& p, uint32_t j)
+// Where part `split` of key j keeps its sums, in keys of dk's and dv's values.
+UA2A_HD int64_t part_line(const AttnGeom& g, const KeyTiles& t, uint32_t unit, uint32_t split, uint32_t j)
 {
-    return (static_cast<int64_t>(p.at.split) * g.units + p.at.unit) * t.span + j;
+    const int64_t of = static_cast<int64_t>(split) * g.units + unit;
+    return j < t.span ? of * t.span + j : t.rest_line + of * (g.keys - t.span) + (j - t.span);
 }
 
 // The tiles of `size` rows that hold the rows of tokens [first, last).

@@ -132,13 +132,14 @@ int launch_forward(ua2a_plan_t plan, AttnLaunch* L, void* workspace, void* strea
         L->attn.partial = static_cast<float*>(workspace);
         L->attn.stats = L->attn.partial + int64_t(g.splits) * g.units * g.rows * g.D;
     }
-    L->kernel = AttnKernel::Forward;
+    // up to 16 rows of a cache have a kernel of their own
+    L->kernel = L->attn.codes != nullptr && g.rows <= kDecodeRows ? AttnKernel::Decode : AttnKernel::Forward;
     attn_grid(workgroups(g), L);
     int err = attn_launch(*L, stream);
     if (err != 0) return fail(plan, "launching the attention kernel", err);
     if (g.splits == 1) return UA2A_OK;
     L->kernel = AttnKernel::Join;
-    attn_grid(ceil_div(int64_t(g.units) * g.rows * (g.D / 4), kAttnBlock), L);
+    attn_grid(int64_t(g.units) * g.rows, L);
     err = attn_launch(*L, stream);
     return err == 0 ? UA2A_OK : fail(plan, "launching the join of attention's parts", err);
 }
@@ -180,36 +181,48 @@ int64_t most_seers(const AttnGeom& g)
 }
 
 // How the keys' gradients go to workgroups.  Sinks are seen by all rows, other
-// keys by a window of them: tiles of sinks are walked in as many parts as makes
-// a part about a window's walk, eight at most (their sums lie in the workspace).
-// With fewer tiles than workgroups that the device holds at once, every tile is
-// walked in parts of 256 rows at least.
+// keys by a window of them, so a tile of sinks would be walked long after the
+// rest: tiles are walked in parts of about a window, and of less where the call
+// is small: as much as leaves two parts for each workgroup that the device
+// holds at once (512), but 512 rows at least, for a part's sums go through the
+// workspace (no more than 64 parts of a tile, and 256 MiB).
 void backward_shape(AttnGradArgs* a)
 {
     AttnGeom& g = a->g;
-    const int64_t tiles = ceil_div(g.keys, kAttnGradKeys), all = int64_t(g.units) * tiles, most = most_seers(g);
-    int64_t lead = 0, splits = 1;
-    if (all < 512) {
-        splits = ceil_div(512, all);
-        if (splits > most / 256) splits = most / 256;
-        lead = tiles;
+    KeyTiles& t = a->keys;
+    const int64_t tiles = ceil_div(g.keys, kAttnGradKeys), most = most_seers(g);
+    const int64_t sinks = g.win.sinks < static_cast<int64_t>(g.keys) ? g.win.sinks : g.keys;
+    const int64_t lead = most < g.rows ? ceil_div(sinks, kAttnGradKeys) : 0;
+    const int64_t span = lead * kAttnGradKeys < g.keys ? lead * kAttnGradKeys : g.keys;
+    const int64_t all = g.units * (lead * g.rows + (tiles - lead) * most);
+    int64_t part = all / 1024 < most ? all / 1024 : most;
+    if (part < 512) part = 512;
+    int64_t first, rest;
+    for (;; part *= 2) {
+        first = ceil_div(g.rows, part);
+        rest = ceil_div(most, part);
+        first = lead == 0 ? 1 : first > 64 ? 64 : first;
+        rest = rest > 64 ? 64 : rest;
+        const int64_t lines = (first > 1 ? first * span : 0) + (rest > 1 ? rest * (g.keys - span) : 0);
+        if (lines * g.units * g.D * 8 <= (int64_t(256) << 20)) break;
     }
-    if (splits <= 1 && g.win.sinks > 0 && most < g.rows) {
-        splits = (g.rows + most / 2) / most;
-        const int64_t sinks = g.win.sinks < g.keys ? g.win.sinks : g.keys;
-        lead = ceil_div(sinks, kAttnGradKeys);
-    }
-    if (splits > 8) splits = 8;
-    if (splits <= 1) {
-        splits = 1;
-        lead = 0;
-    }
-    set_items(&g, tiles, splits);
-    a->keys.lead = static_cast<uint32_t>(lead);
-    a->keys.span = lead * kAttnGradKeys < g.keys ? static_cast<uint32_t>(lead * kAttnGradKeys) : g.keys;
-    a->keys.per_unit = static_cast<uint32_t>(lead * splits + tiles - lead);
-    a->keys.d_per_unit = make_div32(a->keys.per_unit);
-    g.items = g.units * a->keys.per_unit;
+    set_items(&g, tiles, 1);
+    t.lead = static_cast<uint32_t>(lead);
+    t.span = static_cast<uint32_t>(span);
+    t.lead_parts = static_cast<uint32_t>(first);
+    t.rest_parts = static_cast<uint32_t>(rest);
+    t.per_unit = static_cast<uint32_t>(lead * first + (tiles - lead) * rest);
+    t.d_per_unit = make_div32(t.per_unit);
+    t.d_lead_parts = make_div32(t.lead_parts);
+    t.d_rest_parts = make_div32(t.rest_parts);
+    t.rest_line = first > 1 ? first * g.units * span : 0;
+    g.items = g.units * t.per_unit;
+}
+
+int64_t part_lines(const AttnGradArgs& a)
+{
+    const KeyTiles& t = a.keys;
+    return t.rest_line + (t.rest_parts > 1 ? int64_t(t.rest_parts) * a.g.units * (a.g.keys - t.span) : 0);
 }
 
 // delta's place, whole lines of 16 bytes
@@ -217,9 +230,7 @@ int64_t delta_floats(const AttnGeom& g) { return ceil_div(int64_t(g.units) * g.r
 
 int64_t backward_workspace(const AttnGradArgs& a)
 {
-    const AttnGeom& g = a.g;
-    const int64_t parts = a.keys.lead > 0 ? int64_t(g.splits) * g.units * a.keys.span * 2 * g.D : 0;
-    return (delta_floats(g) + parts) * 4;
+    return (delta_floats(a.g) + part_lines(a) * 2 * a.g.D) * 4;
 }
 
 int plan_backward(ua2a_plan_t plan, const ua2a_attention_grad_t* n, AttnLaunch* L)
@@ -459,9 +470,9 @@ int ua2a_attention_backward(ua2a_plan_t plan, const ua2a_attention_grad_t* n, vo
     attn_grid(workgroups(g), &L);
     err = attn_launch(L, stream);
     if (err != 0) return fail(plan, "launching attention's backward kernel of keys", err);
-    if (a.keys.lead == 0) return UA2A_OK;
+    if (part_lines(a) == 0) return UA2A_OK;
     L.kernel = AttnKernel::GradJoin;
-    attn_grid(ceil_div(int64_t(g.units) * a.keys.span * (g.D / 2), kAttnBlock), &L);
+    attn_grid(ceil_div(int64_t(g.units) * (a.keys.rest_parts > 1 ? g.keys : a.keys.span) * (g.D / 2), kAttnBlock), &L);
     err = attn_launch(L, stream);
     return err == 0 ? UA2A_OK : fail(plan, "launching the join of the keys' gradients", err);
 }

@@ -11,6 +11,7 @@ namespace ua2a {
 constexpr uint32_t kRopeBlock = 256;         // lanes per workgroup of the rotary kernel
 constexpr uint32_t kAttnBlock = 256;         // lanes per workgroup, four waves
 constexpr uint32_t kAttnWaveRows = 32;       // rows of a wave, the columns of its matrix tiles
+constexpr uint32_t kDecodeRows = 16;         // most rows of the kernel of single tokens
 constexpr uint32_t kAttnRows = 128;          // rows of a workgroup whose waves take rows of their own
 constexpr uint32_t kAttnKeys = 64;           // keys of a tile that four waves share
 constexpr uint32_t kAttnSplitKeys = 128;     // keys of a tile whose quarters go to the waves
@@ -54,7 +55,7 @@ struct AttnGradArgs {
     void* dv;
     float* delta;                // [units][rows]
     float scale, scale2;
-    float* partial;              // splits > 1: [splits][units][span][2][D]
+    float* partial;              // parts' sums: [KeyTiles' lines][2][D]
 };
 
 struct RopeArgs {
@@ -66,7 +67,7 @@ struct RopeArgs {
     const int32_t* axes;         // [pairs]
 };
 
-enum class AttnKernel : int32_t { Rope, Forward, Join, GradRows, GradKeys, GradJoin };
+enum class AttnKernel : int32_t { Rope, Forward, Decode, Join, GradRows, GradKeys, GradJoin };
 
 struct AttnLaunch {
     AttnKernel kernel;

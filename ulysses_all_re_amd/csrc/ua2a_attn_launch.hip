@@ -7,6 +7,7 @@ namespace ua2a {
 
 // The kernel of a launch; null where none is built for it.
 const void* attention_kernel(const AttnLaunch& L);
+const void* decode_kernel(const AttnLaunch& L);
 const void* attention_grad_kernel(const AttnLaunch& L);
 const void* rope_kernel(const AttnLaunch& L);
 
@@ -18,6 +19,10 @@ int attn_launch(const AttnLaunch& L, void* stream)
     case AttnKernel::Rope:
         fn = rope_kernel(L);
         args[0] = const_cast<RopeArgs*>(&L.rope);
+        break;
+    case AttnKernel::Decode:
+        fn = decode_kernel(L);
+        args[0] = const_cast<AttnArgs*>(&L.attn);
         break;
     case AttnKernel::Forward:
     case AttnKernel::Join:
