@@ -37,8 +37,20 @@ struct WaveCodes {
     u32x4v k[CH], v[CH];
     uint32_t ks[CH], vs[CH];
 
-    __device__ __forceinline__ static uint32_t row(int c) { return ((threadIdx.x & 63) + c * 64) / kAcross; }
-    __device__ __forceinline__ static uint32_t piece(int c) { return ((threadIdx.x & 63) + c * 64) % kAcross; }
+    // Which piece of which row.  Rows of 128: eight lanes take four pieces of two
+    // rows four apart, whose places in LDS lie in different banks.
+    __device__ __forceinline__ static uint32_t row(int c)
+    {
+        const uint32_t lane = threadIdx.x & 63;
+        if constexpr (DP == 128) return c * 8 + ((lane >> 3 & 3) | (lane & 4));
+        return (lane + c * 64) / kAcross;
+    }
+    __device__ __forceinline__ static uint32_t piece(int c)
+    {
+        const uint32_t lane = threadIdx.x & 63;
+        if constexpr (DP == 128) return (lane & 3) | (lane >> 3 & 4);
+        return (lane + c * 64) % kAcross;
+    }
 
     // j0: the tile's first position of this key head, in heads of D codes.  What
     // lies at or past `rows` positions is zeros (none: no row), past D too but
@@ -75,29 +87,36 @@ struct WaveCodes {
         uint32_t top = 0;
 #pragma unroll
         for (int c = 0; c < CH; ++c) top = max(top, max(ks[c], vs[c]));
-        const bool plain = __builtin_amdgcn_ballot_w64(top >= kHigh) == 0 && !look;
         bool odd = false;
+        if (__builtin_amdgcn_ballot_w64(top >= kHigh) == 0 && !look) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const bool whole = piece(c) * 16 + 16 <= D;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t at = place_of<DP>(row(c), piece(c) * 32 + h * 16);
+                    const bool in = h == 0 || whole;
+                    const u32x2v kc = {in ? k[c][2 * h] : 0u, in ? k[c][2 * h + 1] : 0u};
+                    const u32x2v vc = {in ? v[c][2 * h] : 0u, in ? v[c][2 * h + 1] : 0u};
+                    *reinterpret_cast<u32x4v*>(ktile + at) = decode8<T, E4M3>(kc, ks[c]);
+                    *reinterpret_cast<u32x4v*>(vtile + at) = decode8<T, E4M3>(vc, vs[c]);
+                }
+            }
+            return false;
+        }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const bool whole = piece(c) * 16 + 16 <= D;
-            const uint32_t bytes = piece(c) * 32;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t at = place_of<DP>(row(c), bytes + h * 16);
+                const uint32_t at = place_of<DP>(row(c), piece(c) * 32 + h * 16);
                 const bool in = h == 0 || whole;
                 const u32x2v kc = {in ? k[c][2 * h] : 0u, in ? k[c][2 * h + 1] : 0u};
                 const u32x2v vc = {in ? v[c][2 * h] : 0u, in ? v[c][2 * h + 1] : 0u};
-                u32x4v kk, vv;
-                if (plain) {
-                    kk = decode8<T, E4M3>(kc, ks[c]);
-                    vv = decode8<T, E4M3>(vc, vs[c]);
-                } else {
-                    kk = decode_raw<T, 8>(kc, in ? ks[c] : 0u, kFormat);
-                    vv = decode_raw<T, 8>(vc, in ? vs[c] : 0u, kFormat);
-                    if (look) odd |= tame<T, DP>(vv, wild, row(c), piece(c) * 2 + h);
-                }
-                *reinterpret_cast<u32x4v*>(ktile + at) = kk;
-                *reinterpret_cast<u32x4v*>(vtile + at) = vv;
+                *reinterpret_cast<u32x4v*>(ktile + at) = decode_raw<T, 8>(kc, in ? ks[c] : 0u, kFormat);
+                u32x4v x = decode_raw<T, 8>(vc, in ? vs[c] : 0u, kFormat);
+                if (look) odd |= tame<T, DP>(x, wild, row(c), piece(c) * 2 + h);
+                *reinterpret_cast<u32x4v*>(vtile + at) = x;
             }
         }
         return odd;
@@ -252,21 +271,22 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
                 }
         };
         // tiles from + wave, + 4, ...: two of them on their way
+        // (in this order: a wait counts the loads behind the one it is for)
         load(from + wave, next[0]);
+        asm volatile("" ::: "memory");
         load(from + wave + 4, next[1]);
+        const auto step = [&](uint32_t i, WaveCodes<T, DP>& w) {
+            const int32_t k0 = i < to ? position(i) : 0, k1 = k0 + static_cast<int32_t>(kTileKeys);
+            const bool look = !all_seen(top, bottom, k0, k1);
+            const bool odd = w.template put<E4M3>(ktile, vtile, wild, g.D, look);
+            load(i + 8, w);
+            wave_order();
+            if (i < to) attend(k0, look, __builtin_amdgcn_ballot_w64(odd) != 0);
+            wave_order();
+        };
         for (uint32_t i = from + wave; i < to; i += 8) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const uint32_t ii = i + b * 4;
-                if (ii >= to) break;
-                const int32_t k0 = position(ii), k1 = k0 + static_cast<int32_t>(kTileKeys);
-                const bool look = !all_seen(top, bottom, k0, k1);
-                const bool odd = next[b].template put<E4M3>(ktile, vtile, wild, g.D, look);
-                load(ii + 8, next[b]);
-                wave_order();
-                attend(k0, look, __builtin_amdgcn_ballot_w64(odd) != 0);
-                wave_order();
-            }
+            step(i, next[0]);
+            step(i + 4, next[1]);                                // past the last: a tile of zeros that is not used
         }
     }
     l += __shfl_xor(l, 16);
