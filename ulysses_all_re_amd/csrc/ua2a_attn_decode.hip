@@ -17,6 +17,11 @@ namespace {
 
 constexpr uint32_t kTileKeys = 32;
 
+__device__ __forceinline__ int32_t least_of(int32_t a, uint32_t b)
+{
+    return a < static_cast<int32_t>(b) ? a : static_cast<int32_t>(b);
+}
+
 template <class T>
 __device__ __forceinline__ f32x4v mfma16(u32x4v a, u32x4v b, f32x4v c)
 {
@@ -76,50 +81,20 @@ struct WaveCodes {
         }
     }
 
-    // Into the wave's tiles; where `look`, infinities and NaN of the values apart.
-    // Returns whether this lane had any.
+    // One of them into the wave's tile.  Returns the largest scale byte.
     template <bool E4M3>
-    __device__ __forceinline__ bool put(char* ktile, char* vtile, uint8_t* wild, uint32_t D, bool look) const
+    __device__ __forceinline__ static uint32_t put(const u32x4v (&x)[CH], const uint32_t (&xs)[CH], char* tile, uint32_t D)
     {
-        // from here on a code may pass the type's largest value
-        constexpr uint32_t kHigh = 127u + (__is_same(T, _Float16) ? 15u : 127u) - (E4M3 ? 8u : 15u) + 1u;
-        constexpr int32_t kFormat = E4M3 ? UA2A_FORMAT_E4M3 : UA2A_FORMAT_E5M2;
         uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) top = max(top, max(ks[c], vs[c]));
-        bool odd = false;
-        if (__builtin_amdgcn_ballot_w64(top >= kHigh) == 0 && !look) {
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const bool whole = piece(c) * 16 + 16 <= D;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t at = place_of<DP>(row(c), piece(c) * 32 + h * 16);
-                    const bool in = h == 0 || whole;
-                    const u32x2v kc = {in ? k[c][2 * h] : 0u, in ? k[c][2 * h + 1] : 0u};
-                    const u32x2v vc = {in ? v[c][2 * h] : 0u, in ? v[c][2 * h + 1] : 0u};
-                    *reinterpret_cast<u32x4v*>(ktile + at) = decode8<T, E4M3>(kc, ks[c]);
-                    *reinterpret_cast<u32x4v*>(vtile + at) = decode8<T, E4M3>(vc, vs[c]);
-                }
-            }
-            return false;
-        }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const bool whole = piece(c) * 16 + 16 <= D;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t at = place_of<DP>(row(c), piece(c) * 32 + h * 16);
-                const bool in = h == 0 || whole;
-                const u32x2v kc = {in ? k[c][2 * h] : 0u, in ? k[c][2 * h + 1] : 0u};
-                const u32x2v vc = {in ? v[c][2 * h] : 0u, in ? v[c][2 * h + 1] : 0u};
-                *reinterpret_cast<u32x4v*>(ktile + at) = decode_raw<T, 8>(kc, in ? ks[c] : 0u, kFormat);
-                u32x4v x = decode_raw<T, 8>(vc, in ? vs[c] : 0u, kFormat);
-                if (look) odd |= tame<T, DP>(x, wild, row(c), piece(c) * 2 + h);
-                *reinterpret_cast<u32x4v*>(vtile + at) = x;
-            }
+            const u32x2v lo = {x[c][0], x[c][1]}, hi = {whole ? x[c][2] : 0u, whole ? x[c][3] : 0u};
+            *reinterpret_cast<u32x4v*>(tile + place_of<DP>(row(c), piece(c) * 32)) = decode8<T, E4M3>(lo, xs[c]);
+            *reinterpret_cast<u32x4v*>(tile + place_of<DP>(row(c), piece(c) * 32 + 16)) = decode8<T, E4M3>(hi, xs[c]);
+            top = max(top, xs[c]);
         }
-        return odd;
+        return top;
     }
 };
 
@@ -167,7 +142,7 @@ template <class T, int DP, bool E4M3>
 __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(AttnArgs a)
 {
     constexpr uint32_t kTile = kTileKeys * kRow<DP>;
-    __shared__ __attribute__((aligned(16))) char lds[4 * 2 * kTile];         // each wave's keys and values
+    __shared__ __attribute__((aligned(16))) char lds[4 * kTile];             // each wave's keys, then its values
     __shared__ __attribute__((aligned(16))) uint8_t wilds[4 * kTileKeys * (DP / 4)];
     __shared__ float stat[5 * kDecodeRows * 2];                              // the waves', then joined
     const AttnGeom& g = a.g;
@@ -176,8 +151,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
     const AttnPlace at = attn_place(g, item);
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const uint32_t quarter = lane >> 4, col = lane & 15;
-    char* const ktile = lds + wave * 2 * kTile;
-    char* const vtile = ktile + kTile;
+    char* const tile = lds + wave * kTile;
     uint8_t* const wild = wilds + wave * kTileKeys * (DP / 4);
     const AttnSeq seq = attn_seq(g, static_cast<int64_t>(a.starts[at.i]),
                                  a.counts != nullptr ? static_cast<int64_t>(a.counts[at.i]) : static_cast<int64_t>(g.n));
@@ -207,17 +181,38 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
         WaveCodes<T, DP> next[2];
         const auto load = [&](uint32_t i, WaveCodes<T, DP>& w) {
             const int32_t k0 = i < to ? position(i) : 0;
-            const int32_t rows = seq.end - k0 < static_cast<int32_t>(kTileKeys) ? seq.end - k0 : static_cast<int32_t>(kTileKeys);
-            w.load(a, base + static_cast<int64_t>(k0) * g.kvl, i < to ? rows : 0);
+            w.load(a, base + static_cast<int64_t>(k0) * g.kvl, i < to ? least_of(seq.end - k0, kTileKeys) : 0);
         };
-        const auto attend = [&](int32_t k0, bool masked, bool odd) {
+        const auto step = [&](uint32_t i, WaveCodes<T, DP>& w) {
+            const int32_t k0 = i < to ? position(i) : 0, k1 = k0 + static_cast<int32_t>(kTileKeys);
+            const bool masked = i >= to || !all_seen(top, bottom, k0, k1);
+            const int64_t j0 = base + static_cast<int64_t>(k0) * g.kvl;
+            const int32_t rows = i < to ? least_of(seq.end - k0, kTileKeys) : 0;
+            constexpr int32_t kFormat = E4M3 ? UA2A_FORMAT_E4M3 : UA2A_FORMAT_E5M2;
+            const uint32_t ktop = WaveCodes<T, DP>::template put<E4M3>(w.k, w.ks, tile, g.D);
+            if (__builtin_amdgcn_ballot_w64(ktop >= high_scale<T>(kFormat)) != 0)
+                decode_again<T, DP>(tile, g, a.codes + j0 * g.D, a.scales + j0 * g.nb, rows, kFormat, lane, 64);
+            wave_order();
             f32x4v s[2];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 s[b] = f32x4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int ks = 0; ks < DP / 32; ++ks) s[b] = mfma16<T>(along16<DP>(ktile, b * 16, ks), q[ks], s[b]);
+                for (int ks = 0; ks < DP / 32; ++ks) s[b] = mfma16<T>(along16<DP>(tile, b * 16, ks), q[ks], s[b]);
             }
+            wave_order();
+            const uint32_t vtop = WaveCodes<T, DP>::template put<E4M3>(w.v, w.vs, tile, g.D);
+            load(i + 8, w);
+            if (__builtin_amdgcn_ballot_w64(vtop >= high_scale<T>(kFormat)) != 0)
+                decode_again<T, DP>(tile, g, a.codes + a.part + j0 * g.D, a.scales + a.part_scales + j0 * g.nb, rows, kFormat,
+                                    lane, 64);
+            wave_order();
+            bool odd = false;
+            if (masked) {
+                odd = __builtin_amdgcn_ballot_w64(tame_tile<T, DP>(tile, wild, kTileKeys, lane, 64)) != 0;
+                wave_order();
+            }
+            if (i >= to) return;
             if (masked) {
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
@@ -246,7 +241,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
             const u32x4v p = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]), pack2<T>(s[1][0], s[1][1]),
                               pack2<T>(s[1][2], s[1][3])};
 #pragma unroll
-            for (int db = 0; db < DP / 16; ++db) o[db] = mfma16<T>(transposed16<DP>(vtile, db), p, o[db]);
+            for (int db = 0; db < DP / 16; ++db) o[db] = mfma16<T>(transposed16<DP>(tile, db), p, o[db]);
             if (!odd) return;
             uint32_t up[DP / 32], down[DP / 32];
 #pragma unroll
@@ -275,18 +270,11 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
         load(from + wave, next[0]);
         asm volatile("" ::: "memory");
         load(from + wave + 4, next[1]);
-        const auto step = [&](uint32_t i, WaveCodes<T, DP>& w) {
-            const int32_t k0 = i < to ? position(i) : 0, k1 = k0 + static_cast<int32_t>(kTileKeys);
-            const bool look = !all_seen(top, bottom, k0, k1);
-            const bool odd = w.template put<E4M3>(ktile, vtile, wild, g.D, look);
-            load(i + 8, w);
-            wave_order();
-            if (i < to) attend(k0, look, __builtin_amdgcn_ballot_w64(odd) != 0);
-            wave_order();
-        };
         for (uint32_t i = from + wave; i < to; i += 8) {
             step(i, next[0]);
+            wave_order();
             step(i + 4, next[1]);                                // past the last: a tile of zeros that is not used
+            wave_order();
         }
     }
     l += __shfl_xor(l, 16);

@@ -300,6 +300,49 @@ __device__ __forceinline__ u32x4v decode8(u32x2v c, uint32_t byte)
     return r;
 }
 
+// The same over a tile of `rows` rows in LDS, by `lanes` lanes: returns whether this
+// lane met any.
+template <class T, int DP>
+__device__ __forceinline__ bool tame_tile(char* tile, uint8_t* wild, uint32_t rows, uint32_t lane, uint32_t lanes)
+{
+    bool odd = false;
+#pragma unroll 1
+    for (uint32_t i = lane; i < rows * (DP / 8); i += lanes) {
+        const uint32_t row = i / (DP / 8), chunk = i % (DP / 8);
+        char* const p = tile + place_of<DP>(row, chunk * 16);
+        u32x4v v = *reinterpret_cast<const u32x4v*>(p);
+        if (tame<T, DP>(v, wild, row, chunk)) {
+            *reinterpret_cast<u32x4v*>(p) = v;
+            odd = true;
+        }
+    }
+    return odd;
+}
+
+// A tile of a cache decoded once more, as decode_raw does, which keeps codes past
+// the type's largest value there: for scales at which there are such.  The codes
+// and scales of `rows` positions are read again.
+template <class T, int DP>
+__device__ __forceinline__ void decode_again(char* tile, const AttnGeom& g, const uint8_t* codes, const uint8_t* scales,
+                                             int32_t rows, int32_t format, uint32_t lane, uint32_t lanes)
+{
+#pragma unroll 1
+    for (uint32_t i = lane; i < static_cast<uint32_t>(rows) * (DP / 8); i += lanes) {
+        const uint32_t row = i / (DP / 8), chunk = i % (DP / 8), d = chunk * 8;
+        if (d >= g.D) continue;
+        const u32x2v c = *reinterpret_cast<const u32x2v*>(codes + static_cast<int64_t>(row) * g.kvl * g.D + d);
+        const uint32_t byte = scales[static_cast<int64_t>(row) * g.kvl * g.nb + d / kBlockValues];
+        *reinterpret_cast<u32x4v*>(tile + place_of<DP>(row, chunk * 16)) = decode_raw<T, 8>(c, byte, format);
+    }
+}
+
+// The least scale byte at which a code may pass the type's largest value.
+template <class T>
+__device__ __forceinline__ uint32_t high_scale(int32_t format)
+{
+    return 127u + (__is_same(T, _Float16) ? 15u : 127u) - (format == UA2A_FORMAT_E4M3 ? 8u : 15u) + 1u;
+}
+
 // Four values d .. of a row's sums, with its maximum and sum: the result, or a
 // part's place in the workspace.  The lane of d = 0 writes the statistics.
 template <class T>

@@ -46,39 +46,26 @@ struct CodeLoads {
         }
     }
     template <bool E4M3>
-    __device__ __forceinline__ bool put(char* ktile, char* vtile, uint8_t* wild, bool look) const
+    __device__ __forceinline__ void put(char* ktile, char* vtile) const
     {
-        // from here on a code may pass the type's largest value
-        constexpr uint32_t kHigh = 127u + (__is_same(T, _Float16) ? 15u : 127u) - (E4M3 ? 8u : 15u) + 1u;
-        uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) top = max(top, max(ks[c], vs[c]));
-        const bool high = __builtin_amdgcn_ballot_w64(top >= kHigh) != 0;
-        bool odd = false;
-        if (!high && !look) {
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const uint32_t at = place_of<DP>(row(c), chunk(c) * 16);
-                *reinterpret_cast<u32x4v*>(ktile + at) = decode8<T, E4M3>(k[c], ks[c]);
-                *reinterpret_cast<u32x4v*>(vtile + at) = decode8<T, E4M3>(v[c], vs[c]);
-            }
-            return false;
-        }
-        constexpr int32_t kFormat = E4M3 ? UA2A_FORMAT_E4M3 : UA2A_FORMAT_E5M2;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const uint32_t at = place_of<DP>(row(c), chunk(c) * 16);
-            *reinterpret_cast<u32x4v*>(ktile + at) = decode_raw<T, 8>(k[c], ks[c], kFormat);
-            u32x4v x = decode_raw<T, 8>(v[c], vs[c], kFormat);
-            if (look) odd |= tame<T, DP>(x, wild, row(c), chunk(c));
-            *reinterpret_cast<u32x4v*>(vtile + at) = x;
+            *reinterpret_cast<u32x4v*>(ktile + at) = decode8<T, E4M3>(k[c], ks[c]);
+            *reinterpret_cast<u32x4v*>(vtile + at) = decode8<T, E4M3>(v[c], vs[c]);
         }
-        return odd;
     }
-    // Returns whether this lane's values had an infinity or NaN (where `look`).
-    __device__ __forceinline__ bool store(char* ktile, char* vtile, uint8_t* wild, int32_t format, bool look) const
+    // Returns the largest scale byte.
+    __device__ __forceinline__ uint32_t store(char* ktile, char* vtile, int32_t format) const
     {
-        return format == UA2A_FORMAT_E4M3 ? put<true>(ktile, vtile, wild, look) : put<false>(ktile, vtile, wild, look);
+        if (format == UA2A_FORMAT_E4M3)
+            put<true>(ktile, vtile);
+        else
+            put<false>(ktile, vtile);
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) top = max(top, max(ks[c], vs[c]));
+        return top;
     }
 };
 
@@ -211,7 +198,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
     constexpr uint32_t kBuffers = CODES || SHARED ? 1 : 2;
     __shared__ __attribute__((aligned(1024))) char lds[kBuffers * 2 * kTile];
     __shared__ __attribute__((aligned(16))) uint8_t wild[KEYS * (DP / 4)];
-    __shared__ uint32_t odd_tile;
+    __shared__ uint32_t odd_tile, high_tile;
     __shared__ float stat[SHARED ? 5 * 32 * 2 : 1];            // the waves', then joined
     const AttnGeom& g = a.g;
     const uint32_t item = attn_item(g, (blockIdx.y << kAttnGridLog) + blockIdx.x);
@@ -246,7 +233,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
         row_operands<DP>(static_cast<const uint16_t*>(a.q) + place.at, g.D, half, live, q);
 
         const int64_t base = static_cast<int64_t>(at.seq) * g.keys * g.kvl + at.kvh;
-        if (threadIdx.x == 0) odd_tile = ~0u;
+        if (threadIdx.x == 0) odd_tile = high_tile = ~0u;
         const auto position = [&](uint32_t i) { return static_cast<int32_t>(walk_tile(walk, i) * KEYS); };
         // whether some row of the workgroup does not see some key of tile i
         const auto part_seen = [&](int32_t k0) { return !all_seen(top, bottom, k0, k0 + KEYS); };
@@ -268,9 +255,22 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
                 const int32_t k0 = position(i);
                 const bool look = part_seen(k0);
                 __syncthreads();                                 // the last tile has been read
-                if (loads.store(lds, lds + kTile, wild, a.format, look)) odd_tile = i;
+                if (loads.store(lds, lds + kTile, a.format) >= high_scale<T>(a.format)) high_tile = i;
                 if (i + 1 < to) load(i + 1);
                 __syncthreads();
+                if (high_tile == i) {
+                    const int64_t j0 = base + static_cast<int64_t>(k0) * g.kvl;
+                    const int32_t n = seq.end - k0 < KEYS ? seq.end - k0 : KEYS;
+                    const uint8_t *codes = a.codes + j0 * g.D, *scales = a.scales + j0 * g.nb;
+                    decode_again<T, DP>(lds, g, codes, scales, n, a.format, threadIdx.x, kAttnBlock);
+                    decode_again<T, DP>(lds + kTile, g, codes + a.part, scales + a.part_scales, n, a.format, threadIdx.x,
+                                        kAttnBlock);
+                    __syncthreads();
+                }
+                if (look) {
+                    if (tame_tile<T, DP>(lds + kTile, wild, KEYS, threadIdx.x, kAttnBlock)) odd_tile = i;
+                    __syncthreads();
+                }
                 work(i, k0, lds, lds + kTile, look);
             }
         } else {
@@ -309,16 +309,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
                 arrived();
                 if (kBuffers == 2 && i + 1 < to) load(i + 1, other);
                 if (look) {
-#pragma unroll
-                    for (int n = 0; n < Loads::N; ++n) {
-                        const uint32_t x = threadIdx.x + n * kAttnBlock, row = x / (DP / 8), chunk = x % (DP / 8);
-                        char* const p = tile + kTile + place_of<DP>(row, chunk * 16);
-                        u32x4v v = *reinterpret_cast<const u32x4v*>(p);
-                        if (tame<T, DP>(v, wild, row, chunk)) {
-                            *reinterpret_cast<u32x4v*>(p) = v;
-                            odd_tile = i;
-                        }
-                    }
+                    if (tame_tile<T, DP>(tile + kTile, wild, KEYS, threadIdx.x, kAttnBlock)) odd_tile = i;
                     __syncthreads();
                 }
                 work(i, k0, tile, tile + kTile, look);
