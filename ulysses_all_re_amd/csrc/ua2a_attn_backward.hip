@@ -96,7 +96,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
             row_operands<DP>(static_cast<const uint16_t*>(a.out) + place.at, g.D, half, live, o);
 #pragma unroll
             for (int ks = 0; ks < DP / 16; ++ks) delta = dot2_sum(go[ks], o[ks], delta, T{});
-            delta += other_half(delta);
+            delta = add_halves(delta);
         }
         if (live && half == 0) a.delta[static_cast<int64_t>(at.unit) * g.rows + row] = delta;
         row_operands<DP>(static_cast<const uint16_t*>(a.q) + place.at, g.D, half, live, q);

@@ -52,10 +52,16 @@ __device__ __forceinline__ u32x4v operand_of(const f32x16v& c, int s)
     return r;
 }
 
-// The value of the lane 32 places on (or back), joined by f.
-__device__ __forceinline__ float other_half(float x)
+// The largest, and the sum, of a value and the other half's (lane 32 places on or back).
+__device__ __forceinline__ float max_halves(float x)
 {
-    return __shfl_xor(x, 32);
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_halves(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
 // A tile of rows in LDS, DP values each, in chunks of 16 bytes.  Row r keeps its

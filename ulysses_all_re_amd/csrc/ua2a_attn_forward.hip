@@ -104,6 +104,7 @@ __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16
 {
     const uint32_t half = (threadIdx.x & 63) >> 5;
     f32x16v s[NK];
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int b = 0; b < NK; ++b) {
 #pragma unroll
@@ -112,6 +113,7 @@ __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16
         for (int ks = 0; ks < DP / 16; ++ks)
             s[b] = mfma<T>(along<DP>(ktile, row0 + b * 32, ks), q[ks], s[b]);
     }
+    __builtin_amdgcn_s_setprio(0);
     const auto key = [&](int b, int i) {
         return k0 + static_cast<int32_t>(b * 32 + (i / 4) * 8 + half * 4 + i % 4);
     };
@@ -127,7 +129,7 @@ __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16
     for (int b = 0; b < NK; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-    top = fmaxf(top, other_half(top)) * scale2;
+    top = max_halves(top) * scale2;
     const bool grow = top > r.m + 8.f || (r.m == -__builtin_inff() && top > r.m);
     if (__builtin_amdgcn_ballot_w64(grow) != 0) {
         const float next = fmaxf(r.m, top);
@@ -154,10 +156,12 @@ __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16
     for (int b = 0; b < NK; ++b)
 #pragma unroll
         for (int t = 0; t < 2; ++t) p[2 * b + t] = operand_of<T>(s[b], t);
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int db = 0; db < DP / 32; ++db)
 #pragma unroll
         for (int t = 0; t < 2 * NK; ++t) r.o[db] = mfma<T>(transposed<DP>(vtile, row0, t, db), p[t], r.o[db]);
+    __builtin_amdgcn_s_setprio(0);
     if (!odd) return;
     // the tile's infinities and NaN: of the keys that the row sees, one bit per value
     uint32_t up[DP / 32], down[DP / 32];
@@ -322,7 +326,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
         }
     }
     __syncthreads();
-    r.l += other_half(r.l);
+    r.l = add_halves(r.l);
     if constexpr (SHARED) {
         // the four waves' maxima and sums, then their values' sums, 32 rows of DP each
         if (half == 0) {

@@ -108,7 +108,7 @@ void forward_shape(AttnGeom* g, AttnLaunch* L)
     const int64_t tiles = ceil_div(g->rows, per), all = int64_t(g->units) * tiles;
     int64_t splits = 1;
     if (all < 512) {
-        splits = ceil_div(512, all);
+        splits = 512 / all;
         const int64_t most = most_seen(*g, per) / (4 * size);
         if (splits > most) splits = most;
         if (splits < 1) splits = 1;
