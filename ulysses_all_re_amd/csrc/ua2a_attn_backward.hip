@@ -169,16 +169,24 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
 }
 
 // dk and dv.  A wave has 32 keys as columns of its matrix tiles and walks the
-// rows that see one of the workgroup's 128 keys in tiles of 64: scores and
+// rows that see one of the workgroup's 128 keys, tile by tile: scores and
 // dout v^T come as rows x keys, and P and dS go on from their registers to the
 // products with dout and q.  Where a tile's walk is long for the call, workgroups of
 // their own walk parts of it, whose sums a third kernel joins in order.
 template <class T, int DP>
 __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(AttnGradArgs a)
 {
-    constexpr int ROWS = kAttnGradRows;
+    // Of the four operands that a wave keeps for the whole walk the keys' do not fit
+    // the registers beside sums of 128 values (they spill: 3.46 ms against 3.02), so
+    // they lie in LDS, and tiles of rows are half as long (which alone costs a fifth:
+    // heads of 64, 102 us against 128).
+    constexpr bool kKeysInLds = DP == 128;
+    constexpr int ROWS = kKeysInLds ? 32 : 64;
     constexpr uint32_t kTile = ROWS * kRow<DP>;
-    __shared__ __attribute__((aligned(1024))) char lds[4 * kTile];           // two buffers of q and dout
+    constexpr uint32_t kKeyTile = kKeysInLds ? kAttnGradKeys * kRow<DP> : 0;
+    // two buffers of q and dout, and the workgroup's keys
+    __shared__ __attribute__((aligned(1024))) char lds[4 * kTile + kKeyTile];
+    char* const ktile = lds + 4 * kTile;
     __shared__ __attribute__((aligned(16))) float stats[2 * 2 * ROWS];       // ... of lse and -delta
     const AttnGeom& g = a.g;
     const uint32_t item = attn_item(g, (blockIdx.y << kAttnGridLog) + blockIdx.x);
@@ -195,9 +203,24 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(Attn
     zero(dk);
     zero(dv);
     if (static_cast<int32_t>(first) < seq.end) {
-        u32x4v k[DP / 16], v[DP / 16];
-        row_operands<DP>(static_cast<const uint16_t*>(a.k) + to, g.D, half, live, k);
+        u32x4v v[DP / 16], k[kKeysInLds ? 1 : DP / 16];
         row_operands<DP>(static_cast<const uint16_t*>(a.v) + to, g.D, half, live, v);
+        if constexpr (!kKeysInLds) {
+            row_operands<DP>(static_cast<const uint16_t*>(a.k) + to, g.D, half, live, k);
+        } else {
+            typedef TileLoads<DP, kAttnGradKeys> Loads;
+            const uint32_t row_bytes = g.kvl * g.D * 2;
+            const int64_t start = ((static_cast<int64_t>(at.at.seq) * g.keys + first) * g.kvl + at.at.kvh) * g.D * 2;
+            const int32_t n = static_cast<int32_t>(past) < seq.end ? static_cast<int32_t>(past - first) : seq.end - static_cast<int32_t>(first);
+            const u32x4v from_k = descriptor(static_cast<const char*>(a.k) + start, static_cast<uint32_t>(n) * row_bytes);
+#pragma unroll
+            for (int i = 0; i < Loads::N; ++i) {
+                if (!Loads::has(i, wave)) continue;
+                const uint32_t bytes = Loads::bytes(i, wave, g.D);
+                load_to_lds(from_k, bytes == kNowhere ? kNowhere : Loads::row(i, wave) * row_bytes + bytes,
+                            ktile + (i * 4 + wave) * 1024);
+            }
+        }
         // the rows that see this lane's key, and those that see one of the workgroup's
         const Span32 mine = live ? seers_of(g.win, static_cast<int32_t>(j), static_cast<int32_t>(j) + 1, seq.end) : Span32{0, 0};
         const uint32_t ra = static_cast<uint32_t>(mine.first) * g.group, rb = static_cast<uint32_t>(mine.last) * g.group;
@@ -259,7 +282,12 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(Attn
                     }
                 }
 #pragma unroll
-                for (int ks = 0; ks < DP / 16; ++ks) s = mfma<T>(along<DP>(qtile, row0, ks), k[ks], s);
+                for (int ks = 0; ks < DP / 16; ++ks) {
+                    if constexpr (kKeysInLds)
+                        s = mfma<T>(along<DP>(qtile, row0, ks), along<DP>(ktile, wave * 32, ks), s);
+                    else
+                        s = mfma<T>(along<DP>(qtile, row0, ks), k[ks], s);
+                }
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ++ks) dp = mfma<T>(along<DP>(gtile, row0, ks), v[ks], dp);
 #pragma unroll
@@ -327,13 +355,12 @@ template <class T>
 __global__ __launch_bounds__(kAttnBlock) void ua2a_attention_keys_join_kernel(AttnGradArgs a)
 {
     const AttnGeom& g = a.g;
-    const uint32_t per = g.D / 2;
-    const int64_t id = static_cast<int64_t>((blockIdx.y << kAttnGridLog) + blockIdx.x) * kAttnBlock + threadIdx.x;
+    const uint32_t per = g.D / 2, here = fdiv(threadIdx.x, a.keys.d_lanes);
     const uint32_t keys = a.keys.rest_parts > 1 ? g.keys : a.keys.span;      // of a unit that may have parts
-    const int64_t line = id / per;                               // unit * keys + key
-    if (line >= static_cast<int64_t>(g.units) * keys) return;
-    const uint32_t c = static_cast<uint32_t>(id - line * per) * 4;          // of dk's and dv's D
-    const uint32_t unit = static_cast<uint32_t>(line / keys), j = static_cast<uint32_t>(line - static_cast<int64_t>(unit) * keys);
+    const uint32_t line = ((blockIdx.y << kAttnGridLog) + blockIdx.x) * a.keys.per_group + here;   // unit * keys + key
+    if (here >= a.keys.per_group || line >= g.units * keys) return;
+    const uint32_t c = (threadIdx.x - here * per) * 4;                       // of dk's and dv's D
+    const uint32_t unit = fdiv(line, a.keys.d_keys), j = line - unit * keys;
     const uint32_t parts = j < a.keys.span ? a.keys.lead_parts : a.keys.rest_parts;
     if (parts <= 1) return;
     const uint32_t seq = fdiv(unit, g.d_kvl), kvh = unit - seq * g.kvl;

@@ -402,40 +402,41 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
         a.lse[place.stat] = live && r.l != 0.f ? r.m * kLn2 + logf(r.l) : -__builtin_inff();
 }
 
-// The parts of rows whose keys were walked by several workgroups, joined: a
-// workgroup a row.  D / 4 lanes (`wide`) have four values each of a part, so a
-// workgroup takes 8 to 32 parts at once, whose loads are all on their way
-// together (64 parts: 23 us with one wave a row, two parts at once).
+// The parts of rows whose keys were walked by several workgroups, joined.  A group
+// of D / 4 lanes has four values each of eight parts, whose loads are on their way
+// together; more parts take more groups, up to a workgroup (64 parts of 16 rows:
+// 23 us with two parts at once, 6.5 with 64; 3 parts of 18,720 rows: 20 us with a
+// group for each part).
 template <class T>
 __global__ __launch_bounds__(kAttnBlock) void ua2a_attention_join_kernel(AttnArgs a)
 {
     __shared__ f32x4v sums[kAttnBlock];
     __shared__ float tops[kAttnBlock], totals[kAttnBlock];
     const AttnGeom& g = a.g;
-    const int64_t lines = static_cast<int64_t>(g.units) * g.rows;
-    const int64_t line = static_cast<int64_t>((blockIdx.y << kAttnGridLog) + blockIdx.x);
-    if (line >= lines) return;
+    const uint32_t count = g.units * g.rows;                     // < 2^31
+    const int64_t lines = count;
+    const JoinShape js = join_shape(g);
+    const uint32_t d = (threadIdx.x & (js.wide - 1)) * 4, group = threadIdx.x / js.wide, mine = group & (js.at_once - 1);
+    const uint32_t line = ((blockIdx.y << kAttnGridLog) + blockIdx.x) * js.rows + group / js.at_once;
+    const bool in = line < count;
     AttnPlace at;
-    at.unit = static_cast<uint32_t>(line / g.rows);
+    at.unit = in ? fdiv(line, g.d_rows) : 0;
     at.seq = fdiv(at.unit, g.d_kvl);
     at.kvh = at.unit - at.seq * g.kvl;
     at.i = at.seq - fdiv(at.seq, g.d_seqs) * g.seqs;
-    const RowPlace pl = row_place(g, at, static_cast<uint32_t>(line - static_cast<int64_t>(at.unit) * g.rows));
+    const RowPlace pl = row_place(g, at, in ? line - at.unit * g.rows : 0);
     const AttnSeq seq = attn_seq(g, a.starts != nullptr ? static_cast<int64_t>(a.starts[at.i]) : 0,
                                  a.counts != nullptr ? static_cast<int64_t>(a.counts[at.i]) : static_cast<int64_t>(g.n));
-    const bool live = pl.t >= seq.first && pl.t < seq.last;
-    if (!live && a.keep) return;
-    const uint32_t wide = g.D > 64 ? 32 : g.D > 32 ? 16 : 8;
-    const uint32_t d = (threadIdx.x & (wide - 1)) * 4, mine = threadIdx.x / wide, step = kAttnBlock / wide;
+    const bool live = in && pl.t >= seq.first && pl.t < seq.last;
     float m = -__builtin_inff(), l = 0.f;
     f32x4v x = {0.f, 0.f, 0.f, 0.f};
-    constexpr int kAtOnce = 8;
-    for (uint32_t s0 = mine; live && s0 < g.splits; s0 += step * kAtOnce) {
-        float sm[kAtOnce], sl[kAtOnce];
-        f32x4v sx[kAtOnce];
+    constexpr int kEach = kJoinEach;
+    for (uint32_t s0 = mine; live && s0 < g.splits; s0 += js.at_once * kEach) {
+        float sm[kEach], sl[kEach];
+        f32x4v sx[kEach];
 #pragma unroll
-        for (int b = 0; b < kAtOnce; ++b) {
-            const uint32_t s = s0 + b * step;
+        for (int b = 0; b < kEach; ++b) {
+            const uint32_t s = s0 + b * js.at_once;
             sm[b] = -__builtin_inff();
             sl[b] = 0.f;
             sx[b] = f32x4v{0.f, 0.f, 0.f, 0.f};
@@ -446,13 +447,13 @@ __global__ __launch_bounds__(kAttnBlock) void ua2a_attention_join_kernel(AttnArg
         }
         float now = m;
 #pragma unroll
-        for (int b = 0; b < kAtOnce; ++b) now = fmaxf(now, sm[b]);
+        for (int b = 0; b < kEach; ++b) now = fmaxf(now, sm[b]);
         const float mm = now == -__builtin_inff() ? 0.f : now;
         const float f = __builtin_amdgcn_exp2f(m - mm);
         l *= f;
         x *= f;
 #pragma unroll
-        for (int b = 0; b < kAtOnce; ++b) {
+        for (int b = 0; b < kEach; ++b) {
             const float w = __builtin_amdgcn_exp2f(sm[b] - mm);
             l += sl[b] * w;
             x += sx[b] * w;
@@ -463,15 +464,15 @@ __global__ __launch_bounds__(kAttnBlock) void ua2a_attention_join_kernel(AttnArg
     tops[threadIdx.x] = m;
     totals[threadIdx.x] = l;
     __syncthreads();
-    if (mine != 0 || d >= g.D) return;
-    for (uint32_t b = 0; b < step; ++b) m = fmaxf(m, tops[b * wide + threadIdx.x]);
+    if (mine != 0 || d >= g.D || !in || (!live && a.keep)) return;
+    for (uint32_t b = 0; b < js.at_once; ++b) m = fmaxf(m, tops[threadIdx.x + b * js.wide]);
     const float mm = m == -__builtin_inff() ? 0.f : m;
     x = f32x4v{0.f, 0.f, 0.f, 0.f};
     l = 0.f;
-    for (uint32_t b = 0; b < step; ++b) {
-        const float w = __builtin_amdgcn_exp2f(tops[b * wide + threadIdx.x] - mm);
-        l += totals[b * wide + threadIdx.x] * w;
-        x += sums[b * wide + threadIdx.x] * w;
+    for (uint32_t b = 0; b < js.at_once; ++b) {
+        const float w = __builtin_amdgcn_exp2f(tops[threadIdx.x + b * js.wide] - mm);
+        l += totals[threadIdx.x + b * js.wide] * w;
+        x += sums[threadIdx.x + b * js.wide] * w;
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
     u32x2v y = {0, 0};

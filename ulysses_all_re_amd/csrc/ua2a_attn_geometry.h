@@ -86,7 +86,7 @@ struct AttnGeom {
     uint32_t keys;               // positions of a sequence
     uint32_t splits;             // parts of a walk
     uint32_t items;              // units * tiles * splits
-    Div32 d_splits, d_tiles, d_kvl, d_seqs, d_group;
+    Div32 d_splits, d_tiles, d_kvl, d_seqs, d_group, d_rows;
 };
 
 constexpr uint32_t kAttnXcds = 8;
@@ -194,6 +194,24 @@ UA2A_HD bool none_seen(const Seen& a, const Seen& b, int32_t k0, int32_t k1)
     return (k0 >= b.hi || k1 <= a.lo) && k0 >= b.sk;
 }
 
+// How a workgroup of 256 lanes joins rows' parts: `wide` lanes (four values each)
+// take kJoinEach parts at a time, `at_once` such groups a row, `rows` rows.
+constexpr uint32_t kJoinEach = 8;
+struct JoinShape {
+    uint32_t wide, at_once, rows;
+};
+
+UA2A_HD JoinShape join_shape(const AttnGeom& g)
+{
+    JoinShape s;
+    s.wide = g.D > 64 ? 32 : g.D > 32 ? 16 : 8;
+    const uint32_t groups = 256 / s.wide;
+    s.at_once = 1;
+    while (s.at_once * kJoinEach < g.splits && s.at_once < groups) s.at_once *= 2;
+    s.rows = groups / s.at_once;
+    return s;
+}
+
 // ------------------------------------------------------------- keys' gradients
 // A unit's tiles of keys: the first `lead` (span keys) are walked in lead_parts
 // parts each, the others in rest_parts.  Parts' sums lie in the workspace, the
@@ -204,6 +222,8 @@ struct KeyTiles {
     uint32_t per_unit;           // lead * lead_parts + (tiles - lead) * rest_parts
     Div32 d_per_unit, d_lead_parts, d_rest_parts;
     int64_t rest_line;           // where the other tiles' sums start, in keys
+    uint32_t per_group;          // join: keys of a workgroup, D / 2 lanes each
+    Div32 d_lanes, d_keys;       // ... by D / 2, and by the keys of a unit that may have parts
 };
 
 struct KeyPlace {

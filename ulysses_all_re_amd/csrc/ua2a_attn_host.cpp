@@ -70,6 +70,7 @@ int attn_geometry(const ua2a_plan_s* p, const ua2a_window_t& w, int64_t kv_heads
     g->d_kvl = make_div32(g->kvl);
     g->d_seqs = make_div32(g->seqs);
     g->d_group = make_div32(g->group);
+    g->d_rows = make_div32(g->rows);
     return UA2A_OK;
 }
 
@@ -139,7 +140,7 @@ int launch_forward(ua2a_plan_t plan, AttnLaunch* L, void* workspace, void* strea
     if (err != 0) return fail(plan, "launching the attention kernel", err);
     if (g.splits == 1) return UA2A_OK;
     L->kernel = AttnKernel::Join;
-    attn_grid(int64_t(g.units) * g.rows, L);
+    attn_grid(ceil_div(int64_t(g.units) * g.rows, join_shape(g).rows), L);
     err = attn_launch(*L, stream);
     return err == 0 ? UA2A_OK : fail(plan, "launching the join of attention's parts", err);
 }
@@ -215,6 +216,9 @@ void backward_shape(AttnGradArgs* a)
     t.d_per_unit = make_div32(t.per_unit);
     t.d_lead_parts = make_div32(t.lead_parts);
     t.d_rest_parts = make_div32(t.rest_parts);
+    t.per_group = kAttnBlock / (g.D / 2);
+    t.d_lanes = make_div32(g.D / 2);
+    t.d_keys = make_div32(t.rest_parts > 1 || t.span == 0 ? g.keys : t.span);
     t.rest_line = first > 1 ? first * g.units * span : 0;
     g.items = g.units * t.per_unit;
 }
@@ -473,7 +477,7 @@ int ua2a_attention_backward(ua2a_plan_t plan, const ua2a_attention_grad_t* n, vo
     if (err != 0) return fail(plan, "launching attention's backward kernel of keys", err);
     if (part_lines(a) == 0) return UA2A_OK;
     L.kernel = AttnKernel::GradJoin;
-    attn_grid(ceil_div(int64_t(g.units) * (a.keys.rest_parts > 1 ? g.keys : a.keys.span) * (g.D / 2), kAttnBlock), &L);
+    attn_grid(ceil_div(int64_t(g.units) * a.keys.d_keys.d, a.keys.per_group), &L);
     err = attn_launch(L, stream);
     return err == 0 ? UA2A_OK : fail(plan, "launching the join of the keys' gradients", err);
 }

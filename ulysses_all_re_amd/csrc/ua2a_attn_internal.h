@@ -16,7 +16,6 @@ constexpr uint32_t kAttnRows = 128;          // rows of a workgroup whose waves 
 constexpr uint32_t kAttnKeys = 64;           // keys of a tile that four waves share
 constexpr uint32_t kAttnSplitKeys = 128;     // keys of a tile whose quarters go to the waves
 constexpr uint32_t kAttnGradKeys = 128;      // keys of a workgroup of their gradients
-constexpr uint32_t kAttnGradRows = 64;       // rows of a tile that they walk
 constexpr uint32_t kAttnGridLog = 23;        // workgroups along x: 2^31 lanes
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
