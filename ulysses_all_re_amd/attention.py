@@ -160,28 +160,33 @@ class AttentionCalls:
     # ------------------------------------------------------------------ rotary
 
     def _rope(self, x, rotary, positions, from_a, to_a, inverse, out, stream):
-        import torch
-        code = self._type()
-        shapes = (self.in_shape(0), self.out_shape(0))
-        self._check(x, shapes[from_a], "input")
+        specs = self.__dict__.setdefault("_rope_specs", {})
+        spec = specs.get(rotary.naxes)
+        if spec is None:
+            import torch
+            SG, a = self.S_local * self.w, rotary.naxes
+            spec = specs[a] = (self._type(), (self.in_shape(0), self.out_shape(0)), (a, SG), (a, self.B, SG), torch.int32)
+        code, shapes, one, each, int32 = spec
+        if not self._fits(x, self.dtype, shapes[from_a]):
+            self._check(x, shapes[from_a], "input")
         if rotary.D != self.D:
             raise ValueError(f"rotary is for heads of {rotary.D}, the plan has {self.D}")
-        if rotary.turns.device != self.device or rotary.axes.device != self.device:
-            raise ValueError(f"rotary is on {rotary.turns.device}, plan is on {self.device}")
-        SG = self.S_local * self.w
-        one, each = (rotary.naxes, SG), (rotary.naxes, self.B, SG)
-        if positions.dim() == 3 and positions.shape[1] == 1 and self.B != 1:
-            positions = positions[:, 0]                       # one plane for all
+        turns, axes = rotary.turns, rotary.axes
+        if turns.device != self.device or axes.device != self.device:
+            raise ValueError(f"rotary is on {turns.device}, plan is on {self.device}")
         planes = positions.dim() == 3
-        self._expect(positions, torch.int32, each if planes else one, "positions")
+        if planes and positions.shape[1] == 1:
+            positions, planes = positions[:, 0], False            # one plane for all
+        if not self._fits(positions, int32, each if planes else one):
+            self._expect(positions, int32, each if planes else one, "positions")
         if out is None:
+            import torch
             with self._on_stream(stream):
                 out = torch.empty(shapes[to_a], dtype=self.dtype, device=self.device)
-        else:
+        elif not self._fits(out, self.dtype, shapes[to_a]):
             self._check(out, shapes[to_a], "output")
-        args = ua2a_rope_t(x.data_ptr(), out.data_ptr(), positions.data_ptr(), rotary.turns.data_ptr(),
-                           rotary.axes.data_ptr(), rotary.pairs, rotary.naxes, rotary.halves, bool(inverse), planes,
-                           from_a, to_a, code)
+        args = ua2a_rope_t(x.data_ptr(), out.data_ptr(), positions.data_ptr(), turns.data_ptr(), axes.data_ptr(),
+                           rotary.pairs, rotary.naxes, rotary.halves, bool(inverse), planes, from_a, to_a, code)
         self._issue("ua2a_rope", stream, ctypes.byref(args))
         return out
 
@@ -206,68 +211,77 @@ class AttentionCalls:
 
     # --------------------------------------------------------------- attention
 
-    def _window(self, left, right, sinks, chunk) -> ua2a_window_t:
-        sinks, chunk = int(sinks), int(chunk)
-        if sinks < 0 or chunk < 1:
-            raise ValueError(f"sinks must be at least 0 and chunk at least 1, not {sinks} and {chunk}")
-        w = (_bound(left, "left"), _bound(right, "right"), sinks, chunk)
-        if max(w) >= 1 << 31:
-            raise ValueError(f"a window's sizes must be below 2^31, got {w}")
-        return ua2a_window_t(*w)
-
-    def _attention_type(self) -> int:
+    def _attention_spec(self, kind, heads, sizes, left, right, sinks, chunk, scale):
+        """What a kind of call needs, worked out once: (type code, window, scale, key
+        heads on all ranks, bytes of scratch).  heads: key heads of a rank; sizes:
+        (sequences, capacity, n) of a cache's call, else None."""
+        specs = self.__dict__.setdefault("_attention_specs", {})
+        key = (kind, heads, sizes, left, right, sinks, chunk, scale)
+        spec = specs.get(key)
+        if spec is not None:
+            return spec
         code = self._type()
         if code == 2:
             raise TypeError("attention takes bfloat16 and float16 plans, not float32")
         if self.D % 8 or self.D > 128:
             raise ValueError(f"attention takes heads of a multiple of 8 values up to 128, not {self.D}")
-        return code
-
-    def _scale(self, scale) -> float:
+        sinks, chunk = int(sinks), int(chunk)
+        if sinks < 0 or chunk < 1:
+            raise ValueError(f"sinks must be at least 0 and chunk at least 1, not {sinks} and {chunk}")
+        bounds = (_bound(left, "left"), _bound(right, "right"), sinks, chunk)
+        if max(bounds) >= 1 << 31:
+            raise ValueError(f"a window's sizes must be below 2^31, got {bounds}")
         scale = self.D ** -0.5 if scale is None else float(scale)
         if not 0.0 < scale < 3.4e38:
             raise ValueError(f"scale must be positive and finite, not {scale}")
-        return scale
-
-    def _kv_heads(self, heads: int, what: str) -> int:
-        """Key heads on all ranks from those of one."""
         if heads < 1 or (self.H // self.w) % heads:
-            raise ValueError(f"{what} has {heads} heads per rank, which does not divide the plan's {self.H // self.w}")
-        return heads * self.w
+            raise ValueError(f"{heads} key heads per rank do not divide the plan's {self.H // self.w}")
+        window, kv, need = ua2a_window_t(*bounds), heads * self.w, ctypes.c_int64()
+        lib = _pkg._lib or _pkg.load_library()
+        if kind == "cache":
+            cache = ua2a_cache_t(None, None, sizes[0], sizes[1], 1)
+            args = ua2a_cache_attention_t(window=window, n=sizes[2], kv_heads=kv, scale=scale, type=code)
+            rc = lib.ua2a_cache_attention_workspace(self.handle, ctypes.byref(cache), ctypes.byref(args), ctypes.byref(need))
+        elif kind == "backward":
+            args = ua2a_attention_grad_t(window=window, kv_heads=kv, scale=scale, type=code)
+            rc = lib.ua2a_attention_backward_workspace(self.handle, ctypes.byref(args), ctypes.byref(need))
+        else:
+            args = ua2a_attention_t(window=window, kv_heads=kv, scale=scale, type=code)
+            rc = lib.ua2a_attention_workspace(self.handle, ctypes.byref(args), ctypes.byref(need))
+        if rc != UA2A_OK:
+            raise UA2AError(rc, "ua2a_attention_workspace")
+        if len(specs) >= 1024:
+            specs.clear()
+        spec = specs[key] = (code, window, scale, kv, need.value)
+        return spec
 
     def _check_heads(self, q, k, v, counts):
-        """Checks a call's tensors and returns the key heads on all ranks."""
-        import torch
-        self._check(q, self.out_shape(0), "q")
-        w, B, SG, _, D = self.out_shape(0)
+        """Checks a call's tensors and returns the key heads of a rank."""
+        gathered = self.__dict__.get("_gathered")
+        if gathered is None:
+            import torch
+            gathered = self._gathered = (self.out_shape(0), torch.int32)
+        shape, int32 = gathered
+        if not self._fits(q, self.dtype, shape):
+            self._check(q, shape, "q")
         if k.dim() != 5:
             raise ValueError(f"k must be [w, B, S_local*w, heads, D], got {tuple(k.shape)}")
-        kv = self._kv_heads(k.shape[3], "k")
-        shape = (w, B, SG, kv // w, D)
-        self._check(k, shape, "k")
-        self._check(v, shape, "v")
-        if counts is not None:
-            self._expect(counts, torch.int32, (B,), "counts")
-        return kv
+        heads = k.shape[3]
+        kshape = shape[:3] + (heads, shape[4])
+        for t, what in ((k, "k"), (v, "v")):
+            if not self._fits(t, self.dtype, kshape):
+                self._check(t, kshape, what)
+        if counts is not None and not self._fits(counts, int32, (self.B,)):
+            self._expect(counts, int32, (self.B,), "counts")
+        return heads
 
-    def _space(self, name, key, call, stream):
-        """Scratch for a call, None where it takes none: (tensor, bytes).  How much
-        a kind of call takes is asked once."""
-        import torch
-        needs = self.__dict__.setdefault("_attention_space", {})
-        need = needs.get((name,) + key)
-        if need is None:
-            n = ctypes.c_int64()
-            rc = call(ctypes.byref(n))
-            if rc != UA2A_OK:
-                raise UA2AError(rc, name)
-            if len(needs) >= 1024:
-                needs.clear()
-            need = needs[(name,) + key] = n.value
+    def _space(self, need, stream):
+        """Scratch of `need` bytes for a call, None for 0."""
         if need == 0:
-            return None, 0
+            return None
+        import torch
         with self._on_stream(stream):
-            return torch.empty(need, dtype=torch.uint8, device=self.device), need
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
 
     def window_attention(self, q, k, v, *, left=None, right=None, sinks: int = 0, chunk: int = 1, counts=None,
                          scale=None, lse: bool = False, out: Optional[Attention] = None, stream=None) -> Attention:
@@ -282,29 +296,25 @@ class AttentionCalls:
         earlier result to write again.  bfloat16 and float16, D a multiple of 8
         up to 128.
         """
-        import torch
-        code = self._attention_type()
-        window = self._window(left, right, sinks, chunk)
-        scale = self._scale(scale)
-        kv = self._check_heads(q, k, v, counts)
-        w, B, SG, hl, D = self.out_shape(0)
-        stats = (w, B, hl, SG)
+        heads = self._check_heads(q, k, v, counts)
+        code, window, scale, kv, need = self._attention_spec("forward", heads, None, left, right, sinks, chunk, scale)
+        if out is None or lse:
+            import torch
+            w, B, SG, hl, _ = self.out_shape(0)
+            stats = (w, B, hl, SG)
         if out is None:
             with self._on_stream(stream):
                 out = Attention(torch.empty(q.shape, dtype=self.dtype, device=self.device),
                                 torch.empty(stats, dtype=torch.float32, device=self.device) if lse else None)
         else:
-            self._check(out.out, self.out_shape(0), "out.out")
+            if not self._fits(out.out, self.dtype, q.shape):
+                self._check(out.out, q.shape, "out.out")
             if lse:
                 self._expect(out.lse, torch.float32, stats, "out.lse")
             out = Attention(out.out, out.lse if lse else None)
+        space = self._space(need, stream)
         args = ua2a_attention_t(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.out.data_ptr(), _ptr(out.lse), _ptr(counts),
-                                None, 0, window, kv, scale, code)
-        lib = _pkg._lib or _pkg.load_library()
-        space, args.workspace_bytes = self._space(
-            "ua2a_attention_workspace", (kv, window.left, window.right, window.sinks, window.chunk),
-            lambda n: lib.ua2a_attention_workspace(self.handle, ctypes.byref(args), n), stream)
-        args.workspace = _ptr(space)
+                                _ptr(space), need, window, kv, scale, code)
         self._issue("ua2a_attention", stream, ctypes.byref(args))
         return out
 
@@ -316,13 +326,11 @@ class AttentionCalls:
         results.  Sums run in a fixed order, so equal inputs give equal bits.
         ``grads``: an earlier result to write again."""
         import torch
-        code = self._attention_type()
-        window = self._window(left, right, sinks, chunk)
-        scale = self._scale(scale)
-        kv = self._check_heads(q, k, v, counts)
-        w, B, SG, hl, D = self.out_shape(0)
-        self._check(dout, self.out_shape(0), "dout")
-        self._check(out, self.out_shape(0), "out")
+        heads = self._check_heads(q, k, v, counts)
+        code, window, scale, kv, need = self._attention_spec("backward", heads, None, left, right, sinks, chunk, scale)
+        w, B, SG, hl, _ = shape = self.out_shape(0)
+        self._check(dout, shape, "dout")
+        self._check(out, shape, "out")
         self._expect(lse, torch.float32, (w, B, hl, SG), "lse")
         if grads is None:
             with self._on_stream(stream):
@@ -331,14 +339,11 @@ class AttentionCalls:
         else:
             for t, like, what in zip(grads, (q, k, v), AttentionGradients._fields):
                 self._check(t, like.shape, f"grads.{what}")
+            grads = AttentionGradients(*grads)
+        space = self._space(need, stream)
         args = ua2a_attention_grad_t(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                     lse.data_ptr(), *[t.data_ptr() for t in grads], _ptr(counts), None, 0, window, kv,
-                                     scale, code)
-        lib = _pkg._lib or _pkg.load_library()
-        space, args.workspace_bytes = self._space(
-            "ua2a_attention_backward_workspace", (kv, window.left, window.right, window.sinks, window.chunk),
-            lambda n: lib.ua2a_attention_backward_workspace(self.handle, ctypes.byref(args), n), stream)
-        args.workspace = _ptr(space)
+                                     lse.data_ptr(), *[t.data_ptr() for t in grads], _ptr(counts), _ptr(space), need, window,
+                                     kv, scale, code)
         self._issue("ua2a_attention_backward", stream, ctypes.byref(args))
         return grads
 
@@ -356,31 +361,25 @@ class AttentionCalls:
         without a position are left as they were; without ``out`` they are
         zeros (where there can be any, that fills the result first).
         """
-        import torch
-        code = self._attention_type()
-        window = self._window(left, right, sinks, chunk)
-        scale = self._scale(scale)
         self._check_cache_of(cache, None, starts, counts)
-        kv = self._kv_heads(cache.heads, "cache")
         if starts is None:
             raise ValueError("starts is missing")
         n = q.shape[2] if q.dim() == 5 else 0
         shape = (self.w, cache.sequences, n, self.H // self.w, self.D)
-        self._check(q, shape, "q")
+        if not self._fits(q, self.dtype, shape):
+            self._check(q, shape, "q")
         if n < 1:
             raise ValueError("q has no tokens")
+        code, window, scale, kv, need = self._attention_spec("cache", cache.heads, (cache.sequences, cache.capacity, n), left,
+                                                             right, sinks, chunk, scale)
         if out is None:
+            import torch
             with self._on_stream(stream):
                 out = torch.zeros(shape, dtype=self.dtype, device=self.device)
-        else:
+        elif not self._fits(out, self.dtype, shape):
             self._check(out, shape, "out")
-        args = ua2a_cache_attention_t(q.data_ptr(), out.data_ptr(), starts.data_ptr(), _ptr(counts), None, 0, window, n, kv,
-                                      scale, code)
-        lib = _pkg._lib or _pkg.load_library()
-        space, args.workspace_bytes = self._space(
-            "ua2a_cache_attention_workspace",
-            (cache.sequences, cache.capacity, kv, n, window.left, window.right, window.sinks, window.chunk),
-            lambda b: lib.ua2a_cache_attention_workspace(self.handle, cache._ref, ctypes.byref(args), b), stream)
-        args.workspace = _ptr(space)
+        space = self._space(need, stream)
+        args = ua2a_cache_attention_t(q.data_ptr(), out.data_ptr(), starts.data_ptr(), _ptr(counts), _ptr(space), need, window,
+                                      n, kv, scale, code)
         self._issue("ua2a_cache_attention", stream, cache._ref, ctypes.byref(args))
         return out

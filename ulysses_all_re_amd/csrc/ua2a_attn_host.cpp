@@ -300,11 +300,13 @@ int ua2a_rope(ua2a_plan_t plan, const ua2a_rope_t* n, void* stream)
         g.turning = g.pairs / v;
         g.slots = g.turning + rest / v;
     }
-    // a token's lanes: as many heads as divide H and fit a wave, but a lane turns
-    // four heads at least, which its angles serve (16 heads of 64 in halves, 50 MB:
-    // 26 us with one head a lane)
+    // a token's lanes: as many heads as divide H and fit a wave, but in a call that
+    // fills the device a lane turns four heads at least, which its angles serve
+    // (16 heads of 64 in halves, 50 MB: 17 us, 26 with one head a lane; 32 tokens:
+    // 5.9 us with four, 5.2 with one)
+    const uint32_t least_heads = tokens_of(plan) * g.sh.H * g.slots >= (1 << 18) ? 4 : 1;
     g.heads_at_once = 1;
-    for (uint32_t k = 1; k * 4 <= g.sh.H && k * g.slots <= 64; ++k)
+    for (uint32_t k = 1; k * least_heads <= g.sh.H && k * g.slots <= 64; ++k)
         if (g.sh.H % k == 0) g.heads_at_once = k;
     g.lanes = least(g.slots * g.heads_at_once, kRopeBlock);
     g.per_group = kRopeBlock / g.lanes;
