@@ -184,8 +184,8 @@ int64_t most_seers(const AttnGeom& g)
 // How the keys' gradients go to workgroups.  Sinks are seen by all rows, other
 // keys by a window of them, so a tile of sinks would be walked long after the
 // rest: tiles are walked in parts of about a window, and of less where the call
-// is small: as much as leaves two parts for each workgroup that the device
-// holds at once (512), but 512 rows at least, for a part's sums go through the
+// is small: as much as leaves a part for each workgroup that the device holds
+// at once (512), but 512 rows at least, for a part's sums go through the
 // workspace (no more than 64 parts of a tile, and 256 MiB).
 void backward_shape(AttnGradArgs* a)
 {
@@ -196,14 +196,14 @@ void backward_shape(AttnGradArgs* a)
     const int64_t lead = most < g.rows ? ceil_div(sinks, kAttnGradKeys) : 0;
     const int64_t span = lead * kAttnGradKeys < g.keys ? lead * kAttnGradKeys : g.keys;
     const int64_t all = g.units * (lead * g.rows + (tiles - lead) * most);
-    int64_t part = all / 1024 < most ? all / 1024 : most;
+    int64_t part = all / 512 < most ? all / 512 : most;
     if (part < 512) part = 512;
     int64_t first, rest;
     for (;; part *= 2) {
-        first = ceil_div(g.rows, part);
-        rest = ceil_div(most, part);
-        first = lead == 0 ? 1 : first > 64 ? 64 : first;
-        rest = rest > 64 ? 64 : rest;
+        first = (g.rows + part / 2) / part;                      // the nearest
+        rest = (most + part / 2) / part;
+        first = lead == 0 || first < 1 ? 1 : first > 64 ? 64 : first;
+        rest = rest < 1 ? 1 : rest > 64 ? 64 : rest;
         const int64_t lines = (first > 1 ? first * span : 0) + (rest > 1 ? rest * (g.keys - span) : 0);
         if (lines * g.units * g.D * 8 <= (int64_t(256) << 20)) break;
     }
