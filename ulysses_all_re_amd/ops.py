@@ -32,6 +32,10 @@ it in mode 1 (a sub-layer norm, with the residual's addition), each in one
 launch forward and one or two backward.  ``checkpoint`` keeps what the backward
 pass needs of the activations in 8 bits, a little over half a 2-byte type.
 
+``rope_all_to_all_4D`` is the same entry point with rotary positions, in one
+launch either way, and ``window_attention`` the attention of what mode 0
+gathers, over a sliding window and sinks; both have gradients.
+
 Both caches are bounded: at most ``MAX_PLANS`` plans and ``MAX_WINDOWS``
 windows are kept, the least recently used going first (a window's plans go
 with it).  A dropped window returns to torch's allocator in its own stream's
@@ -48,7 +52,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import Plan
+from . import Plan, Rotary
 
 MAX_PLANS = 64
 MAX_WINDOWS = 8
@@ -346,3 +350,157 @@ def norm_all_to_all_4D(x: torch.Tensor, weight: Optional[torch.Tensor], scatter_
     if out_format:
         out = (out, scales)
     return out if residual is None else (out, total)
+
+
+# ------------------------------------------------- rotary positions, attention
+
+
+def _rotary(D: int, turns, axes, naxes: int, halves: bool) -> Rotary:
+    """The Rotary that an operator's tensors are of."""
+    r = Rotary.__new__(Rotary)
+    r.D, r.pairs, r.naxes, r.halves = D, turns.numel(), naxes, halves
+    r.turns, r.axes, r.device = turns, axes, turns.device
+    return r
+
+
+@torch.library.custom_op("ua2a::rope_exchange", mutates_args=())
+def rope_exchange(x: torch.Tensor, positions: torch.Tensor, turns: torch.Tensor, axes: torch.Tensor, w: int, mode: int,
+                  naxes: int, halves: bool, inverse: bool) -> torch.Tensor:
+    """Rotary positions joined with the rank-stacked exchange on the GPU, as
+    ``Plan.rope_exchange``; turns, axes, naxes and halves are a Rotary's."""
+    if mode not in (0, 1):
+        raise ValueError("mode must be 0 or 1")
+    if x.device.type != "cuda":
+        raise RuntimeError(f"the exchange runs on the GPU only (got a {x.device.type} tensor)")
+    B, S, H, D = _local_shape(x.shape, w, mode)
+    with _lock:
+        plan = _plan_for(w, B, S, H, D, x.dtype, x.device)
+        return plan.rope_exchange(x.contiguous(), _rotary(D, turns, axes, naxes, halves), positions.contiguous(), mode, inverse)
+
+
+@rope_exchange.register_fake
+def _rope_exchange_fake(x, positions, turns, axes, w, mode, naxes, halves, inverse):
+    return x.new_empty(_out_shape(x.shape, w, mode))
+
+
+def _rope_setup_context(ctx, inputs, output):
+    _, positions, turns, axes, w, mode, naxes, halves, inverse = inputs
+    ctx.save_for_backward(positions, turns, axes)
+    ctx.args = (w, mode, naxes, halves, inverse)
+
+
+def _rope_backward(ctx, grad):
+    # a rotation's transpose turns the other way, an exchange's is its inverse
+    positions, turns, axes = ctx.saved_tensors
+    w, mode, naxes, halves, inverse = ctx.args
+    dx = rope_exchange(grad.contiguous(), positions, turns, axes, w, 1 - mode, naxes, halves, not inverse)
+    return dx, None, None, None, None, None, None, None, None
+
+
+rope_exchange.register_autograd(_rope_backward, setup_context=_rope_setup_context)
+
+
+def rope_all_to_all_4D(x: torch.Tensor, rotary: Rotary, positions: torch.Tensor, scatter_dim: int, gather_dim: int, w: int,
+                       inverse: bool = False) -> torch.Tensor:
+    """``all_to_all_4D`` with rotary positions, in one launch.
+
+    ``rotary``: a :class:`Rotary`.  ``positions``: int32 ``[axes, S_local*w]``
+    or ``[axes, B, S_local*w]``, tokens in gathered order.  ``inverse`` turns
+    the other way.  The gradient of x is the same call the other way round.
+    """
+    if (scatter_dim, gather_dim) == (2, 1):
+        mode = 0
+    elif (scatter_dim, gather_dim) == (1, 2):
+        mode = 1
+    else:
+        raise ValueError(f"unsupported (scatter_dim, gather_dim) = ({scatter_dim}, {gather_dim}); "
+                         "use (2, 1) for heads -> sequence or (1, 2) for the inverse")
+    return rope_exchange(x, positions, rotary.turns, rotary.axes, w, mode, rotary.naxes, rotary.halves, inverse)
+
+
+def _attention_plan(q, k, w: int) -> Plan:
+    """The plan of gathered queries ``[w, B, S, heads, D]`` (caller holds _lock)."""
+    if q.device.type != "cuda":
+        raise RuntimeError(f"attention runs on the GPU only (got a {q.device.type} tensor)")
+    B, S, H, D = _local_shape(q.shape, w, 1)
+    return _plan_for(w, B, S, H, D, q.dtype, q.device)
+
+
+@torch.library.custom_op("ua2a::window_attention", mutates_args=())
+def _window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, counts: Optional[torch.Tensor], w: int,
+                      left: Optional[int], right: Optional[int], sinks: int, chunk: int, scale: Optional[float],
+                      lse: bool) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(out, lse) of ``Plan.window_attention``; lse is empty where it is not asked for."""
+    with _lock:
+        plan = _attention_plan(q, k, w)
+        r = plan.window_attention(q.contiguous(), k.contiguous(), v.contiguous(), left=left, right=right, sinks=sinks,
+                                  chunk=chunk, counts=None if counts is None else counts.contiguous(), scale=scale, lse=lse)
+    return r.out, r.lse if lse else q.new_empty(0, dtype=torch.float32)
+
+
+@_window_attention.register_fake
+def _window_attention_fake(q, k, v, counts, w, left, right, sinks, chunk, scale, lse):
+    _, B, SG, hl, _ = q.shape
+    return (torch.empty_like(q, memory_format=torch.contiguous_format),
+            q.new_empty((w, B, hl, SG) if lse else (0,), dtype=torch.float32))
+
+
+@torch.library.custom_op("ua2a::window_attention_backward", mutates_args=())
+def _window_attention_grads(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                            lse: torch.Tensor, counts: Optional[torch.Tensor], w: int, left: Optional[int],
+                            right: Optional[int], sinks: int, chunk: int, scale: Optional[float]) -> Tuple[
+                                torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dq, dk, dv) of ``Plan.window_attention_backward``."""
+    with _lock:
+        plan = _attention_plan(q, k, w)
+        r = plan.window_attention_backward(dout.contiguous(), q.contiguous(), k.contiguous(), v.contiguous(), out, lse,
+                                           left=left, right=right, sinks=sinks, chunk=chunk, scale=scale,
+                                           counts=None if counts is None else counts.contiguous())
+    return r.dq, r.dk, r.dv
+
+
+@_window_attention_grads.register_fake
+def _window_attention_grads_fake(dout, q, k, v, out, lse, counts, w, left, right, sinks, chunk, scale):
+    return tuple(torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k, v))
+
+
+def _attention_setup_context(ctx, inputs, output):
+    q, k, v, counts, w, left, right, sinks, chunk, scale, lse = inputs
+    out, stats = output
+    ctx.mark_non_differentiable(stats)
+    ctx.set_materialize_grads(False)
+    ctx.args = (w, left, right, sinks, chunk, scale)
+    ctx.has = lse
+    ctx.save_for_backward(q, k, v, out, stats, counts)
+
+
+def _attention_backward(ctx, g_out, g_stats):
+    if g_out is None:
+        return (None,) * 11
+    if not ctx.has:
+        raise RuntimeError("a call without lse has no gradient")
+    q, k, v, out, stats, counts = ctx.saved_tensors
+    dq, dk, dv = _window_attention_grads(g_out, q, k, v, out, stats, counts, *ctx.args)
+    needs = ctx.needs_input_grad
+    return (dq if needs[0] else None, dk if needs[1] else None, dv if needs[2] else None) + (None,) * 8
+
+
+_window_attention.register_autograd(_attention_backward, setup_context=_attention_setup_context)
+
+
+def window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, w: int, left: Optional[int] = None,
+                     right: Optional[int] = None, sinks: int = 0, chunk: int = 1, counts: Optional[torch.Tensor] = None,
+                     scale: Optional[float] = None) -> torch.Tensor:
+    """softmax(scale q k^T) v of gathered heads ``[w, B, S, heads, D]`` (what mode 0
+    gives), over a sliding window and sinks; k and v may have fewer heads.
+
+    A query at position p sees, with c(x) = x // chunk, the positions j with
+    ``c(p) - left <= c(j) <= c(p) + right`` (None: no bound) and the first
+    ``sinks``; with ``right=0`` nothing past its own chunk.  ``counts``: int32
+    ``[B]`` on the device, the tokens of each plane's sequences; the rest is
+    padding, whose rows and gradients are zeros.  bfloat16 and float16, D a
+    multiple of 8 up to 128.  q, k and v have gradients.
+    """
+    wants = torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v))
+    out, _ = _window_attention(q, k, v, counts, w, left, right, sinks, chunk, scale, wants)
+    return out
