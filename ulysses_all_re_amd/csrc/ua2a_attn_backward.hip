@@ -61,7 +61,10 @@ __device__ __forceinline__ void store_row(void* out, int64_t at, uint32_t D, con
 
 // dq, and delta for the other kernel.  As forward, a wave has 32 rows as columns
 // of its matrix tiles and walks tiles of 64 keys: scores and dout v^T come as
-// keys x rows, dS goes on to its product with k from the registers it is in.
+// keys x rows, dS goes on to its product with k from the registers it is in.  A
+// row's dS add up to zero, so what rounding leaves of them weighs more than in the
+// other sums; dS goes in as two values of the type (an error of dq of 1.45 times
+// its own rounding's falls to 1.0 times; three products become four).
 template <class T, int DP>
 __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(AttnGradArgs a)
 {
@@ -155,10 +158,15 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
                         if (!sees(seen, bk0 + static_cast<int32_t>((x / 4) * 8 + half * 4 + x % 4))) dp[x] = 0.f;
                 }
                 const u32x4v ds[2] = {operand_of<T>(dp, 0), operand_of<T>(dp, 1)};
+                const u32x4v rest[2] = {rest_of<T>(dp, ds[0], 0), rest_of<T>(dp, ds[1], 1)};
 #pragma unroll
                 for (int db = 0; db < DP / 32; ++db)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) dq[db] = mfma<T>(transposed<DP>(ktile, b * 32, t, db), ds[t], dq[db]);
+                    for (int t = 0; t < 2; ++t) {
+                        const u32x4v k = transposed<DP>(ktile, b * 32, t, db);
+                        dq[db] = mfma<T>(k, ds[t], dq[db]);
+                        dq[db] = mfma<T>(k, rest[t], dq[db]);
+                    }
             }
             char* const t = ktile;
             ktile = other;

@@ -52,6 +52,19 @@ __device__ __forceinline__ u32x4v operand_of(const f32x16v& c, int s)
     return r;
 }
 
+// What that rounding left of them, rounded itself.
+template <class T>
+__device__ __forceinline__ u32x4v rest_of(const f32x16v& c, u32x4v rounded, int s)
+{
+    u32x4v r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const auto x = pair_of<T>(rounded[i]);
+        r[i] = pack2<T>(c[8 * s + 2 * i] - static_cast<float>(x[0]), c[8 * s + 2 * i + 1] - static_cast<float>(x[1]));
+    }
+    return r;
+}
+
 // The largest, and the sum, of a value and the other half's (lane 32 places on or back).
 __device__ __forceinline__ float max_halves(float x)
 {
