@@ -50,7 +50,7 @@ __global__ __launch_bounds__(kRopeBlock) void ua2a_rope_kernel(RopeArgs a)
 {
     constexpr bool kTwo = HALVES || V == 1;                      // a slot's pairs lie in two vectors
     constexpr int NP = kTwo ? V : V / 2;
-    constexpr int kBatch = 4;                                    // heads whose loads are in flight
+    constexpr int kBatch = 4;                                    // heads whose loads are on their way together
     typedef typename Raw<T, V>::type R;
     const RopeGeom& g = a.g;
     const uint32_t wg = (blockIdx.y << kAttnGridLog) + blockIdx.x;
@@ -76,6 +76,23 @@ __global__ __launch_bounds__(kRopeBlock) void ua2a_rope_kernel(RopeArgs a)
         } else {
             d = slot * V;
         }
+        const auto offset = [&](uint32_t h, bool a_side) {
+            return a_side ? a_offset(g.sh, at.a, h, D, g.sh.a_rank, d) : (static_cast<int64_t>(at.p) * H + h) * D + d;
+        };
+        const bool two = kTwo && pairs_here;
+        R lo[kBatch], hi[kTwo ? kBatch : 1];
+        const auto load = [&](uint32_t h) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const uint32_t hh = h + k * g.heads_at_once;
+                if (hh >= H) continue;
+                const int64_t from = offset(hh, g.from_a);
+                lo[k] = load_values<T, V>(a.x, from);
+                if constexpr (kTwo)
+                    if (two) hi[k] = load_values<T, V>(a.x, from + far);
+            }
+        };
+        load(h0);                                                // on their way while the angles are worked out
         float c[NP], s[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -91,21 +108,7 @@ __global__ __launch_bounds__(kRopeBlock) void ua2a_rope_kernel(RopeArgs a)
                 if (g.inverse) s[i] = -s[i];
             }
         }
-        const auto offset = [&](uint32_t h, bool a_side) {
-            return a_side ? a_offset(g.sh, at.a, h, D, g.sh.a_rank, d) : (static_cast<int64_t>(at.p) * H + h) * D + d;
-        };
-        const bool two = kTwo && pairs_here;
-        for (uint32_t h = h0; h < H; h += g.heads_at_once * kBatch) {
-            R lo[kBatch], hi[kTwo ? kBatch : 1];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const uint32_t hh = h + k * g.heads_at_once;
-                if (hh >= H) continue;
-                const int64_t from = offset(hh, g.from_a);
-                lo[k] = load_values<T, V>(a.x, from);
-                if constexpr (kTwo)
-                    if (two) hi[k] = load_values<T, V>(a.x, from + far);
-            }
+        const auto turn = [&](uint32_t h) {
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const uint32_t hh = h + k * g.heads_at_once;
@@ -132,13 +135,18 @@ __global__ __launch_bounds__(kRopeBlock) void ua2a_rope_kernel(RopeArgs a)
 #pragma unroll
                     for (int i = 0; i < NP; ++i) {
                         // past the pairs values stay as they are, infinities too
-                        const bool turn = d / 2 + i < g.pairs;
-                        u[2 * i] = turn ? __builtin_fmaf(x[2 * i], c[i], -(x[2 * i + 1] * s[i])) : x[2 * i];
-                        u[2 * i + 1] = turn ? __builtin_fmaf(x[2 * i + 1], c[i], x[2 * i] * s[i]) : x[2 * i + 1];
+                        const bool turns = d / 2 + i < g.pairs;
+                        u[2 * i] = turns ? __builtin_fmaf(x[2 * i], c[i], -(x[2 * i + 1] * s[i])) : x[2 * i];
+                        u[2 * i + 1] = turns ? __builtin_fmaf(x[2 * i + 1], c[i], x[2 * i] * s[i]) : x[2 * i + 1];
                     }
                     store_values<T, V>(a.out, to, pack<T, V>(u));
                 }
             }
+        };
+        const uint32_t batch = g.heads_at_once * kBatch;
+        for (uint32_t h = h0; h < H; h += batch) {
+            turn(h);
+            load(h + batch);
         }
     }
 }
