@@ -293,7 +293,7 @@ struct RopeGeom {
     uint32_t heads_at_once;      // heads that a token's lanes take at once
     uint32_t lanes;              // of a token
     uint32_t per_group;          // tokens of a workgroup
-    Div32 d_lanes, d_slots, d_SG;
+    Div32 d_lanes, d_slots, d_SG, d_pairs;
 };
 
 }  // namespace ua2a

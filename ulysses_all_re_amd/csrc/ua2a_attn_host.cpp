@@ -313,6 +313,7 @@ int ua2a_rope(ua2a_plan_t plan, const ua2a_rope_t* n, void* stream)
     g.d_lanes = make_div32(g.lanes);
     g.d_slots = make_div32(g.slots);
     g.d_SG = make_div32(g.sh.SG);
+    g.d_pairs = make_div32(g.pairs);
     const int64_t bytes = plan->layout.tensor_bytes;
     const Range ins[] = {{n->positions, each * n->naxes * 4}, {n->turns, int64_t(n->pairs) * 8},
                          {n->axes, int64_t(n->pairs) * 4},

@@ -1,8 +1,8 @@
 // gfx950 kernel of rotary positions, joined with the exchange or within a
 // layout (ua2a_attn.h).  Each value is read once and written once, so HBM
-// bandwidth bounds it; what the angles cost is kept off that path by working
-// out a lane's cosines and sines once for a token and using them for every
-// head that the lane turns.
+// bandwidth bounds it, as long as what the angles cost is kept off that path: a
+// workgroup works out its tokens' cosines and sines once, a pair a lane, and
+// hands them round in LDS.
 #include "ua2a_act_device.h"
 #include "ua2a_attn_internal.h"
 
@@ -40,12 +40,31 @@ __device__ __forceinline__ void cos_sin(uint32_t turn, float* c, float* s)
     *s = (quarter & 2) != 0 ? -b : b;
 }
 
+// The angle of a pair for the token in place `where` of the positions.
+__device__ __forceinline__ void angle_of(const RopeArgs& a, uint32_t pair, uint32_t where, float* c, float* s)
+{
+    const RopeGeom& g = a.g;
+    int32_t axis = a.axes[pair];
+    axis = axis < 0 ? 0 : axis;
+    axis = axis < static_cast<int32_t>(g.naxes) ? axis : static_cast<int32_t>(g.naxes) - 1;
+    const int32_t pos = a.positions[static_cast<int64_t>(axis) * g.axis_stride + where];
+    cos_sin(turn_of(pos, a.turns[pair]), c, s);
+    if (g.inverse) *s = -*s;
+}
+
+__device__ __forceinline__ uint32_t position_of(const RopeGeom& g, const TokenPlace& at)
+{
+    return g.per_plane ? at.a : at.a - fdiv(at.a, g.d_SG) * g.sh.SG;
+}
+
 // A lane turns slot `slot` of a head for every `heads_at_once`-th head of a
 // token.  A slot is V values at d (pairs side by side, V / 2 of them; or, past
 // the pairs, values to copy), with HALVES V values at d and V at d + pairs
 // (those slots come first, then the values to copy), and with V = 1 one pair
-// either way, or one value.
-template <class T, int V, bool HALVES>
+// either way, or one value.  TABLE: the angles come from LDS (video-DiT: 270 us
+// with each lane's own); otherwise a lane works its own out (V = 1, and heads of
+// more than 256 slots).
+template <class T, int V, bool HALVES, bool TABLE>
 __global__ __launch_bounds__(kRopeBlock) void ua2a_rope_kernel(RopeArgs a)
 {
     constexpr bool kTwo = HALVES || V == 1;                      // a slot's pairs lie in two vectors
@@ -53,17 +72,20 @@ __global__ __launch_bounds__(kRopeBlock) void ua2a_rope_kernel(RopeArgs a)
     constexpr int kBatch = 4;                                    // heads whose loads are on their way together
     typedef typename Raw<T, V>::type R;
     const RopeGeom& g = a.g;
+    // [token][pair]: at most 256 / slots tokens of slots * V pairs
+    __shared__ f32x2v table[TABLE ? kRopeBlock * (HALVES ? V : V / 2) : 1];
     const uint32_t wg = (blockIdx.y << kAttnGridLog) + blockIdx.x;
     const uint32_t within = fdiv(threadIdx.x, g.d_lanes), lane = threadIdx.x - within * g.lanes;
-    const int64_t token64 = static_cast<int64_t>(wg) * g.per_group + within;
-    if (within >= g.per_group || token64 >= static_cast<int64_t>(g.tokens)) return;
-    const uint32_t token = static_cast<uint32_t>(token64);
-    const TokenPlace at = token_place(g.sh, token);
-    const uint32_t plane = fdiv(at.a, g.d_SG);
-    const uint32_t where = g.per_plane ? at.a : at.a - plane * g.sh.SG;
+    const int64_t first = static_cast<int64_t>(wg) * g.per_group;
+    const bool in = within < g.per_group && first + within < static_cast<int64_t>(g.tokens);
+    if constexpr (!TABLE) {
+        if (!in) return;
+    }
+    const TokenPlace at = token_place(g.sh, in ? static_cast<uint32_t>(first + within) : 0);
+    const uint32_t where = position_of(g, at);
     const uint32_t h0 = fdiv(lane, g.d_slots);
     const uint32_t D = g.sh.D, H = g.sh.H, turning = g.turning;
-    for (uint32_t slot = lane - h0 * g.slots; slot < g.slots; slot += g.lanes) {
+    for (uint32_t slot = lane - h0 * g.slots; TABLE || slot < g.slots; slot += g.lanes) {
         // first value, the second vector's distance, and which of the pairs turn
         const bool pairs_here = slot < turning;
         uint32_t d, far = 0;
@@ -85,7 +107,7 @@ __global__ __launch_bounds__(kRopeBlock) void ua2a_rope_kernel(RopeArgs a)
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const uint32_t hh = h + k * g.heads_at_once;
-                if (hh >= H) continue;
+                if (hh >= H || !in) continue;
                 const int64_t from = offset(hh, g.from_a);
                 lo[k] = load_values<T, V>(a.x, from);
                 if constexpr (kTwo)
@@ -94,18 +116,33 @@ __global__ __launch_bounds__(kRopeBlock) void ua2a_rope_kernel(RopeArgs a)
         };
         load(h0);                                                // on their way while the angles are worked out
         float c[NP], s[NP];
+        if constexpr (TABLE) {
+            for (uint32_t e = threadIdx.x; e < g.per_group * g.pairs; e += blockDim.x) {
+                const uint32_t t = fdiv(e, g.d_pairs), pair = e - t * g.pairs;
+                if (first + t >= static_cast<int64_t>(g.tokens)) break;
+                const TokenPlace place = token_place(g.sh, static_cast<uint32_t>(first + t));
+                f32x2v cs;
+                float x, y;
+                angle_of(a, pair, position_of(g, place), &x, &y);
+                cs[0] = x;
+                cs[1] = y;
+                table[e] = cs;
+            }
+            __syncthreads();
+            if (!in) return;
+        }
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const uint32_t pair = kTwo ? (HALVES ? d : slot) + i : d / 2 + i;
             c[i] = 1.f;
             s[i] = 0.f;
-            if (pairs_here && pair < g.pairs) {
-                int32_t axis = a.axes[pair];
-                axis = axis < 0 ? 0 : axis;
-                axis = axis < static_cast<int32_t>(g.naxes) ? axis : static_cast<int32_t>(g.naxes) - 1;
-                const int32_t pos = a.positions[static_cast<int64_t>(axis) * g.axis_stride + where];
-                cos_sin(turn_of(pos, a.turns[pair]), &c[i], &s[i]);
-                if (g.inverse) s[i] = -s[i];
+            if (!pairs_here || pair >= g.pairs) continue;
+            if constexpr (TABLE) {
+                const f32x2v cs = table[within * g.pairs + pair];
+                c[i] = cs[0];
+                s[i] = cs[1];
+            } else {
+                angle_of(a, pair, where, &c[i], &s[i]);
             }
         }
         const auto turn = [&](uint32_t h) {
@@ -148,14 +185,22 @@ __global__ __launch_bounds__(kRopeBlock) void ua2a_rope_kernel(RopeArgs a)
             turn(h);
             load(h + batch);
         }
+        if constexpr (TABLE) return;                             // one slot a lane
     }
 }
 
 template <class T, int V>
 const void* typed_fn(const AttnLaunch& L)
 {
-    if (V > 1 && L.rope.g.halves) return reinterpret_cast<const void*>(&ua2a_rope_kernel<T, V, (V > 1)>);
-    return reinterpret_cast<const void*>(&ua2a_rope_kernel<T, V, false>);
+    if constexpr (V == 1) {
+        return reinterpret_cast<const void*>(&ua2a_rope_kernel<T, 1, false, false>);
+    } else {
+        if (L.rope.g.slots > kRopeBlock)
+            return L.rope.g.halves ? reinterpret_cast<const void*>(&ua2a_rope_kernel<T, V, true, false>)
+                                   : reinterpret_cast<const void*>(&ua2a_rope_kernel<T, V, false, false>);
+        return L.rope.g.halves ? reinterpret_cast<const void*>(&ua2a_rope_kernel<T, V, true, true>)
+                               : reinterpret_cast<const void*>(&ua2a_rope_kernel<T, V, false, true>);
+    }
 }
 
 }  // namespace
