@@ -16,6 +16,7 @@ namespace ua2a {
 namespace {
 
 constexpr uint32_t kTileKeys = 32;
+constexpr int kNonTemporal = 2;              // a buffer load's cache policy: nt
 
 __device__ __forceinline__ int32_t least_of(int32_t a, uint32_t b)
 {
@@ -74,8 +75,9 @@ struct WaveCodes {
             const uint32_t d = piece(c) * 16;
             const bool ok = d < g.D;
             const uint32_t at = ok ? row(c) * step + d : kNowhere, sat = ok ? row(c) * sstep + d / kBlockValues : kNowhere;
-            k[c] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(kd, at, 0, 0));
-            v[c] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(vd, at, 0, 0));
+            // not kept in the caches, for nobody reads them again (62 us against 56)
+            k[c] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(kd, at, 0, kNonTemporal));
+            v[c] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(vd, at, 0, kNonTemporal));
             ks[c] = __builtin_amdgcn_raw_buffer_load_b8(ksd, sat, 0, 0);
             vs[c] = __builtin_amdgcn_raw_buffer_load_b8(vsd, sat, 0, 0);
         }
@@ -104,6 +106,13 @@ __device__ __forceinline__ void wave_order()
 {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+}
+
+// The largest of a value and the neighbouring quarter's (lane 16 places on or back).
+__device__ __forceinline__ float max_quarters(float x)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 // A's operand with a row of the tile per lane, rows row0 .. + 15, depth step ks.
@@ -221,8 +230,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
             float high = -__builtin_inff();
 #pragma unroll
             for (int x = 0; x < 8; ++x) high = fmaxf(high, s[x / 4][x % 4]);
-            high = fmaxf(high, __shfl_xor(high, 16));
-            high = fmaxf(high, __shfl_xor(high, 32)) * a.scale2;
+            high = max_halves(max_quarters(high)) * a.scale2;
             // the maximum may lag by 2^8, which costs no precision
             const bool grow = high > m + 8.f || (m == -__builtin_inff() && high > m);
             if (__builtin_amdgcn_ballot_w64(grow) != 0) {
@@ -277,8 +285,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
             wave_order();
         }
     }
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
+    l = add_halves(l + __shfl_xor(l, 16));
     if (quarter == 0) {
         stat[(wave * kDecodeRows + col) * 2] = m;
         stat[(wave * kDecodeRows + col) * 2 + 1] = l;
