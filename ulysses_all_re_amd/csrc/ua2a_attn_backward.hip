@@ -373,6 +373,7 @@ __global__ __launch_bounds__(kAttnBlock) void ua2a_attention_keys_join_kernel(At
     if (parts <= 1) return;
     const uint32_t seq = fdiv(unit, g.d_kvl), kvh = unit - seq * g.kvl;
     f32x4v x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (uint32_t s = 0; s < parts; ++s)
         x += *reinterpret_cast<const f32x4v*>(a.partial + part_line(g, a.keys, unit, s, j) * 2 * g.D + c);
     const bool is_v = c >= g.D;

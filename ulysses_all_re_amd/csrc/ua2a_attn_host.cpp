@@ -184,9 +184,11 @@ int64_t most_seers(const AttnGeom& g)
 // How the keys' gradients go to workgroups.  Sinks are seen by all rows, other
 // keys by a window of them, so a tile of sinks would be walked long after the
 // rest: tiles are walked in parts of about a window, and of less where the call
-// is small: as much as leaves a part for each workgroup that the device holds
+// is small: as much as leaves two parts for each workgroup that the device holds
 // at once (512), but 512 rows at least, for a part's sums go through the
-// workspace (no more than 64 parts of a tile, and 256 MiB).
+// workspace (no more than 64 parts of a tile, and 256 MiB).  Eight units
+// of 6,124 keys, rows of 4 heads of 64: 171 us, join included; with one part
+// for each workgroup 179, in two parts of everything (sinks' tiles last) 431.
 void backward_shape(AttnGradArgs* a)
 {
     AttnGeom& g = a->g;
@@ -196,7 +198,7 @@ void backward_shape(AttnGradArgs* a)
     const int64_t lead = most < g.rows ? ceil_div(sinks, kAttnGradKeys) : 0;
     const int64_t span = lead * kAttnGradKeys < g.keys ? lead * kAttnGradKeys : g.keys;
     const int64_t all = g.units * (lead * g.rows + (tiles - lead) * most);
-    int64_t part = all / 512 < most ? all / 512 : most;
+    int64_t part = all / 1024 < most ? all / 1024 : most;
     if (part < 512) part = 512;
     int64_t first, rest;
     for (;; part *= 2) {
