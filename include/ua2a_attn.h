@@ -42,8 +42,8 @@ extern "C" {
  * out may be x itself where `from` and `to` are equal; no other overlap of
  * out with an input.
  * Errors: INVALID_ARG (NULL, a type that is not the plan's, bad side or flag),
- * SHAPE (pairs < 1 or 2 * pairs > D, naxes < 1, 2^31 positions or tokens'
- * pieces of 16 bytes), ALIGN (x, out by their type, positions and axes by 4,
+ * SHAPE (pairs < 1 or 2 * pairs > D, naxes < 1, 2^31 tokens, or positions on
+ * all axes), ALIGN (x, out by their type, positions and axes by 4,
  * turns by 8), ALIAS, DEVICE (no state change); HIP (the plan becomes
  * disabled); DISABLED.
  */
@@ -80,7 +80,7 @@ typedef struct ua2a_window_s {
 
 /*
  * ua2a_attention: softmax(scale * q k^T) v of gathered heads (A layout),
- * every sequence (w * B of them) by itself, one launch, or two where a part
+ * every sequence (w * B of them) by itself; one launch, or two where parts
  * of the keys goes to workgroups of its own.
  *   q, out     [w][B][S_local*w][H/w][D]
  *   k, v       [w][B][S_local*w][kv_heads/w][D]; query head h of a rank takes
@@ -98,11 +98,12 @@ typedef struct ua2a_window_s {
  * exp(s - m) are rounded to the type for the product with v, their sum is
  * not; out is rounded once.  What a row does not see plays no part in it,
  * infinities and NaN included; a row whose weights are all zero is zeros.
- * D must be a multiple of 8 up to 128; all tensors 16-byte aligned; scale > 0.
+ * D must be a multiple of 8 up to 128; all tensors 16-byte aligned; scale > 0
+ * and finite, in powers of two too (scale * log2 e).
  * No output may overlap an input, another output or the workspace.
  * Errors: INVALID_ARG (NULL, type, scale, chunk < 1, a bound < -1), SHAPE (D,
- * kv_heads not a multiple of w or no divisor of H, kv_heads/w * D over 2^22,
- * 2^31 rows or more), ALIGN, ALIAS, CAPACITY (workspace), DEVICE, HIP, DISABLED.
+ * kv_heads not a multiple of w or no divisor of H, H/w * D over 2^22, 2^31
+ * tokens times heads of a rank or more, 2^38 values of a tensor), ALIGN, ALIAS, CAPACITY (workspace), DEVICE, HIP, DISABLED.
  */
 typedef struct ua2a_attention_s {
     const void* q;
@@ -134,8 +135,11 @@ int ua2a_attention_workspace(ua2a_plan_t plan, const ua2a_attention_t* args, int
  * With P = exp(scale * s - lse), delta = sum(dout * out) of a row:
  *   dv = P^T dout,  dS = P * (dout v^T - delta),  dq = scale dS k,  dk = scale dS^T q.
  * Sums are in 32 bits, in a fixed order; P and dS are rounded to the type for
- * the products, the gradients once.  Padding may hold anything; infinities and
- * NaN elsewhere reach the gradients of rows and keys near them too.
+ * the products with dout and q, dS to two values of it (their sum has twice the
+ * digits) for the product with k, the gradients once.  So with fp16 a dS past
+ * 65504 is infinite and one below 2^-25 is nothing, as in any product of that
+ * type: scale the loss.  Padding may hold anything; infinities and NaN elsewhere
+ * reach the gradients of rows and keys near them too.
  */
 typedef struct ua2a_attention_grad_s {
     const void* dout;

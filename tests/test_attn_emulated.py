@@ -317,3 +317,11 @@ def test_parts_fit_their_workspace(dry):
         assert dry.ua2a_attention_backward(plan, ctypes.byref(args), None) == 0
         assert dry.ua2a_attn_emu_errors() == 0
         dry.ua2a_destroy(plan)
+
+
+def test_a_scale_past_the_range_in_powers_of_two(dry):
+    plan = make_plan(dry, 2, 1, 8, 8, 16)
+    assert dry.ua2a_attention(plan, ctypes.byref(attention_args(scale=3e38)), None) == INVALID
+    assert dry.ua2a_attention(plan, ctypes.byref(attention_args(scale=2e38)), None) == 0
+    assert dry.ua2a_attention_backward(plan, ctypes.byref(grad_args(scale=3e38)), None) == INVALID
+    dry.ua2a_destroy(plan)

@@ -177,3 +177,39 @@ def test_fake_shapes_and_gradients():
         ops.rope_all_to_all_4D(torch.zeros(w, B, S, H, D), r, torch.zeros(2, S * w, dtype=torch.int32), 2, 1, w)
     with pytest.raises(RuntimeError, match="GPU only"):
         ops.window_attention(*[torch.zeros(w, B, S * w, 2, D)] * 3, w)
+
+
+def test_rotary_tables_are_checked():
+    """A rotary's tensors that were replaced, or an operator's of other sizes, never reach the library."""
+    plan = _host_plan(w=2, B=3, S=4, H=4, D=16)
+    calls = Calls(plan)
+    x, flat = torch.zeros(plan.in_shape(0), dtype=torch.bfloat16), torch.zeros(2, 8, dtype=torch.int32)
+    for change, error in ((dict(turns=torch.zeros(5, dtype=torch.int64)), ValueError), (dict(turns=torch.zeros(6, dtype=torch.int32)), TypeError),
+                          (dict(turns=torch.zeros(12, dtype=torch.int64)[::2]), ValueError), (dict(axes=torch.zeros(5, dtype=torch.int32)), ValueError),
+                          (dict(axes=torch.zeros(6, dtype=torch.int64)), TypeError), (dict(axes=torch.zeros(6, device="meta", dtype=torch.int32)), ValueError)):
+        r = ua.Rotary(16, (6, 6), device="cpu")
+        r.__dict__.update(change)
+        with pytest.raises(error, match="rotary"):
+            plan.rope_exchange(x, r, flat, 0)
+        if "axes" in change:                                   # as the operator makes it from its tensors
+            with pytest.raises(error, match="rotary"):
+                plan.rope_exchange(x, ops._rotary(16, r.turns, r.axes, 2, False), flat, 0)
+    assert not calls.seen
+    with pytest.raises(ValueError, match="heads of 32"):
+        ops.rope_all_to_all_4D(x, ua.Rotary(32, (6, 6), device="cpu"), flat, 2, 1, 2)
+
+
+def test_a_scale_in_a_tensor_is_read_at_each_call():
+    plan = _host_plan(w=2, B=3, S=4, H=8, D=16)
+    calls = Calls(plan)
+    q = torch.zeros(plan.out_shape(0), dtype=torch.bfloat16)
+    scale, left = torch.tensor(0.5), torch.tensor(3)
+    for value in (0.5, 0.25, 2.0):
+        scale.fill_(value)
+        left.fill_(int(value * 4))
+        plan.window_attention(q, q, q, scale=scale, left=left)
+        args = calls.seen[-1][1][0]._obj
+        assert (args.scale, args.window.left) == (value, int(value * 4))
+    for scale in (1e-40, 3e38, float("inf")):
+        with pytest.raises(ValueError, match="scale"):
+            plan.window_attention(q, q, q, scale=scale)

@@ -257,3 +257,40 @@ def test_scales_past_the_type():
         got = plan.cache_attention(cache, q, starts)
         nan = torch.isnan(got)
         assert bool(nan[0, 1, :, 0].all()) and int(nan.sum()) == q.shape[2] * 64          # a head, and no other
+
+
+def test_forward_and_backward_captured_together():
+    """A block's forward and backward pass in one graph, replayed on new inputs and counts
+    with eager work of the same leaves in between: the eager bits every time."""
+    w, B, S, H, D = 2, 2, 96, 8, 64
+    note("block captured")
+    x = values((w, B, S, H, D), torch.bfloat16, 1).requires_grad_(True)
+    wts = [values((H, D), torch.bfloat16, i, 0.5) for i in (2, 3, 4)]
+    dy, counts = values((w, B, S, H, D), torch.bfloat16, 5), ints([S * w, 100])
+    rotary, pos = ua.Rotary(D, (24, 20, 20), device=DEV), grid(S * w)
+
+    def step():
+        y = block(x, wts, rotary, pos, w, counts)
+        return (y,) + torch.autograd.grad(y, x, dy)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [t.detach() for t in step()]
+    for seed, short in ((10, 0), (20, 1), (30, 150)):
+        with torch.no_grad():
+            for i, t in enumerate([x, dy] + wts):
+                t.copy_(values(tuple(t.shape), t.dtype, seed + i))
+            counts.copy_(ints([short, S * w]))
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in got]
+        want = [t.detach() for t in step()]
+        torch.cuda.synchronize()
+        for k, e in zip(kept, want):
+            assert torch.equal(k, e), seed

@@ -148,7 +148,6 @@ class Rotary:
 def _bound(x, what: str) -> int:
     if x is None:
         return -1
-    x = int(x)
     if x < 0:
         raise ValueError(f"{what} must be at least 0, or None for no bound, not {x}")
     return x
@@ -165,15 +164,17 @@ class AttentionCalls:
         if spec is None:
             import torch
             SG, a = self.S_local * self.w, rotary.naxes
-            spec = specs[a] = (self._type(), (self.in_shape(0), self.out_shape(0)), (a, SG), (a, self.B, SG), torch.int32)
-        code, shapes, one, each, int32 = spec
+            spec = specs[a] = (self._type(), (self.in_shape(0), self.out_shape(0)), (a, SG), (a, self.B, SG), torch.int32,
+                               torch.int64)
+        code, shapes, one, each, int32, int64 = spec
         if not self._fits(x, self.dtype, shapes[from_a]):
             self._check(x, shapes[from_a], "input")
         if rotary.D != self.D:
             raise ValueError(f"rotary is for heads of {rotary.D}, the plan has {self.D}")
-        turns, axes = rotary.turns, rotary.axes
-        if turns.device != self.device or axes.device != self.device:
-            raise ValueError(f"rotary is on {turns.device}, plan is on {self.device}")
+        turns, axes, pairs = rotary.turns, rotary.axes, (rotary.pairs,)
+        if not (self._fits(turns, int64, pairs) and self._fits(axes, int32, pairs)):
+            self._expect(turns, int64, pairs, "rotary.turns")
+            self._expect(axes, int32, pairs, "rotary.axes")
         planes = positions.dim() == 3
         if planes and positions.shape[1] == 1:
             positions, planes = positions[:, 0], False            # one plane for all
@@ -216,6 +217,10 @@ class AttentionCalls:
         heads on all ranks, bytes of scratch).  heads: key heads of a rank; sizes:
         (sequences, capacity, n) of a cache's call, else None."""
         specs = self.__dict__.setdefault("_attention_specs", {})
+        if scale is not None:
+            scale = float(scale)                               # a tensor's value may change from call to call
+        left, right = (x if x is None else int(x) for x in (left, right))
+        sinks, chunk = int(sinks), int(chunk)
         key = (kind, heads, sizes, left, right, sinks, chunk, scale)
         spec = specs.get(key)
         if spec is not None:
@@ -225,15 +230,14 @@ class AttentionCalls:
             raise TypeError("attention takes bfloat16 and float16 plans, not float32")
         if self.D % 8 or self.D > 128:
             raise ValueError(f"attention takes heads of a multiple of 8 values up to 128, not {self.D}")
-        sinks, chunk = int(sinks), int(chunk)
         if sinks < 0 or chunk < 1:
             raise ValueError(f"sinks must be at least 0 and chunk at least 1, not {sinks} and {chunk}")
         bounds = (_bound(left, "left"), _bound(right, "right"), sinks, chunk)
         if max(bounds) >= 1 << 31:
             raise ValueError(f"a window's sizes must be below 2^31, got {bounds}")
-        scale = self.D ** -0.5 if scale is None else float(scale)
-        if not 0.0 < scale < 3.4e38:
-            raise ValueError(f"scale must be positive and finite, not {scale}")
+        scale = self.D ** -0.5 if scale is None else scale
+        if not 1e-37 < scale < 1e38:
+            raise ValueError(f"scale must be positive and finite (within 1e-37 and 1e38), not {scale}")
         if heads < 1 or (self.H // self.w) % heads:
             raise ValueError(f"{heads} key heads per rank do not divide the plan's {self.H // self.w}")
         window, kv, need = ua2a_window_t(*bounds), heads * self.w, ctypes.c_int64()
@@ -359,7 +363,7 @@ class AttentionCalls:
         sequence i has position ``starts[i] + t``, where that lies in the
         cache, and the positions up to the last of them hold keys.  Rows
         without a position are left as they were; without ``out`` they are
-        zeros (where there can be any, that fills the result first).
+        zeros (the result is filled first).
         """
         self._check_cache_of(cache, None, starts, counts)
         if starts is None:

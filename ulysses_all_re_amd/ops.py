@@ -415,6 +415,8 @@ def rope_all_to_all_4D(x: torch.Tensor, rotary: Rotary, positions: torch.Tensor,
     else:
         raise ValueError(f"unsupported (scatter_dim, gather_dim) = ({scatter_dim}, {gather_dim}); "
                          "use (2, 1) for heads -> sequence or (1, 2) for the inverse")
+    if rotary.D != x.shape[-1]:
+        raise ValueError(f"rotary is for heads of {rotary.D}, x has {x.shape[-1]}")
     return rope_exchange(x, positions, rotary.turns, rotary.axes, w, mode, rotary.naxes, rotary.halves, inverse)
 
 
