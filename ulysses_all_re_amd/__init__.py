@@ -22,8 +22,9 @@ exchange one batch plane at a time through a window sized for one plane.)
 ``Plan.exchange_ranks`` runs it between per-rank tensors (one allocation
 each, the ranks' shapes without the leading w), optionally only for the runs
 a range of ranks sends.  The operators of include/ua2a_act.h (RMS norms joined
-with the exchange, 8-bit checkpoints, the 8-bit key/value cache) are methods
-of ``Plan`` too; see ``activations.py``.
+with the exchange, 8-bit checkpoints, the 8-bit key/value cache) and of
+include/ua2a_attn.h (rotary positions, windowed attention) are methods of
+``Plan`` too; see ``activations.py`` and ``attention.py``.
 """
 from __future__ import annotations
 

@@ -3,7 +3,7 @@
     python -m ulysses_all_re_amd.build
 
 The library is compiled with hipcc for MI355X (gfx950) only, from the
-sources under csrc/ and the public header include/ua2a.h.
+sources under csrc/ and the public headers under include/.
 """
 from __future__ import annotations
 

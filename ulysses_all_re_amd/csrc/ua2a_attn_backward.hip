@@ -5,7 +5,13 @@
 //   dq = scale dS k,  dk = scale dS^T q,  dv = P^T dout.
 // The first two products (s and dout v^T) are made twice, once where rows keep
 // their sums (dq) and once where keys keep theirs (dk, dv): seven products
-// instead of five, and in return no atomics, so equal inputs give equal bits.
+// instead of five (and an eighth, for dS's second part), and in return no atomics,
+// so equal inputs give equal bits.
+//
+// The matrix products and what stands between them bound the first kernel, waiting
+// for operands in LDS the second: 12 heads of 128 over 32,760 tokens, a window of three
+// frames of 1560 and the first, take 2.1 ms and 3.1 (matrix units busy 60 % and 39 % of
+// the time); the eight products alone would be 4.0 ms at a large matrix product's rate.
 #include "ua2a_attn_device.h"
 
 namespace ua2a {
@@ -64,7 +70,7 @@ __device__ __forceinline__ void store_row(void* out, int64_t at, uint32_t D, con
 // keys x rows, dS goes on to its product with k from the registers it is in.  A
 // row's dS add up to zero, so what rounding leaves of them weighs more than in the
 // other sums; dS goes in as two values of the type (an error of dq of 1.45 times
-// its own rounding's falls to 1.0 times; three products become four).
+// its own rounding's falls to 1.0 times; three products become four, 1.69 ms 2.13).
 template <class T, int DP>
 __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(AttnGradArgs a)
 {

@@ -187,9 +187,9 @@ int64_t most_seers(const AttnGeom& g)
 // rest: tiles are walked in parts of about a window, and of less where the call
 // is small: as much as leaves two parts for each workgroup that the device holds
 // at once (512), but 512 rows at least, for a part's sums go through the
-// workspace (no more than 64 parts of a tile, and 256 MiB).  Eight
-// units of 6,124 keys, rows of 4 heads of 64: the whole call takes 237 us, with
-// one part for each workgroup 263.
+// workspace (no more than 64 parts of a tile, and 256 MiB).  A
+// call of eight units of 6,124 keys at most, four rows a key, heads of 64, takes
+// 231-258 us, with one part for each workgroup 245-266.
 void backward_shape(AttnGradArgs* a)
 {
     AttnGeom& g = a->g;
