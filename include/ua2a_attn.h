@@ -166,7 +166,8 @@ int ua2a_attention_backward_workspace(ua2a_plan_t plan, const ua2a_attention_gra
 /*
  * ua2a_cache_attention: the same attention of n new tokens of every sequence
  * of a cache, over what the cache holds (code * scale, rounded to the type, as
- * ua2a_cache_read gives it).
+ * ua2a_cache_read gives it).  Up to 16 queries of a key head take their weights
+ * as two values of the type into the product with v.
  *   q, out     [w][sequences][n][H/w][D] (the mode-0 exchange of the tokens
  *              that ua2a_cache_write takes has them in this order)
  *   kv_heads   the cache's heads on all ranks (its H in place of the plan's)

@@ -52,16 +52,21 @@ __device__ __forceinline__ u32x4v operand_of(const f32x16v& c, int s)
     return r;
 }
 
-// What that rounding left of them, rounded itself.
+// What rounding to a pair of the type left of two values, rounded itself.
+template <class T>
+__device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t rounded)
+{
+    const auto x = pair_of<T>(rounded);
+    return pack2<T>(a - static_cast<float>(x[0]), b - static_cast<float>(x[1]));
+}
+
+// What operand_of's rounding left.
 template <class T>
 __device__ __forceinline__ u32x4v rest_of(const f32x16v& c, u32x4v rounded, int s)
 {
     u32x4v r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const auto x = pair_of<T>(rounded[i]);
-        r[i] = pack2<T>(c[8 * s + 2 * i] - static_cast<float>(x[0]), c[8 * s + 2 * i + 1] - static_cast<float>(x[1]));
-    }
+    for (int i = 0; i < 4; ++i) r[i] = rest2<T>(c[8 * s + 2 * i], c[8 * s + 2 * i + 1], rounded[i]);
     return r;
 }
 
