@@ -86,6 +86,7 @@ struct AttnGeom {
     uint32_t keys;               // positions of a sequence
     uint32_t splits;             // parts of a walk
     uint32_t items;              // units * tiles * splits
+    uint32_t order;              // 1: a unit's tiles from the last to the first
     Div32 d_splits, d_tiles, d_kvl, d_seqs, d_group, d_rows;
 };
 
@@ -100,6 +101,10 @@ UA2A_HD uint32_t attn_item(const AttnGeom& g, uint32_t id)
     return i < per && item < g.items ? item : g.items;
 }
 
+// Which of `tiles` comes i-th: where walks grow from tile to tile, the last first, so
+// that what ends last is short.
+UA2A_HD uint32_t tile_in_order(uint32_t order, uint32_t tiles, uint32_t i) { return order != 0 ? tiles - 1 - i : i; }
+
 struct AttnPlace {
     uint32_t unit, tile, split;
     uint32_t seq;                // of all ranks: rank * seqs + sequence
@@ -113,7 +118,7 @@ UA2A_HD AttnPlace attn_place(const AttnGeom& g, uint32_t item)
     const uint32_t ut = fdiv(item, g.d_splits);
     p.split = item - ut * g.splits;
     p.unit = fdiv(ut, g.d_tiles);
-    p.tile = ut - p.unit * g.tiles;
+    p.tile = tile_in_order(g.order, g.tiles, ut - p.unit * g.tiles);
     p.seq = fdiv(p.unit, g.d_kvl);
     p.kvh = p.unit - p.seq * g.kvl;
     p.i = p.seq - fdiv(p.seq, g.d_seqs) * g.seqs;
@@ -245,7 +250,7 @@ UA2A_HD KeyPlace key_place(const AttnGeom& g, const KeyTiles& t, uint32_t item)
         i -= leading;
         const uint32_t tile = fdiv(i, t.d_rest_parts);
         p.at.split = i - tile * t.rest_parts;
-        p.at.tile = t.lead + tile;
+        p.at.tile = t.lead + tile_in_order(g.order, g.tiles - t.lead, tile);
         p.parts = t.rest_parts;
     }
     p.at.seq = fdiv(p.at.unit, g.d_kvl);

@@ -86,6 +86,17 @@ int64_t most_seen(const AttnGeom& g, int64_t rows)
     return seen < g.keys ? seen : g.keys;
 }
 
+// Whether walks grow from tile to tile: of rows where only the left has no bound, of
+// keys where only the right has none.  They then run from the last tile to the first:
+// 8 heads of 128 over 32,768 tokens, causal, forward 2150 us, 2550 from the first (32
+// heads over 8192 740, 780; as many units of rows in pairs of a long and a short walk
+// 840), backward 8110, 8800.
+uint32_t order_of(const AttnGeom& g, bool keys)
+{
+    if ((g.win.left < 0) == (g.win.right < 0)) return 0;
+    return (g.win.left < 0) == keys ? 0 : 1;
+}
+
 void set_items(AttnGeom* g, int64_t tiles, int64_t splits)
 {
     g->tiles = static_cast<uint32_t>(tiles);
@@ -116,6 +127,7 @@ void forward_shape(AttnGeom* g, AttnLaunch* L)
         if (splits < 1) splits = 1;
     }
     set_items(g, tiles, splits);
+    g->order = order_of(*g, false);
     L->DP = padded_head(g->D);
     L->block = kAttnBlock;
 }
@@ -211,6 +223,7 @@ void backward_shape(AttnGradArgs* a)
         if (lines * g.units * g.D * 8 <= (int64_t(256) << 20)) break;
     }
     set_items(&g, tiles, 1);
+    g.order = order_of(g, true);
     t.lead = static_cast<uint32_t>(lead);
     t.span = static_cast<uint32_t>(span);
     t.lead_parts = static_cast<uint32_t>(first);
@@ -473,6 +486,7 @@ int ua2a_attention_backward(ua2a_plan_t plan, const ua2a_attention_grad_t* n, vo
     const AttnGeom by_keys = g;
     L.kernel = AttnKernel::GradRows;
     set_items(&g, ceil_div(g.rows, kAttnRows), 1);
+    g.order = order_of(g, false);
     attn_grid(workgroups(g), &L);
     int err = attn_launch(L, stream);
     if (err != 0) return fail(plan, "launching attention's backward kernel of rows", err);
