@@ -13,10 +13,10 @@
 // heads of 128: 40 heads over 75,600 tokens, a window of three frames of 3600 and
 // the first, take 21.3 ms, 970 TFLOP/s, where a large matrix product of the library
 // reaches 1162 on this card (matrix units busy 44 % of the time, the others 42).
-// With heads of 64 a product costs half as much and an exponential the same: 32
-// heads over 6124 tokens in fp16, a window of 1024, 564 TFLOP/s.  A cache's keys are
-// decoded on their way (1560 tokens of 12 heads over 6,240 to 7,800 positions: 600
-// TFLOP/s).  Tiles go straight from memory to LDS, in two buffers with a barrier a tile
+// Everything visible, 32 heads of 128 over 8192 tokens: 938 TFLOP/s; heads of 64, with
+// as many exponentials for half the products, 886; a window of 1024 of such, whose walks
+// are 18 tiles with a quarter of them masked, 564 to 670.  A cache's keys are decoded on
+// their way (1560 tokens of 12 heads over 7,800 positions: 600 TFLOP/s).  Tiles go straight from memory to LDS, in two buffers with a barrier a tile
 // (24.6 ms through registers, 22.5 so); a row's halves are joined in registers and
 // the wave at its products has priority (21.5).  Blocks of 32 keys worked on in turn,
 // one's products beside the other's exponentials, spill (43 ms; heads of 64 207 us
