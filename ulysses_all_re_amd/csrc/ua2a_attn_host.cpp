@@ -86,15 +86,16 @@ int64_t most_seen(const AttnGeom& g, int64_t rows)
     return seen < g.keys ? seen : g.keys;
 }
 
-// Whether walks grow from tile to tile: of rows where only the left has no bound, of
-// keys where only the right has none.  They then run from the last tile to the first:
-// 8 heads of 128 over 32,768 tokens, causal, forward 2150 us, 2550 from the first (32
-// heads over 8192 740, 780; as many units of rows in pairs of a long and a short walk
-// 840), backward 8110, 8800.
+// Whether walks grow from tile to tile: of rows where the left reaches further than
+// the right, of keys the other way round.  They then run from the last tile to the
+// first, so that what ends last is short: 32 heads of 128 over 8192 tokens, causal,
+// 612 us, 684 from the first (heads of 64 369, 420), 8 over 32,768 2150, 2550, backward
+// 8110, 8800; a window of 1024 of 6124 tokens 148, 154; long and short walks in turn 8 %
+// slower than from the first.
 uint32_t order_of(const AttnGeom& g, bool keys)
 {
-    if ((g.win.left < 0) == (g.win.right < 0)) return 0;
-    return (g.win.left < 0) == keys ? 0 : 1;
+    const int64_t left = g.win.left < 0 ? kMost32 + 1 : g.win.left, right = g.win.right < 0 ? kMost32 + 1 : g.win.right;
+    return keys ? right > left : right < left;
 }
 
 void set_items(AttnGeom* g, int64_t tiles, int64_t splits)
