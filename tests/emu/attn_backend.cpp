@@ -445,4 +445,21 @@ extern "C" {
 int64_t ua2a_attn_emu_errors(void) { return g_errors; }
 int64_t ua2a_attn_emu_last(int32_t k) { return g_last[k]; }
 void ua2a_attn_emu_dry(int32_t on) { g_dry = on; }
+
+// What the kernels take of a tile of `size` keys from k0 on, for rows at positions p0 .. p1 of a
+// sequence of `end` keys: 1 all seen, 2 none seen; and in sees[] what the row at p0 sees of each.
+int32_t ua2a_attn_emu_tile(const ua2a_window_t* w, int32_t p0, int32_t p1, int32_t end, uint32_t k0, uint32_t size,
+                           uint8_t* seen)
+{
+    using namespace ua2a;
+    WindowGeom g;
+    g.left = static_cast<int32_t>(w->left);
+    g.right = static_cast<int32_t>(w->right);
+    g.sinks = static_cast<int32_t>(w->sinks);
+    g.chunk = static_cast<uint32_t>(w->chunk);
+    g.d_chunk = make_div32(g.chunk);
+    const Seen a = seen_by(g, p0, end), b = seen_by(g, p1, end);
+    for (uint32_t i = 0; i < size; ++i) seen[i] = sees(a, k0 + i);
+    return (all_seen(a, b, k0, k0 + size) ? 1 : 0) | (none_seen(a, b, k0, k0 + size) ? 2 : 0);
+}
 }

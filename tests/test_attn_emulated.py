@@ -325,3 +325,35 @@ def test_a_scale_past_the_range_in_powers_of_two(dry):
     assert dry.ua2a_attention(plan, ctypes.byref(attention_args(scale=2e38)), None) == 0
     assert dry.ua2a_attention_backward(plan, ctypes.byref(grad_args(scale=3e38)), None) == INVALID
     dry.ua2a_destroy(plan)
+
+
+@pytest.mark.parametrize("end", [(1 << 31) - 1, (1 << 31) - 2, (1 << 31) - 64, (1 << 31) - 128, 1000])
+def test_tiles_at_the_end_of_the_largest_cache(lib, end):
+    """A tile that reaches 2^31: what the kernels take as seen by all rows, by none, and by a
+    row, against the definition in Python's integers."""
+    flags = (ctypes.c_uint8 * 128)()
+    for left, right, sinks, chunk in [(0, 0, 0, 1), (None, 0, 0, 1), (40, 0, 5, 1), (None, None, 0, 1), (0, 0, (1 << 31) - 1, 1),
+                                      (1, 0, 4, 50), (3, 7, 0, 1), (0, None, 9, 16), (200, 0, 0, 1)]:
+        window = window_of((left, right, sinks, chunk))
+
+        def sees(p, j):
+            c = j // chunk - p // chunk
+            near = (left is None or c >= -left) and (right is None or c <= right)
+            return j < end and (near or (j < sinks and (right != 0 or c <= 0)))
+
+        for size in (32, 64, 128):
+            last = (end - 1) // size * size
+            for k0 in (0, last - size, last):
+                for p0, p1 in ((end - 1, end - 1), (end - 31, end - 1), (end - 128, end - 60)):
+                    got = lib.ua2a_attn_emu_tile(ctypes.byref(window), p0, p1, end, k0, size, flags)
+                    at = (end, left, right, sinks, chunk, size, k0, p0, p1)
+                    rows = [[sees(p, j) for j in range(k0, k0 + size)] for p in range(p0, p1 + 1)]
+                    assert list(map(bool, flags[:size])) == rows[0], at
+                    if got & 1:
+                        assert all(map(all, rows)), at
+                    if got & 2:
+                        assert not any(map(any, rows)), at
+                    # a tile that one row sees whole, or not at all, is known as such
+                    if p0 == p1:
+                        assert bool(got & 1) == all(rows[0]) or sinks, at
+                        assert bool(got & 2) == (not any(rows[0])), at

@@ -119,11 +119,12 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
             const uint32_t bytes = Loads::bytes(n, wave, g.D);
             offset[n] = bytes == kNowhere ? kNowhere : Loads::row(n, wave) * row_bytes + bytes;
         }
-        const auto position = [&](uint32_t i) { return static_cast<int32_t>(walk_tile(walk, i) * KEYS); };
+        const auto position = [&](uint32_t i) { return walk_tile(walk, i) * KEYS; };
         const auto load = [&](uint32_t i, char* tile) {
-            const int32_t k0 = position(i);
+            const uint32_t k0 = position(i);
             const int64_t start = (base + static_cast<int64_t>(k0) * g.kvl) * g.D * 2;
-            const uint32_t bytes = static_cast<uint32_t>(seq.end - k0 < KEYS ? seq.end - k0 : KEYS) * row_bytes;
+            const int32_t left = seq.end - static_cast<int32_t>(k0);
+            const uint32_t bytes = static_cast<uint32_t>(left < KEYS ? left : KEYS) * row_bytes;
             const u32x4v k = descriptor(static_cast<const char*>(a.k) + start, bytes),
                          v = descriptor(static_cast<const char*>(a.v) + start, bytes);
 #pragma unroll
@@ -137,13 +138,13 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
         char *ktile = lds, *other = lds + 2 * kTile;
         load(0, ktile);
         for (uint32_t i = 0; i < walk.total; ++i) {
-            const int32_t k0 = position(i);
+            const uint32_t k0 = position(i);
             char* const vtile = ktile + kTile;
             arrived();
             if (i + 1 < walk.total) load(i + 1, other);
 #pragma unroll
             for (int b = 0; b < NK; ++b) {
-                const int32_t bk0 = k0 + b * 32;
+                const uint32_t bk0 = k0 + b * 32;
                 if (!rows || none_seen(wtop, wbottom, bk0, bk0 + 32)) continue;
                 const bool masked = !all_seen(wtop, wbottom, bk0, bk0 + 32);
                 f32x16v s, dp;
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
                 if (masked) {
 #pragma unroll
                     for (int x = 0; x < 16; ++x)
-                        if (!sees(seen, bk0 + static_cast<int32_t>((x / 4) * 8 + half * 4 + x % 4))) dp[x] = 0.f;
+                        if (!sees(seen, bk0 + ((x / 4) * 8 + half * 4 + x % 4))) dp[x] = 0.f;
                 }
                 const u32x4v ds[2] = {operand_of<T>(dp, 0), operand_of<T>(dp, 1)};
                 const u32x4v rest[2] = {rest_of<T>(dp, ds[0], 0), rest_of<T>(dp, ds[1], 1)};

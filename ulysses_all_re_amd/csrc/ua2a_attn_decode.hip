@@ -192,17 +192,17 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
             if (live && d < g.D) q[ks] = *reinterpret_cast<const u32x4v*>(static_cast<const uint16_t*>(a.q) + place.at + d);
         }
         const int64_t base = static_cast<int64_t>(at.seq) * g.keys * g.kvl + at.kvh;
-        const auto position = [&](uint32_t i) { return static_cast<int32_t>(walk_tile(walk, i) * kTileKeys); };
+        const auto position = [&](uint32_t i) { return walk_tile(walk, i) * kTileKeys; };
         WaveCodes<T, DP> next[2];
         const auto load = [&](uint32_t i, WaveCodes<T, DP>& w) {
-            const int32_t k0 = i < to ? position(i) : 0;
-            w.load(a, base + static_cast<int64_t>(k0) * g.kvl, i < to ? least_of(seq.end - k0, kTileKeys) : 0);
+            const uint32_t k0 = i < to ? position(i) : 0;
+            w.load(a, base + static_cast<int64_t>(k0) * g.kvl, i < to ? least_of(seq.end - static_cast<int32_t>(k0), kTileKeys) : 0);
         };
         const auto step = [&](uint32_t i, WaveCodes<T, DP>& w) {
-            const int32_t k0 = i < to ? position(i) : 0, k1 = k0 + static_cast<int32_t>(kTileKeys);
+            const uint32_t k0 = i < to ? position(i) : 0, k1 = k0 + kTileKeys;
             const bool masked = i >= to || !all_seen(top, bottom, k0, k1);
             const int64_t j0 = base + static_cast<int64_t>(k0) * g.kvl;
-            const int32_t rows = i < to ? least_of(seq.end - k0, kTileKeys) : 0;
+            const int32_t rows = i < to ? least_of(seq.end - static_cast<int32_t>(k0), kTileKeys) : 0;
             constexpr int32_t kFormat = E4M3 ? UA2A_FORMAT_E4M3 : UA2A_FORMAT_E5M2;
             const uint32_t ktop = WaveCodes<T, DP>::template put<E4M3>(w.k, w.ks, tile, g.D);
             if (__builtin_amdgcn_ballot_w64(ktop >= high_scale<T>(kFormat)) != 0)
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
             if (masked) {
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
-                    if (!sees(seen, k0 + static_cast<int32_t>(x / 4 * 16 + quarter * 4 + x % 4))) s[x / 4][x % 4] = -__builtin_inff();
+                    if (!sees(seen, k0 + (x / 4 * 16 + quarter * 4 + x % 4))) s[x / 4][x % 4] = -__builtin_inff();
             }
             float high = -__builtin_inff();
 #pragma unroll
@@ -270,7 +270,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
             for (int w = 0; w < DP / 32; ++w) up[w] = down[w] = 0;
 #pragma unroll 1
             for (uint32_t j = 0; j < kTileKeys; ++j) {
-                const bool see = sees(seen, k0 + static_cast<int32_t>(j));
+                const bool see = sees(seen, k0 + j);
                 const uint32_t* bits = reinterpret_cast<const uint32_t*>(wild + j * (DP / 4));
 #pragma unroll
                 for (int w = 0; w < DP / 32; ++w) {

@@ -112,7 +112,7 @@ struct Rows {
 // operands are), their sum is not.
 template <class T, int DP, int NK>
 __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16], const char* ktile, const char* vtile,
-                                       const uint8_t* wild, uint32_t row0, int32_t k0, const Seen& seen, float scale2,
+                                       const uint8_t* wild, uint32_t row0, uint32_t k0, const Seen& seen, float scale2,
                                        bool masked, bool odd)
 {
     const uint32_t half = (threadIdx.x & 63) >> 5;
@@ -128,7 +128,7 @@ __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16
     }
     __builtin_amdgcn_s_setprio(0);
     const auto key = [&](int b, int i) {
-        return k0 + static_cast<int32_t>(b * 32 + (i / 4) * 8 + half * 4 + i % 4);
+        return k0 + (b * 32 + (i / 4) * 8 + half * 4 + i % 4);
     };
     if (masked) {
 #pragma unroll
@@ -182,7 +182,7 @@ __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16
     for (int db = 0; db < DP / 32; ++db) up[db] = down[db] = 0;
 #pragma unroll 1
     for (uint32_t j = 0; j < 32 * NK; ++j) {
-        const bool see = sees(seen, k0 + static_cast<int32_t>(j));
+        const bool see = sees(seen, k0 + j);
 #pragma unroll
         for (int db = 0; db < DP / 32; ++db) {
             const uint32_t* bits = reinterpret_cast<const uint32_t*>(wild + (row0 + j) * (DP / 4)) + db;
@@ -251,12 +251,17 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
 
         const int64_t base = static_cast<int64_t>(at.seq) * g.keys * g.kvl + at.kvh;
         if (threadIdx.x == 0) odd_tile = high_tile = ~0u;
-        const auto position = [&](uint32_t i) { return static_cast<int32_t>(walk_tile(walk, i) * KEYS); };
+        const auto position = [&](uint32_t i) { return walk_tile(walk, i) * KEYS; };
+        // the keys of the tile from k0 on that exist
+        const auto keys_of = [&](uint32_t k0) {
+            const int32_t n = seq.end - static_cast<int32_t>(k0);
+            return n < KEYS ? n : KEYS;
+        };
         // whether some row of the workgroup does not see some key of tile i
-        const auto part_seen = [&](int32_t k0) { return !all_seen(top, bottom, k0, k0 + KEYS); };
-        const auto work = [&](uint32_t i, int32_t k0, const char* ktile, const char* vtile, bool look) {
+        const auto part_seen = [&](uint32_t k0) { return !all_seen(top, bottom, k0, k0 + KEYS); };
+        const auto work = [&](uint32_t i, uint32_t k0, const char* ktile, const char* vtile, bool look) {
             const uint32_t row0 = SHARED ? wave * 32 : 0;
-            const int32_t wk0 = k0 + static_cast<int32_t>(row0);
+            const uint32_t wk0 = k0 + row0;
             if (!rows || none_seen(wtop, wbottom, wk0, wk0 + 32 * NK)) return;
             attend<T, DP, NK>(r, q, ktile, vtile, wild, row0, wk0, seen, a.scale2,
                               !all_seen(wtop, wbottom, wk0, wk0 + 32 * NK), look && odd_tile == i);
@@ -264,12 +269,12 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
         if constexpr (CODES) {
             CodeLoads<T, DP, KEYS> loads;
             const auto load = [&](uint32_t i) {
-                const int32_t k0 = position(i);
-                loads.load(a, base + static_cast<int64_t>(k0) * g.kvl, seq.end - k0 < KEYS ? seq.end - k0 : KEYS);
+                const uint32_t k0 = position(i);
+                loads.load(a, base + static_cast<int64_t>(k0) * g.kvl, keys_of(k0));
             };
             if (from < to) load(from);
             for (uint32_t i = from; i < to; ++i) {
-                const int32_t k0 = position(i);
+                const uint32_t k0 = position(i);
                 const bool look = part_seen(k0);
                 __syncthreads();                                 // the last tile has been read
                 if (loads.store(lds, lds + kTile, a.format) >= high_scale<T>(a.format)) high_tile = i;
@@ -277,7 +282,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
                 __syncthreads();
                 if (high_tile == i) {
                     const int64_t j0 = base + static_cast<int64_t>(k0) * g.kvl;
-                    const int32_t n = seq.end - k0 < KEYS ? seq.end - k0 : KEYS;
+                    const int32_t n = keys_of(k0);
                     const uint8_t *codes = a.codes + j0 * g.D, *scales = a.scales + j0 * g.nb;
                     decode_again<T, DP>(lds, g, codes, scales, n, a.format, threadIdx.x, kAttnBlock);
                     decode_again<T, DP>(lds + kTile, g, codes + a.part, scales + a.part_scales, n, a.format, threadIdx.x,
@@ -300,9 +305,9 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
                 offset[n] = bytes == kNowhere ? kNowhere : Loads::row(n, wave) * row_bytes + bytes;
             }
             const auto load = [&](uint32_t i, char* tile) {
-                const int32_t k0 = position(i);
+                const uint32_t k0 = position(i);
                 const int64_t start = (base + static_cast<int64_t>(k0) * g.kvl) * g.D * 2;
-                const uint32_t bytes = static_cast<uint32_t>(seq.end - k0 < KEYS ? seq.end - k0 : KEYS) * row_bytes;
+                const uint32_t bytes = static_cast<uint32_t>(keys_of(k0)) * row_bytes;
                 const u32x4v k = descriptor(static_cast<const char*>(a.k) + start, bytes),
                              v = descriptor(static_cast<const char*>(a.v) + start, bytes);
 #pragma unroll
@@ -317,7 +322,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
             char* other = lds + (kBuffers - 1) * 2 * kTile;
             if (from < to && kBuffers == 2) load(from, tile);
             for (uint32_t i = from; i < to; ++i) {
-                const int32_t k0 = position(i);
+                const uint32_t k0 = position(i);
                 const bool look = part_seen(k0);
                 if constexpr (kBuffers == 1) {
                     __syncthreads();                             // the last tile has been read

@@ -24,7 +24,11 @@ struct Seen {
     int32_t lo, hi, sk;
 };
 
-UA2A_HD bool sees(const Seen& s, int32_t j) { return (j >= s.lo && j < s.hi) || j < s.sk; }
+// Positions of a tile are unsigned: the last tile of the largest cache reaches 2^31.
+UA2A_HD bool sees(const Seen& s, uint32_t j)
+{
+    return (j >= static_cast<uint32_t>(s.lo) && j < static_cast<uint32_t>(s.hi)) || j < static_cast<uint32_t>(s.sk);
+}
 
 // p in [0, end).  All three grow with p.
 UA2A_HD Seen seen_by(const WindowGeom& g, int32_t p, int32_t end)
@@ -190,13 +194,13 @@ UA2A_HD uint32_t split_at(uint32_t total, uint32_t splits, uint32_t split)
 
 // Whether each (all) or any of the rows between those that see `a` and `b` sees
 // a position of [k0, k1).
-UA2A_HD bool all_seen(const Seen& a, const Seen& b, int32_t k0, int32_t k1)
+UA2A_HD bool all_seen(const Seen& a, const Seen& b, uint32_t k0, uint32_t k1)
 {
-    return (b.lo <= k0 && k1 <= a.hi) || k1 <= a.sk;
+    return (static_cast<uint32_t>(b.lo) <= k0 && k1 <= static_cast<uint32_t>(a.hi)) || k1 <= static_cast<uint32_t>(a.sk);
 }
-UA2A_HD bool none_seen(const Seen& a, const Seen& b, int32_t k0, int32_t k1)
+UA2A_HD bool none_seen(const Seen& a, const Seen& b, uint32_t k0, uint32_t k1)
 {
-    return (k0 >= b.hi || k1 <= a.lo) && k0 >= b.sk;
+    return (k0 >= static_cast<uint32_t>(b.hi) || k1 <= static_cast<uint32_t>(a.lo)) && k0 >= static_cast<uint32_t>(b.sk);
 }
 
 // How a workgroup of 256 lanes joins rows' parts: `wide` lanes (four values each)
