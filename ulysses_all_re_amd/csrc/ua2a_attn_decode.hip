@@ -104,6 +104,18 @@ struct WaveCodes {
         }
         return top;
     }
+
+    // Whether there are infinities or NaN among this lane's codes of e5m2 (what lies
+    // past D may count too).  e4m3 has none but NaN, and scales past the type give none.
+    __device__ __forceinline__ static bool unbounded(const u32x4v (&x)[CH])
+    {
+        uint32_t any = 0;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) any |= (x[c][i] & 0x7c7c7c7cu) + 0x04040404u;
+        return (any & 0x80808080u) != 0;
+    }
 };
 
 // Lanes of a wave read what others of it wrote: a wave's LDS operations run in
@@ -217,13 +229,15 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
             }
             wave_order();
             const uint32_t vtop = WaveCodes<T, DP>::template put<E4M3>(w.v, w.vs, tile, g.D);
+            // zero times an infinity is NaN, and the weights' second parts may be zero or less
+            const bool apart = masked || (!E4M3 && __builtin_amdgcn_ballot_w64(WaveCodes<T, DP>::unbounded(w.v)) != 0);
             load(i + 8, w);
             if (__builtin_amdgcn_ballot_w64(vtop >= high_scale<T>(kFormat)) != 0)
                 decode_again<T, DP>(tile, g, a.codes + a.part + j0 * g.D, a.scales + a.part_scales + j0 * g.nb, rows, kFormat,
                                     lane, 64);
             wave_order();
             bool odd = false;
-            if (masked) {
+            if (apart) {
                 odd = __builtin_amdgcn_ballot_w64(tame_tile<T, DP>(tile, wild, kTileKeys, lane, 64)) != 0;
                 wave_order();
             }
