@@ -47,3 +47,48 @@ def test_visible_infinities_of_a_cache(t, n):
             want[..., d], got[..., d] = 0, 0
         want[..., 127], got[..., 127], want[..., 0], got[..., 0] = 0, 0, 0, 0
         assert torch.equal(got, want), window
+
+
+def small_weights_error(gap):
+    """Of weights `gap` powers of two below the largest, relative: their rounding.  The
+    largest is held at 2^13 at least, fp16 has 11 digits down to 2^-14 and half a step of
+    2^-25 below; then the result's own rounding, and 2^-14 for the sums and exponentials."""
+    return max(2.0 ** -11, 2.0 ** (gap - 13 - 25)) + 2.0 ** -11 + 2.0 ** -14
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("gap", [6.0, 12.0, 17.4, 19.0])
+def test_one_key_takes_most_of_the_weight(gap, t):
+    """A token (a sink) `gap` nats above thousands of others, its value zero and theirs 16:
+    what the others give together is right, by every kernel, wherever the token stands."""
+    dtype = TYPES[t]
+    N, D = 6000, 64
+    x = torch.tensor(gap / 8, dtype=dtype)                        # a score of 8 x and others of 0
+    x = float(x.double())
+    weight = torch.exp(torch.tensor(-8 * x, dtype=torch.float64))
+    error = 2.0 ** -7 if t == "bf16" else small_weights_error(8 * x * 1.4427)
+
+    def check(got, others, what):
+        want = 16 * others * weight / (1 + others * weight)           # no subnormal of the type
+        off = float((got.double().cpu() - want).abs().max() / want)
+        note(f"{what} {t} {gap}: {off:.2e} of {error:.2e}")
+        assert off <= error, what
+
+    plan = ua.Plan(1, 1, N, 1, D, dtype, device=DEV)
+    one = ua.Plan(1, 1, 1, 1, D, dtype, device=DEV)
+    for place in (0, N // 2, N - 1):
+        q, v = (torch.full(plan.out_shape(0), a, dtype=dtype, device=DEV) for a in (1.0, 16.0))
+        k = torch.zeros_like(q)
+        k[0, 0, place] = x
+        v[0, 0, place] = 0
+        check(plan.window_attention(q, k, v).out, N - 1, f"prompt {place}")
+        # the same scores over a cache
+        cache = ua.Cache(1, 1, D, 1, N, E4M3, DEV)
+        cache.scales.view(torch.uint8).fill_(127)
+        codes = cache.codes.view(torch.uint8).zero_()
+        codes[1] = 0x58                                           # 16
+        codes[1, 0, 0, place] = 0
+        codes[0, 0, 0, place] = 0x38                              # 1
+        for n in (1, 20, 70):
+            qn = torch.full((1, 1, n, 1, D), x, dtype=dtype, device=DEV)
+            check(one.cache_attention(cache, qn, ints([N - n]), right=None), N - 1, f"cache {place} {n}")

@@ -251,10 +251,9 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
 #pragma unroll
             for (int x = 0; x < 8; ++x) high = fmaxf(high, s[x / 4][x % 4]);
             high = max_halves(max_quarters(high)) * a.scale2;
-            // the maximum may lag by 2^8, which costs no precision
-            const bool grow = high > m + 8.f || (m == -__builtin_inff() && high > m);
+            const bool grow = high > m + kAhead<T> || (m == -__builtin_inff() && high > m);
             if (__builtin_amdgcn_ballot_w64(grow) != 0) {
-                const float now = fmaxf(m, high), f = now == m ? 1.f : __builtin_amdgcn_exp2f(m - now);
+                const float now = fmaxf(m, high - kLift<T>), f = now == m ? 1.f : __builtin_amdgcn_exp2f(m - now);
                 m = now;
                 l *= f;
 #pragma unroll

@@ -52,6 +52,26 @@ __device__ __forceinline__ u32x4v operand_of(const f32x16v& c, int s)
     return r;
 }
 
+// A row's weights are held as exp2(score - base).  The base follows the row's largest
+// score: set kLift under it, and set again when a score is more than kAhead over it, so
+// that sums are rescaled a few times in all.  32 bits and bf16 have exponents to spare.
+// fp16 has 11 digits from 2^-14 to 2^15 and loses them below, so there the largest is
+// held between 2^13 and 2^15: weights keep their digits to 2^-27 of the largest (2^-14
+// without; a token that takes nearly all the weight left 0.9 times the others' sum at 2^-25,
+// now 1.000), and half a step is 2^-38 of it.
+template <class T>
+constexpr float kLift = __is_same(T, __bf16) ? 0.f : 13.f;
+template <class T>
+constexpr float kAhead = __is_same(T, __bf16) ? 8.f : 15.f;
+
+// Log of a row's sum from its base m and the sum l of its weights; the lift is taken out
+// first (exactly), so that one near zero keeps its digits.
+template <class T>
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return l != 0.f ? (m + kLift<T>) * kLn2 + logf(l * (1.f / static_cast<float>(1 << static_cast<int>(kLift<T>)))) : -__builtin_inff();
+}
+
 // What rounding to a pair of the type left of two values, rounded itself.
 template <class T>
 __device__ __forceinline__ uint32_t rest2(float a, float b, uint32_t rounded)
@@ -390,7 +410,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, const AttnPlace& a
     u32x2v y = {0, 0};
     if (live) y = u32x2v{pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv)};
     *reinterpret_cast<u32x2v*>(static_cast<uint16_t*>(a.out) + pl.at + d) = y;
-    if (d == 0 && a.lse != nullptr) a.lse[pl.stat] = live && l != 0.f ? m * kLn2 + logf(l) : -__builtin_inff();
+    if (d == 0 && a.lse != nullptr) a.lse[pl.stat] = live ? lse_of<T>(m, l) : -__builtin_inff();
 }
 
 }  // namespace

@@ -86,7 +86,7 @@ struct CodeLoads {
 template <class T, int DP>
 struct Rows {
     f32x16v o[DP / 32];
-    float m;                     // times log2(e); -inf until the row has seen a key
+    float m;                     // the weights' base, times log2(e); -inf until the row has seen a key
     float l;                     // of this half's keys
 
     __device__ __forceinline__ void clear()
@@ -106,10 +106,9 @@ struct Rows {
 // sees (zero times them is NaN): zeros are in their places, and `wild` says
 // where they were.
 //
-// The maximum may lag by 2^8: exp2 then gives up to 256, which costs no
-// precision, and a row's sums are rescaled a few times in all.  The weights are
-// rounded to the type for the product (relative half a step of it, as its
-// operands are), their sum is not.
+// The base lags (kLift, kAhead), which costs no precision.  The weights are rounded to
+// the type for the product (relative half a step of it, as its operands are), their sum
+// is not.
 template <class T, int DP, int NK>
 __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16], const char* ktile, const char* vtile,
                                        const uint8_t* wild, uint32_t row0, uint32_t k0, const Seen& seen, float scale2,
@@ -143,9 +142,9 @@ __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
     top = max_halves(top) * scale2;
-    const bool grow = top > r.m + 8.f || (r.m == -__builtin_inff() && top > r.m);
+    const bool grow = top > r.m + kAhead<T> || (r.m == -__builtin_inff() && top > r.m);
     if (__builtin_amdgcn_ballot_w64(grow) != 0) {
-        const float next = fmaxf(r.m, top);
+        const float next = fmaxf(r.m, top - kLift<T>);
         const float f = next == r.m ? 1.f : __builtin_amdgcn_exp2f(r.m - next);
         r.m = next;
         r.l *= f;
@@ -417,7 +416,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
             if (d < g.D) *reinterpret_cast<u32x2v*>(static_cast<uint16_t*>(a.out) + place.at + d) = y;
         }
     if (half == 0 && a.lse != nullptr)
-        a.lse[place.stat] = live && r.l != 0.f ? r.m * kLn2 + logf(r.l) : -__builtin_inff();
+        a.lse[place.stat] = live ? lse_of<T>(r.m, r.l) : -__builtin_inff();
 }
 
 // The parts of rows whose keys were walked by several workgroups, joined.  A group
@@ -496,7 +495,7 @@ __global__ __launch_bounds__(kAttnBlock) void ua2a_attention_join_kernel(AttnArg
     u32x2v y = {0, 0};
     if (live) y = u32x2v{pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv)};
     *reinterpret_cast<u32x2v*>(static_cast<uint16_t*>(a.out) + pl.at + d) = y;
-    if (d == 0 && a.lse != nullptr) a.lse[pl.stat] = live && l != 0.f ? m * kLn2 + logf(l) : -__builtin_inff();
+    if (d == 0 && a.lse != nullptr) a.lse[pl.stat] = live ? lse_of<T>(m, l) : -__builtin_inff();
 }
 
 template <class T, int DP>
