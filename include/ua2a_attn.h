@@ -137,10 +137,13 @@ int ua2a_attention_workspace(ua2a_plan_t plan, const ua2a_attention_t* args, int
  *   dv = P^T dout,  dS = P * (dout v^T - delta),  dq = scale dS k,  dk = scale dS^T q.
  * Sums are in 32 bits, in a fixed order; P and dS are rounded to the type for
  * the products with dout and q, dS to two values of it (their sum has twice the
- * digits) for the product with k, the gradients once.  So with fp16 a dS past
- * 65504 is infinite and one below 2^-25 is nothing, as in any product of that
- * type: scale the loss.  Padding may hold anything; infinities and NaN elsewhere
- * reach the gradients of rows and keys near them too.
+ * digits) for the product with k, the gradients once.  In fp16 they go in times
+ * a power of two that comes out of the sums again, so that many keys or small
+ * gradients leave them their digits: for dq one of each row's own, at which no
+ * dS passes the type; for dk and dv one between 1 and 2^15 for 128 keys and the
+ * rows that one workgroup walks, as large as their |dout|, |v| and delta allow.
+ * There a dS past 65504 is still infinite.  Padding may hold anything;
+ * infinities and NaN elsewhere reach the gradients of rows and keys near them too.
  */
 typedef struct ua2a_attention_grad_s {
     const void* dout;

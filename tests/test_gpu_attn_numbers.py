@@ -92,3 +92,100 @@ def test_one_key_takes_most_of_the_weight(gap, t):
         for n in (1, 20, 70):
             qn = torch.full((1, 1, n, 1, D), x, dtype=dtype, device=DEV)
             check(one.cache_attention(cache, qn, ints([N - n]), right=None), N - 1, f"cache {place} {n}")
+
+
+def exact_gradients(dout, q, k, v, out, lse, window, scale):
+    """dq, dk, dv of one head in float64, blocks of rows at a time."""
+    q, k, v, dout, out, lse = (x.double() for x in (q, k, v, dout, out, lse))
+    n = q.shape[0]
+    left, right, sinks, chunk = window
+    assert chunk == 1 and sinks == 0
+    dq, dk, dv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    j = torch.arange(n, device=q.device)
+    for r in range(0, n, 2048):
+        rows = slice(r, min(n, r + 2048))
+        p = j[rows]
+        seen = torch.ones(len(p), n, dtype=torch.bool, device=q.device)
+        if left is not None:
+            seen &= j >= p[:, None] - left
+        if right is not None:
+            seen &= j <= p[:, None] + right
+        prob = torch.where(seen, torch.exp(scale * (q[rows] @ k.T) - lse[rows, None]), 0.0)
+        ds = prob * (dout[rows] @ v.T - (dout[rows] * out[rows]).sum(-1, keepdim=True))
+        dq[rows] = scale * (ds @ k)
+        dk += scale * (ds.T @ q[rows])
+        dv += prob.T @ dout[rows]
+    return dq, dk, dv
+
+
+# tokens, D, window, size of dout, of v, of q and k
+GRADIENTS = [(6124, 64, (512, 512, 0, 1), 0.02, 1.0, 1.0), (6124, 64, (None, None, 0, 1), 1e-3, 1.0, 1.0),
+             (24576, 64, (None, None, 0, 1), 0.02, 1.0, 1.0), (24576, 64, (None, None, 0, 1), 1e-3, 1.0, 1.0),
+             (24576, 128, (None, 0, 0, 1), 0.02, 1.0, 1.0), (3000, 32, (None, 0, 0, 1), 1e-5, 1.0, 1.5),
+             (1000, 128, (None, 0, 0, 1), 30.0, 1.0, 1.5), (700, 64, (300, 0, 0, 1), 4.0, 700.0, 0.5), (40, 72, (None, 0, 0, 1), 1.0, 1.0, 1.0)]
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", GRADIENTS, ids=lambda v: "-".join(map(str, v[:2] + v[2][:2] + v[3:])))
+def test_gradients_beside_their_own_rounding(case, t):
+    """Root mean squares of what gradients are off by, beside that of rounding the exact
+    ones.  dq takes dS as two values of the type: what is left is its own rounding (1.2 for
+    scores, sums and chance).  dk takes dS and dv takes P rounded once more: errors as
+    large as the result's own and independent of it, 1.42 together (1.7)."""
+    n, D, window, size, vsize, qsize = case
+    dtype = TYPES[t]
+    plan = ua.Plan(1, 1, n, 1, D, dtype, device=DEV)
+    q, k = (values(plan.out_shape(0), dtype, 70 + i, qsize) for i in range(2))
+    v, dout = values(plan.out_shape(0), dtype, 72, vsize), values(plan.out_shape(0), dtype, 73, size)
+    r = plan.window_attention(q, k, v, lse=True, **as_args(window))
+    got = plan.window_attention_backward(dout, q, k, v, r.out, r.lse, **as_args(window))
+    want = exact_gradients(*(x[0, 0, :, 0] for x in (dout, q, k, v, r.out)), r.lse[0, 0, 0], window, D ** -0.5)
+    told = []
+    for g, x, times, what in zip(got, want, (1.2, 1.7, 1.7), ("dq", "dk", "dv")):
+        g = g[0, 0, :, 0]
+        assert bool(torch.isfinite(g).all()), what
+        off, own = (float((y.double() - x).norm() / x.norm()) for y in (g, x.to(dtype)))
+        told.append(f"{what} {off:.3g} of {own:.3g}")
+        assert off <= times * own, (told, times)
+    note(f"gradients {case} {t}: {told}")
+
+
+@pytest.mark.parametrize("D", [40, 128])
+def test_large_dS_in_fp16(D):
+    """Values so large that a dS passes fp16 at the power of two that its row's gradient
+    would take: dq is right all the same, past fp16's own range too; dk and dv up to it."""
+    n, window = 300, (None, 0, 0, 1)
+    plan = ua.Plan(1, 1, n, 2, D, torch.float16, device=DEV)
+    q, k = (values(plan.out_shape(0), torch.float16, 80 + i, 0.5) for i in range(2))
+    base, dout = values(plan.out_shape(0), torch.float16, 82), values(plan.out_shape(0), torch.float16, 83, 4.0)
+    j = torch.arange(n, device=DEV)
+
+    def most(v):
+        r = plan.window_attention(q, k, v, **as_args(window)).out.double()
+        sizes = []
+        for h in range(2):
+            x = [t[0, 0, :, h].double() for t in (q, k, v, dout)]
+            prob = torch.softmax(torch.where(j <= j[:, None], D ** -0.5 * (x[0] @ x[1].T), float("-inf")), -1)
+            sizes.append(float((prob * (x[3] @ x[2].T - (x[3] * r[0, 0, :, h]).sum(-1, keepdim=True))).abs().max()))
+        return max(sizes)
+
+    for wanted, outputs in ((40000.0, 3), (200000.0, 1)):
+        v = (base.float() * (wanted / most(base))).half()
+        assert bool(torch.isfinite(v).all()) and 0.8 * wanted < most(v) < 1.2 * wanted
+        # rows' |dout| is below 2^6, so they go in times 2^3 at least
+        assert most(v) * 2.0 ** 3 > 65504 and float(dout.double().norm(dim=-1).max()) < 64
+        r = plan.window_attention(q, k, v, lse=True, **as_args(window))
+        got = plan.window_attention_backward(dout, q, k, v, r.out, r.lse, **as_args(window))
+        for h in range(2):
+            want = exact_gradients(*(x[0, 0, :, h] for x in (dout, q, k, v, r.out)), r.lse[0, 0, h], window, D ** -0.5)
+            for g, x, times, what in list(zip(got, want, (1.2, 1.7, 1.7), ("dq", "dk", "dv")))[:outputs]:
+                fits = x.abs() < 65504
+                off, own = (float((y.double() - x)[fits].norm() / x[fits].norm()) for y in (g[0, 0, :, h], x.half()))
+                note(f"large dS {D} {wanted} {what}: {off:.3g} of {own:.3g}")
+                assert off <= times * own, what
+    # an infinite gradient: its row has none, the others their bits
+    dout[0, 0, 100, 1, 3] = float("inf")
+    bad = plan.window_attention_backward(dout, q, k, v, r.out, r.lse, **as_args(window)).dq
+    assert not bool(torch.isfinite(bad[0, 0, 100, 1]).any())
+    bad[0, 0, 100, 1] = got.dq[0, 0, 100, 1]
+    assert torch.equal(bad, got.dq)

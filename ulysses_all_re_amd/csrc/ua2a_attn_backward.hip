@@ -65,18 +65,43 @@ __device__ __forceinline__ void store_row(void* out, int64_t at, uint32_t D, con
         }
 }
 
+// The largest of a value over a wave's lanes.
+__device__ __forceinline__ float max_wave(float x)
+{
+#pragma unroll
+    for (int by = 1; by < 64; by *= 2) x = fmaxf(x, __shfl_xor(x, by));
+    return x;
+}
+
+// The exponent of a value that is not below zero: 2^e <= x < 2^(e + 1); 128 of infinity.
+__device__ __forceinline__ int32_t exponent_of(float x) { return static_cast<int32_t>(__float_as_uint(x) >> 23) - 127; }
+
+__device__ __forceinline__ int32_t clamped(int32_t x, int32_t lo, int32_t hi) { return x < lo ? lo : x < hi ? x : hi; }
+
+__device__ __forceinline__ float power_of_two(int32_t e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 // dq, and delta for the other kernel.  As forward, a wave has 32 rows as columns
 // of its matrix tiles and walks tiles of 64 keys: scores and dout v^T come as
 // keys x rows, dS goes on to its product with k from the registers it is in.  A
 // row's dS add up to zero, so what rounding leaves of them weighs more than in the
 // other sums; dS goes in as two values of the type (an error of dq of 1.45 times
 // its own rounding's falls to 1.0 times; three products become four, 1.69 ms 2.13).
+//
+// In fp16 a row's dS go in times 2^lift, which comes out of its sums in 32 bits: with many
+// keys P alone is among fp16's subnormals, where the second part has nothing left to say
+// (24,576 keys, dout of 1e-3: 20 times its own rounding's).  The lift puts |dout| at 2^8, and
+// a dS then is about 2^8 P |v|'s share of it.  Where one passes the type all the same (values
+// in the hundreds), the workgroup walks its keys once more with that row's lift 14 lower,
+// at which none can: |dS| <= P |dout| (|v| + |out|) < 2^9 * 2^20.5 with heads of 128.
 template <class T, int DP>
 __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(AttnGradArgs a)
 {
     constexpr int KEYS = kAttnKeys, NK = KEYS / 32;
     constexpr uint32_t kTile = KEYS * kRow<DP>;
+    constexpr bool kLifted = !__is_same(T, __bf16);
     __shared__ __attribute__((aligned(1024))) char lds[4 * kTile];           // two buffers of keys and values
+    __shared__ float sizes[kLifted ? 4 : 1][2];                              // the waves' largest |dout| and |delta|
+    __shared__ uint32_t passed;                                              // a dS passed the type
     const AttnGeom& g = a.g;
     const uint32_t item = attn_item(g, (blockIdx.y << kAttnGridLog) + blockIdx.x);
     if (item >= g.items) return;
@@ -109,7 +134,22 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
         }
         if (live && half == 0) a.delta[static_cast<int64_t>(at.unit) * g.rows + row] = delta;
         row_operands<DP>(static_cast<const uint16_t*>(a.q) + place.at, g.D, half, live, q);
-        const float lse2 = live ? lse2_of(a.lse[place.stat]) : __builtin_inff();
+        float lse2 = live ? lse2_of(a.lse[place.stat]) : __builtin_inff();
+        int32_t lift = 0;
+        if constexpr (kLifted) {
+            float norm = 0.f;                                    // |dout|^2
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) norm = dot2_sum(go[ks], go[ks], norm, T{});
+            norm = add_halves(norm);
+            lift = clamped(8 - (exponent_of(norm) >> 1), -16, 32);
+            lse2 -= static_cast<float>(lift);
+            const float most = max_wave(norm), far = max_wave(fabsf(delta));
+            if (lane == 0) {
+                sizes[wave][0] = most;
+                sizes[wave][1] = far;
+            }
+            if (threadIdx.x == 0) passed = 0;
+        }
         const int64_t base = static_cast<int64_t>(at.seq) * g.keys * g.kvl + at.kvh;
         typedef TileLoads<DP, KEYS> Loads;
         uint32_t offset[Loads::N];
@@ -136,48 +176,81 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
             }
         };
         char *ktile = lds, *other = lds + 2 * kTile;
-        load(0, ktile);
-        for (uint32_t i = 0; i < walk.total; ++i) {
-            const uint32_t k0 = position(i);
-            char* const vtile = ktile + kTile;
-            arrived();
-            if (i + 1 < walk.total) load(i + 1, other);
+        const auto walk_keys = [&]() {
+            load(0, ktile);
+            for (uint32_t i = 0; i < walk.total; ++i) {
+                const uint32_t k0 = position(i);
+                char* const vtile = ktile + kTile;
+                arrived();
+                if (i + 1 < walk.total) load(i + 1, other);
 #pragma unroll
-            for (int b = 0; b < NK; ++b) {
-                const uint32_t bk0 = k0 + b * 32;
-                if (!rows || none_seen(wtop, wbottom, bk0, bk0 + 32)) continue;
-                const bool masked = !all_seen(wtop, wbottom, bk0, bk0 + 32);
-                f32x16v s, dp;
+                for (int b = 0; b < NK; ++b) {
+                    const uint32_t bk0 = k0 + b * 32;
+                    if (!rows || none_seen(wtop, wbottom, bk0, bk0 + 32)) continue;
+                    const bool masked = !all_seen(wtop, wbottom, bk0, bk0 + 32);
+                    f32x16v s, dp;
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    s[x] = 0.f;
-                    dp[x] = -delta;
-                }
-#pragma unroll
-                for (int ks = 0; ks < DP / 16; ++ks) s = mfma<T>(along<DP>(ktile, b * 32, ks), q[ks], s);
-#pragma unroll
-                for (int ks = 0; ks < DP / 16; ++ks) dp = mfma<T>(along<DP>(vtile, b * 32, ks), go[ks], dp);
-#pragma unroll
-                for (int x = 0; x < 16; ++x) dp[x] *= __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], a.scale2, -lse2));
-                if (masked) {
-#pragma unroll
-                    for (int x = 0; x < 16; ++x)
-                        if (!sees(seen, bk0 + ((x / 4) * 8 + half * 4 + x % 4))) dp[x] = 0.f;
-                }
-                const u32x4v ds[2] = {operand_of<T>(dp, 0), operand_of<T>(dp, 1)};
-                const u32x4v rest[2] = {rest_of<T>(dp, ds[0], 0), rest_of<T>(dp, ds[1], 1)};
-#pragma unroll
-                for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const u32x4v k = transposed<DP>(ktile, b * 32, t, db);
-                        dq[db] = mfma<T>(k, ds[t], dq[db]);
-                        dq[db] = mfma<T>(k, rest[t], dq[db]);
+                    for (int x = 0; x < 16; ++x) {
+                        s[x] = 0.f;
+                        dp[x] = -delta;
                     }
+#pragma unroll
+                    for (int ks = 0; ks < DP / 16; ++ks) s = mfma<T>(along<DP>(ktile, b * 32, ks), q[ks], s);
+#pragma unroll
+                    for (int ks = 0; ks < DP / 16; ++ks) dp = mfma<T>(along<DP>(vtile, b * 32, ks), go[ks], dp);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) dp[x] *= __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], a.scale2, -lse2));
+                    if (masked) {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            if (!sees(seen, bk0 + ((x / 4) * 8 + half * 4 + x % 4))) dp[x] = 0.f;
+                    }
+                    const u32x4v ds[2] = {operand_of<T>(dp, 0), operand_of<T>(dp, 1)};
+                    const u32x4v rest[2] = {rest_of<T>(dp, ds[0], 0), rest_of<T>(dp, ds[1], 1)};
+#pragma unroll
+                    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const u32x4v k = transposed<DP>(ktile, b * 32, t, db);
+                            dq[db] = mfma<T>(k, ds[t], dq[db]);
+                            dq[db] = mfma<T>(k, rest[t], dq[db]);
+                        }
+                }
+                char* const t = ktile;
+                ktile = other;
+                other = t;
             }
-            char* const t = ktile;
-            ktile = other;
-            other = t;
+        };
+        walk_keys();
+        if constexpr (kLifted) {
+            // an infinite dS leaves no finite value in its row: infinity times zero is NaN
+            const bool past_range = live && !(fabsf(dq[0][0]) < __builtin_inff());
+            if (past_range) passed = 1;
+            if (threadIdx.x == 0) {
+                float most = 0.f, far = 0.f;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    most = fmaxf(most, sizes[w][0]);
+                    far = fmaxf(far, sizes[w][1]);
+                }
+                float* const to = a.sizes + (static_cast<int64_t>(at.unit) * g.tiles + at.tile) * 2;
+                to[0] = sqrtf(most);
+                to[1] = far;
+            }
+            __syncthreads();
+            if (passed != 0) {
+                if (past_range) {
+                    lift -= 14;
+                    lse2 += 14.f;
+                }
+                zero(dq);
+                walk_keys();
+            }
+            const float down = power_of_two(-lift);
+#pragma unroll
+            for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) dq[db][x] *= down;
         }
     }
     if (in) store_row<T, DP>(a.dq, place.at, g.D, dq, a.scale, live);
@@ -188,6 +261,12 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
 // dout v^T come as rows x keys, and P and dS go on from their registers to the
 // products with dout and q.  Where a tile's walk is long for the call, workgroups of
 // their own walk parts of it, whose sums a third kernel joins in order.
+//
+// In fp16 P and dS go in times 2^lift, between 1 and 2^15, which comes out of the sums in 32
+// bits: with many keys both are among fp16's subnormals otherwise (24,576 keys, dout of
+// 1e-3: dk off by 25 times its own rounding).  The workgroup takes the largest lift at
+// which no dS can pass 2^15, from its own |v| and the largest |dout| and |delta| that the
+// rows' kernel left for each of its tiles: |dS| <= P (|dout| |v| + |delta|).
 template <class T, int DP>
 __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(AttnGradArgs a)
 {
@@ -203,6 +282,8 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(Attn
     __shared__ __attribute__((aligned(1024))) char lds[4 * kTile + kKeyTile];
     char* const ktile = lds + 4 * kTile;
     __shared__ __attribute__((aligned(16))) float stats[2 * 2 * ROWS];       // ... of lse and -delta
+    constexpr bool kLifted = !__is_same(T, __bf16);
+    __shared__ float sizes[kLifted ? 4 : 1][3];                              // the waves' largest |v|^2, |dout| and |delta|
     const AttnGeom& g = a.g;
     const uint32_t item = attn_item(g, (blockIdx.y << kAttnGridLog) + blockIdx.x);
     if (item >= g.items) return;
@@ -217,6 +298,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(Attn
     f32x16v dk[DP / 32], dv[DP / 32];
     zero(dk);
     zero(dv);
+    float down = 1.f;                                            // undoes the lift of P and dS
     if (static_cast<int32_t>(first) < seq.end) {
         u32x4v v[DP / 16], k[kKeysInLds ? 1 : DP / 16];
         row_operands<DP>(static_cast<const uint16_t*>(a.v) + to, g.D, half, live, v);
@@ -243,6 +325,40 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(Attn
         const RowWalk walk = row_walk(g, seers_of(g.win, static_cast<int32_t>(first), end, seq.end), ROWS);
         const uint32_t from = split_at(walk.total, at.parts, at.at.split), upto = split_at(walk.total, at.parts, at.at.split + 1);
         const uint32_t live_rows = static_cast<uint32_t>(seq.last) * g.group;
+        int32_t lift = 0;
+        if constexpr (kLifted) {
+            float norm = 0.f, most = 0.f, far = 0.f;             // |v|^2; of the rows to walk, |dout| and |delta|
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) norm = dot2_sum(v[ks], v[ks], norm, T{});
+            norm = add_halves(norm);
+            const uint32_t tiles = (g.rows + kAttnRows - 1) / kAttnRows;
+            if (from < upto) {
+                const uint32_t last = umin32((walk.from + upto) * ROWS, live_rows);
+                for (uint32_t t = (walk.from + from) * ROWS / kAttnRows + threadIdx.x; t * kAttnRows < last; t += kAttnBlock) {
+                    const float* const of = a.sizes + (static_cast<int64_t>(at.at.unit) * tiles + t) * 2;
+                    most = fmaxf(most, of[0]);
+                    far = fmaxf(far, of[1]);
+                }
+            }
+            norm = max_wave(norm);
+            most = max_wave(most);
+            far = max_wave(far);
+            if (lane == 0) {
+                sizes[wave][0] = norm;
+                sizes[wave][1] = most;
+                sizes[wave][2] = far;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                norm = fmaxf(norm, sizes[w][0]);
+                most = fmaxf(most, sizes[w][1]);
+                far = fmaxf(far, sizes[w][2]);
+            }
+            // P to 1, and any dS, within 2^15, where that takes no less than 1
+            lift = __builtin_amdgcn_readfirstlane(clamped(14 - exponent_of(sqrtf(norm) * most + far), 0, 15));
+            down = power_of_two(-lift);
+        }
         typedef TileLoads<DP, ROWS> Loads;
         uint32_t bytes[Loads::N];
 #pragma unroll
@@ -268,7 +384,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(Attn
                 const bool is_lse = threadIdx.x < ROWS;
                 float x = is_lse ? __builtin_inff() : 0.f;
                 if (r < live_rows)
-                    x = is_lse ? lse2_of(a.lse[row_place(g, at.at, r).stat])
+                    x = is_lse ? lse2_of(a.lse[row_place(g, at.at, r).stat]) - static_cast<float>(lift)
                                : -a.delta[static_cast<int64_t>(at.at.unit) * g.rows + r];
                 stat[threadIdx.x] = x;
             }
@@ -341,6 +457,15 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_keys_kernel(Attn
         }
     }
     if (!in) return;
+    if constexpr (kLifted) {
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                dk[db][x] *= down;
+                dv[db][x] *= down;
+            }
+    }
     if (at.parts > 1) {
         float* line = a.partial + part_line(g, a.keys, at.at.unit, at.at.split, j) * 2 * g.D;
 #pragma unroll

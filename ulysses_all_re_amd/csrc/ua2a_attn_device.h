@@ -56,9 +56,9 @@ __device__ __forceinline__ u32x4v operand_of(const f32x16v& c, int s)
 // score: set kLift under it, and set again when a score is more than kAhead over it, so
 // that sums are rescaled a few times in all.  32 bits and bf16 have exponents to spare.
 // fp16 has 11 digits from 2^-14 to 2^15 and loses them below, so there the largest is
-// held between 2^13 and 2^15: weights keep their digits to 2^-27 of the largest (2^-14
-// without; a token that takes nearly all the weight left 0.9 times the others' sum at 2^-25,
-// now 1.000), and half a step is 2^-38 of it.
+// held between 2^13 and 2^15: weights keep their digits to 2^-27 of the largest, and half
+// a step is 2^-38 of it (2^-14 and 2^-25 without: beside a token 17.4 nats above them the
+// others of its walk were nothing).
 template <class T>
 constexpr float kLift = __is_same(T, __bf16) ? 0.f : 13.f;
 template <class T>

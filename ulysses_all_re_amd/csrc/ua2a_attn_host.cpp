@@ -195,6 +195,9 @@ int64_t most_seers(const AttnGeom& g)
     return tokens < g.n ? tokens * g.group : g.rows;
 }
 
+// The sizes of tiles of rows, whole lines of 16 bytes
+int64_t size_floats(const AttnGeom& g) { return ceil_div(int64_t(g.units) * ceil_div(g.rows, kAttnRows) * 2, 4) * 4; }
+
 // How the keys' gradients go to workgroups.  Sinks are seen by all rows, other
 // keys by a window of them, so a tile of sinks would be walked long after the
 // rest: tiles are walked in parts of about a window, and of less where the call
@@ -221,7 +224,7 @@ void backward_shape(AttnGradArgs* a)
         first = lead == 0 || first < 1 ? 1 : first > 64 ? 64 : first;
         rest = rest < 1 ? 1 : rest > 64 ? 64 : rest;
         const int64_t lines = (first > 1 ? first * span : 0) + (rest > 1 ? rest * (g.keys - span) : 0);
-        if (lines * g.units * g.D * 8 <= (int64_t(256) << 20)) break;
+        if (lines == 0 || lines * g.units * g.D * 8 + size_floats(g) * 4 <= (int64_t(256) << 20)) break;
     }
     set_items(&g, tiles, 1);
     g.order = order_of(g, true);
@@ -251,7 +254,7 @@ int64_t delta_floats(const AttnGeom& g) { return ceil_div(int64_t(g.units) * g.r
 
 int64_t backward_workspace(const AttnGradArgs& a)
 {
-    return (delta_floats(a.g) + part_lines(a) * 2 * a.g.D) * 4;
+    return (delta_floats(a.g) + size_floats(a.g) + part_lines(a) * 2 * a.g.D) * 4;
 }
 
 int plan_backward(ua2a_plan_t plan, const ua2a_attention_grad_t* n, AttnLaunch* L)
@@ -483,7 +486,8 @@ int ua2a_attention_backward(ua2a_plan_t plan, const ua2a_attention_grad_t* n, vo
     a.scale = n->scale;
     a.scale2 = n->scale * kLog2e;
     a.delta = static_cast<float*>(n->workspace);
-    a.partial = a.delta + delta_floats(g);
+    a.sizes = a.delta + delta_floats(g);
+    a.partial = a.sizes + size_floats(g);
     const AttnGeom by_keys = g;
     L.kernel = AttnKernel::GradRows;
     set_items(&g, ceil_div(g.rows, kAttnRows), 1);

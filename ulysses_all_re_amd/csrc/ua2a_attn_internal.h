@@ -53,6 +53,7 @@ struct AttnGradArgs {
     void* dk;
     void* dv;
     float* delta;                // [units][rows]
+    float* sizes;                // [units][tiles of rows][2]: largest |dout| and |delta| of the tile's rows
     float scale, scale2;
     float* partial;              // parts' sums: [KeyTiles' lines][2][D]
 };
