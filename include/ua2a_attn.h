@@ -100,7 +100,7 @@ typedef struct ua2a_window_s {
  * of the row's largest, and below that is off by 2^-38 of it at most.)  What a row does not see plays no part in it,
  * infinities and NaN included; a row whose weights are all zero is zeros.
  * D must be a multiple of 8 up to 128; all tensors 16-byte aligned; scale > 0
- * and finite, in powers of two too (scale * log2 e).
+ * and finite, in powers of two too (scale * log2 e), and so must scores be.
  * No output may overlap an input, another output or the workspace.
  * Errors: INVALID_ARG (NULL, type, scale, chunk < 1, a bound < -1), SHAPE (D,
  * kv_heads not a multiple of w or no divisor of H, H/w * D over 2^22, 2^31
@@ -144,6 +144,7 @@ int ua2a_attention_workspace(ua2a_plan_t plan, const ua2a_attention_t* args, int
  * rows that one workgroup walks, as large as their |dout|, |v| and delta allow.
  * There a dS past 65504 is still infinite.  Padding may hold anything;
  * infinities and NaN elsewhere reach the gradients of rows and keys near them too.
+ * lse is in 32 bits, so P is off by about 2^-22 of the largest score's size.
  */
 typedef struct ua2a_attention_grad_s {
     const void* dout;

@@ -189,3 +189,49 @@ def test_large_dS_in_fp16(D):
     assert not bool(torch.isfinite(bad[0, 0, 100, 1]).any())
     bad[0, 0, 100, 1] = got.dq[0, 0, 100, 1]
     assert torch.equal(bad, got.dq)
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("power", [5, 15, 16, 17, 22, 25, 26, 27, 28, 31, 33, 40, 100])
+def test_scores_of_any_size(power, t):
+    """Scores of +-2^power, about, and half of that, no whole steps in powers of two: the largest take all of the weight,
+    shared alike, by every kernel, from the first key to the last."""
+    dtype = TYPES[t]
+    N, D, scale = 200, 64, 1.37 * 2.0 ** power
+    plan, one = ua.Plan(1, 1, N, 1, D, dtype, device=DEV), ua.Plan(1, 1, 1, 1, D, dtype, device=DEV)
+    scale32 = float(torch.tensor(scale))
+    codes = {0.5: 0x30, 1.0: 0x38, -1.0: 0xb8, 0.0: 0}
+    v = (torch.arange(N * D, device=DEV).view(N, D) % 15 - 7).to(dtype) / 8
+    cache = ua.Cache(1, 1, D, 1, N, E4M3, DEV)
+    cache.scales.view(torch.uint8).fill_(127)
+    held = cache.codes.view(torch.uint8)
+    held[1, 0, 0, :, 0] = (v.float()).to(E4M3).view(torch.uint8)
+    # k's first value of most keys, and where the largest stand
+    for rest, top, places in ((0.5, 1.0, [0]), (0.5, 1.0, [130]), (-1.0, 0.5, [199]), (0.0, 1.0, [3, 140]), (-1.0, 0.0, [64, 65, 66, 67]),
+                              (-1.0, -1.0, [0])):
+        k = torch.zeros(1, 1, N, 1, D, dtype=dtype, device=DEV)
+        k[..., 0] = rest
+        held[0].zero_()
+        held[0, ..., 0] = codes[rest]
+        for p in places:
+            k[0, 0, p, 0, 0] = top
+            held[0, 0, 0, p, 0, 0] = codes[top]
+        q = torch.zeros_like(k)
+        q[..., 0] = 0.73
+        few = list(range(N)) if rest == top else places
+        by = scale32 * float(q[0, 0, 0, 0, 0])                      # of a key's first value
+        others = torch.exp(torch.tensor((rest - top) * by, dtype=torch.float64)).item() if rest != top else 0.0
+        left = [j for j in range(N) if j not in few]
+        x = v.double()
+        want = (x[few].sum(0) + others * x[left].sum(0)) / (len(few) + others * len(left))
+        # a weight and the result are rounded to the type; 2^-20 for the sums of equal weights
+        error = 2.0 ** (-11 if t == "fp16" else -8) * 2 * 1.02
+        size = (x[few].abs().sum(0) + others * x[left].abs().sum(0)) / (len(few) + others * len(left))
+        r = plan.window_attention(q, k, v.view(1, 1, N, 1, D), scale=scale, lse=True)
+        assert bool(((r.out.double()[0, 0, :, 0] - want).abs() <= size * error + 2.0 ** -24).all()), (rest, top)
+        lse = top * by + torch.log(torch.tensor(len(few) + others * len(left), dtype=torch.float64)).item()
+        # three roundings of 32 bits of a number of its size
+        assert bool(((r.lse.double() - lse).abs() <= abs(lse) * 2.0 ** -22 + 2.0 ** -20).all()), (rest, top)
+        for n in (1, 16, 20, 70):
+            got = one.cache_attention(cache, q[:, :, :n].contiguous(), ints([N - n]), right=None, scale=scale)
+            assert bool(((got.double()[0, 0, :, 0] - want).abs() <= size * error + 2.0 ** -24).all()), (rest, top, n)

@@ -191,6 +191,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
 #pragma unroll
     for (int db = 0; db < DP / 16; ++db) o[db] = f32x4v{0.f, 0.f, 0.f, 0.f};
     float m = -__builtin_inff(), l = 0.f;
+    bool far = false;                                                        // uniform: some row's base is (far_base)
     if (seq.last > seq.first) {
         const Seen top = seen_by_row(g, seq, 0), bottom = seen_by_row(g, seq, past - 1);
         const Seen seen = seen_by_row(g, seq, place.row);
@@ -251,18 +252,26 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
 #pragma unroll
             for (int x = 0; x < 8; ++x) high = fmaxf(high, s[x / 4][x % 4]);
             high = max_halves(max_quarters(high)) * a.scale2;
-            const bool grow = high > m + kAhead<T> || (m == -__builtin_inff() && high > m);
+            const bool grow = ahead_of<T>(high, m);
             if (__builtin_amdgcn_ballot_w64(grow) != 0) {
-                const float now = fmaxf(m, high - kLift<T>), f = now == m ? 1.f : __builtin_amdgcn_exp2f(m - now);
+                const float now = fmaxf(m, base_of<T>(high)), f = now == m ? 1.f : __builtin_amdgcn_exp2f(m - now);
                 m = now;
+                far = __builtin_amdgcn_ballot_w64(far_base(now)) != 0;
                 l *= f;
 #pragma unroll
                 for (int db = 0; db < DP / 16; ++db) o[db] *= f;
             }
             const float mm = m == -__builtin_inff() ? 0.f : m;
+            float times = a.scale2, plus = -mm;
+            if (far) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x) s[x / 4][x % 4] = far_exponent(s[x / 4][x % 4], a.scale2, mm);
+                times = 1.f;
+                plus = 0.f;
+            }
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-                s[x / 4][x % 4] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x / 4][x % 4], a.scale2, -mm));
+                s[x / 4][x % 4] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x / 4][x % 4], times, plus));
                 l += s[x / 4][x % 4];
             }
             const u32x4v p = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]), pack2<T>(s[1][0], s[1][1]),

@@ -64,6 +64,34 @@ constexpr float kLift = __is_same(T, __bf16) ? 0.f : 13.f;
 template <class T>
 constexpr float kAhead = __is_same(T, __bf16) ? 8.f : 15.f;
 
+// A weight's exponent is fma(score, scale2, -base), and the base is a rounded product: the
+// largest score's own exponent is off by up to half a step of its size, which the sums and
+// their divisor share.  Past kFar, a step of 2^-7, both are taken from rounded products and
+// nothing is lifted, or from 2^26 on weights would pass fp16, and from 2^33 on 32 bits.
+constexpr float kFar = 65536.f;
+__device__ __forceinline__ bool far_base(float m) { return fabsf(m) > kFar && fabsf(m) < __builtin_inff(); }
+
+template <class T>
+__device__ __forceinline__ float base_of(float top)
+{
+    return far_base(top) ? top : top - kLift<T>;
+}
+
+// Whether a row whose largest score is `top` needs another base.  The difference is exact
+// where it is small; infinite where there was no score.
+template <class T>
+__device__ __forceinline__ bool ahead_of(float top, float m)
+{
+    return top - m > kAhead<T>;
+}
+
+__device__ __forceinline__ float far_exponent(float score, float scale2, float m)
+{
+    float x = score * scale2;
+    asm("" : "+v"(x));                                           // no fma of the two
+    return x - m;
+}
+
 // Log of a row's sum from its base m and the sum l of its weights; the lift is taken out
 // first (exactly), so that one near zero keeps its digits.
 template <class T>

@@ -88,6 +88,7 @@ struct Rows {
     f32x16v o[DP / 32];
     float m;                     // the weights' base, times log2(e); -inf until the row has seen a key
     float l;                     // of this half's keys
+    bool far;                    // uniform: some row's base is (far_base)
 
     __device__ __forceinline__ void clear()
     {
@@ -97,6 +98,7 @@ struct Rows {
             for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
         m = -__builtin_inff();
         l = 0.f;
+        far = false;
     }
 };
 
@@ -142,11 +144,12 @@ __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
     top = max_halves(top) * scale2;
-    const bool grow = top > r.m + kAhead<T> || (r.m == -__builtin_inff() && top > r.m);
+    const bool grow = ahead_of<T>(top, r.m);
     if (__builtin_amdgcn_ballot_w64(grow) != 0) {
-        const float next = fmaxf(r.m, top - kLift<T>);
+        const float next = fmaxf(r.m, base_of<T>(top));
         const float f = next == r.m ? 1.f : __builtin_amdgcn_exp2f(r.m - next);
         r.m = next;
+        r.far = __builtin_amdgcn_ballot_w64(far_base(next)) != 0;
         r.l *= f;
 #pragma unroll
         for (int db = 0; db < DP / 32; ++db)
@@ -154,12 +157,21 @@ __device__ __forceinline__ void attend(Rows<T, DP>& r, const u32x4v (&q)[DP / 16
             for (int i = 0; i < 16; ++i) r.o[db][i] *= f;
     }
     const float m = r.m == -__builtin_inff() ? 0.f : r.m;
+    float times = scale2, plus = -m;
+    if (r.far) {
+#pragma unroll
+        for (int b = 0; b < NK; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[b][i] = far_exponent(s[b][i], scale2, m);
+        times = 1.f;
+        plus = 0.f;
+    }
     float sum = 0.f;
 #pragma unroll
     for (int b = 0; b < NK; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], scale2, -m));
+            s[b][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][i], times, plus));
             sum += s[b][i];
         }
     r.l += sum;
