@@ -235,3 +235,54 @@ def test_scores_of_any_size(power, t):
         for n in (1, 16, 20, 70):
             got = one.cache_attention(cache, q[:, :, :n].contiguous(), ints([N - n]), right=None, scale=scale)
             assert bool(((got.double()[0, 0, :, 0] - want).abs() <= size * error + 2.0 ** -24).all()), (rest, top, n)
+
+
+@pytest.mark.parametrize("t,fmt,code,byte", [("fp16", E4M3, 0x7e, 136), ("fp16", E5M2, 0x7b, 129), ("bf16", E4M3, 0x7e, 248),
+                                             ("bf16", E5M2, 0x7b, 241)], ids=["fp16-e4m3", "fp16-e5m2", "bf16-e4m3", "bf16-e5m2"])
+def test_codes_past_the_type_are_its_largest(t, fmt, code, byte):
+    """The format's largest code at a scale that takes it past the type: a query that sees
+    that position alone gets the type's largest value, by every kernel of the cache; as a
+    key it is the same value too."""
+    dtype = TYPES[t]
+    plan = ua.Plan(1, 1, 1, 2, 64, dtype, device=DEV)
+    cache, _ = make_cache(1, 2, 300, 2, 64, fmt, 8)
+    codes, scales = cache.codes.view(torch.uint8), cache.scales.view(torch.uint8)
+    codes[:, 0, 0, 70, 1, 7], codes[:, 0, 0, 70, 1, 40] = code, code | 0x80
+    scales[:, 0, 0, 70, 1] = byte
+    kk, vv = plan.cache_read(cache, 300)
+    most = torch.finfo(dtype).max
+    assert float(vv[0, 0, 70, 1, 7]) == most and float(vv[0, 0, 70, 1, 40]) == -most
+    for n in (1, 3, 16, 20, 32, 33, 70):
+        # (bf16: the largest value times |q7 - q40|, which is up to 8, has to be a score of 32 bits)
+        q = values((1, 2, n, 2, 64), dtype, 9, 1.0 if t == "fp16" else 2.0 ** -4)
+        start = 70 - n // 2
+        got, want = plan.cache_attention(cache, q, ints([start, 5]), left=0)[0, 0], vv[0, 0, start:start + n]
+        # the row of the largest key has a score in the ten thousands (in fp16; any size in
+        # bf16), whose exponent is off by 2^-10: a weight between two values of the type in
+        # the product, not in the sum, so half a step of a weight and half of the result
+        near = want.double().abs() * 2 * (2.0 ** -11 if t == "fp16" else 2.0 ** -8) * 1.02
+        assert bool(((got.double() - want.double()).abs() <= near).all()), n
+        rest = [i for i in range(n) if start + i != 70]
+        assert torch.equal(got[rest], want[rest]), n
+        # a score of a quarter of the key's largest value: it takes all of the weight, or none
+        q.zero_()
+        q[0, 0, :, 1, 7] = 0.25
+        got = plan.cache_attention(cache, q, ints([100, 5]), scale=1.0)
+        assert torch.equal(got[0, 0, :, 1], vv[0, 0, 70, 1].expand(n, -1)), n
+        got = plan.cache_attention(cache, -q, ints([100, 5]), scale=1.0)
+        assert float(got[0, 0, :, 1].abs().max()) < 100.0, n
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+def test_means_of_the_largest_values(t):
+    """Values that are all the type's largest, or infinite: so are their means, whatever
+    the weights, and for an infinity the kind is kept."""
+    dtype = TYPES[t]
+    N, D = 500, 64
+    plan = ua.Plan(1, 1, N, 2, D, dtype, device=DEV)
+    q, k = (values(plan.out_shape(0), dtype, 90 + i) for i in range(2))
+    # weights' sums in 32 bits stay finite: bf16's largest value times no more than one key's weight
+    window = (0, 0, 0, 1) if t == "bf16" else (None, 0, 0, 1)
+    for x in (torch.finfo(dtype).max, -torch.finfo(dtype).max, float("inf"), float("-inf")):
+        v = torch.full(plan.out_shape(0), x, dtype=dtype, device=DEV)
+        assert torch.equal(plan.window_attention(q, k, v, **as_args(window)).out, v), x

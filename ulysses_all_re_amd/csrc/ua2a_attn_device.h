@@ -42,6 +42,17 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// A result that is finite within the type.  The weights of a row's sums are rounded and the
+// sum of the weights is not, so a mean of the type's largest values may come out a little
+// past it: that is the largest, no infinity.
+template <class T>
+constexpr float kMost = __is_same(T, __bf16) ? 3.3895314e38f : 65504.f;
+template <class T>
+__device__ __forceinline__ float within(float x)
+{
+    return fabsf(x) < __builtin_inff() ? fminf(fmaxf(x, -kMost<T>), kMost<T>) : x;
+}
+
 // Registers 8s .. 8s + 7 of a result, rounded to the type: B's operand of depth step s.
 template <class T>
 __device__ __forceinline__ u32x4v operand_of(const f32x16v& c, int s)
@@ -436,7 +447,8 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, const AttnPlace& a
     if (!live && a.keep) return;
     const float inv = live && l != 0.f ? 1.f / l : 0.f;
     u32x2v y = {0, 0};
-    if (live) y = u32x2v{pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv)};
+    if (live)
+        y = u32x2v{pack2<T>(within<T>(x[0] * inv), within<T>(x[1] * inv)), pack2<T>(within<T>(x[2] * inv), within<T>(x[3] * inv))};
     *reinterpret_cast<u32x2v*>(static_cast<uint16_t*>(a.out) + pl.at + d) = y;
     if (d == 0 && a.lse != nullptr) a.lse[pl.stat] = live ? lse_of<T>(m, l) : -__builtin_inff();
 }

@@ -415,7 +415,18 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_kernel(AttnArgs 
         return;
     }
     if (!live && a.keep) return;
-    const float inv = live && r.l != 0.f ? 1.f / r.l : 0.f;
+    float inv = live && r.l != 0.f ? 1.f / r.l : 0.f, top = 0.f;
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(r.o[db][i]));
+    if (top * inv > kMost<T>) {                                  // rare: one look at the largest (`within` on each: attn_small 8.1 us, 8.6)
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r.o[db][i] = within<T>(r.o[db][i] * inv);
+        inv = 1.f;
+    }
 #pragma unroll
     for (int db = 0; db < DP / 32; ++db)
 #pragma unroll
@@ -505,7 +516,8 @@ __global__ __launch_bounds__(kAttnBlock) void ua2a_attention_join_kernel(AttnArg
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
     u32x2v y = {0, 0};
-    if (live) y = u32x2v{pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv)};
+    if (live)
+        y = u32x2v{pack2<T>(within<T>(x[0] * inv), within<T>(x[1] * inv)), pack2<T>(within<T>(x[2] * inv), within<T>(x[3] * inv))};
     *reinterpret_cast<u32x2v*>(static_cast<uint16_t*>(a.out) + pl.at + d) = y;
     if (d == 0 && a.lse != nullptr) a.lse[pl.stat] = live ? lse_of<T>(m, l) : -__builtin_inff();
 }
