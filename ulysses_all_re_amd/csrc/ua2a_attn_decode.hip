@@ -218,8 +218,10 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
             const int32_t rows = i < to ? least_of(seq.end - static_cast<int32_t>(k0), kTileKeys) : 0;
             constexpr int32_t kFormat = E4M3 ? UA2A_FORMAT_E4M3 : UA2A_FORMAT_E5M2;
             const uint32_t ktop = WaveCodes<T, DP>::template put<E4M3>(w.k, w.ks, tile, g.D);
-            if (__builtin_amdgcn_ballot_w64(ktop >= high_scale<T>(kFormat)) != 0)
+            if (__builtin_amdgcn_ballot_w64(ktop >= high_scale<T>(kFormat)) != 0) {
+                wave_order();                                    // over what other lanes put there
                 decode_again<T, DP>(tile, g, a.codes + j0 * g.D, a.scales + j0 * g.nb, rows, kFormat, lane, 64);
+            }
             wave_order();
             f32x4v s[2];
 #pragma unroll
@@ -233,9 +235,11 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_decode_kernel(At
             // zero times an infinity is NaN, and the weights' second parts may be zero or less
             const bool apart = masked || (!E4M3 && __builtin_amdgcn_ballot_w64(WaveCodes<T, DP>::unbounded(w.v)) != 0);
             load(i + 8, w);
-            if (__builtin_amdgcn_ballot_w64(vtop >= high_scale<T>(kFormat)) != 0)
+            if (__builtin_amdgcn_ballot_w64(vtop >= high_scale<T>(kFormat)) != 0) {
+                wave_order();
                 decode_again<T, DP>(tile, g, a.codes + a.part + j0 * g.D, a.scales + a.part_scales + j0 * g.nb, rows, kFormat,
                                     lane, 64);
+            }
             wave_order();
             bool odd = false;
             if (apart) {
