@@ -97,7 +97,8 @@ typedef struct ua2a_window_s {
  * Types bf16 and fp16.  Scores, softmax and sums are in 32 bits; the weights
  * exp(s - m) are rounded to the type for the product with v, their sum is
  * not; out is rounded once.  (In fp16 a weight has its 11 digits down to 2^-27
- * of the row's largest, and below that is off by 2^-38 of it at most.)  What a row does not see plays no part in it,
+ * of the row's largest, and below that is off by 2^-38 of it at most.  In bf16
+ * the sums hold up to 2^8 times v: |v| times the keys stays below 2^119.)  What a row does not see plays no part in it,
  * infinities and NaN included; a row whose weights are all zero is zeros.
  * D must be a multiple of 8 up to 128; all tensors 16-byte aligned; scale > 0
  * and finite, in powers of two too (scale * log2 e), and so must scores be.

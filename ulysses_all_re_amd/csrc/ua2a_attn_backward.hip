@@ -8,10 +8,14 @@
 // instead of five (and an eighth, for dS's second part), and in return no atomics,
 // so equal inputs give equal bits.
 //
-// The matrix products and what stands between them bound the first kernel, waiting
-// for operands in LDS the second: 12 heads of 128 over 32,760 tokens, a window of three
-// frames of 1560 and the first, take 2.1 ms and 3.1 (matrix units busy 60 % and 39 % of
-// the time); the eight products alone would be 4.0 ms at a large matrix product's rate.
+// The matrix products and what stands between them bound the first kernel, waiting the
+// second: 12 heads of 128 over 32,760 tokens, a window of three frames of 1560 and the
+// first, take 2.1 ms and 3.1 (matrix units busy 60 % and 39 % of the time, waves waiting
+// 33 % and 59 %); the eight products alone would be 4.0 ms at a large matrix product's
+// rate.  Some of the waiting is for operands in LDS, some for memory in every tile: the
+// next tile's lse and delta pass through registers, whose wait takes the tile's loads with
+// it, and both kernels wait for the next tile where they first use operands that were
+// loaded before the loop (see TileLoads).
 #include "ua2a_attn_device.h"
 
 namespace ua2a {
@@ -264,7 +268,7 @@ __global__ __launch_bounds__(kAttnBlock, 2) void ua2a_attention_rows_kernel(Attn
 //
 // In fp16 P and dS go in times 2^lift, between 1 and 2^15, which comes out of the sums in 32
 // bits: with many keys both are among fp16's subnormals otherwise (24,576 keys, dout of
-// 1e-3: dk off by 25 times its own rounding).  The workgroup takes the largest lift at
+// 1e-3: dk off by 20 times its own rounding).  The workgroup takes the largest lift at
 // which no dS can pass 2^15, from its own |v| and the largest |dout| and |delta| that the
 // rows' kernel left for each of its tiles: |dS| <= P (|dout| |v| + |delta|).
 template <class T, int DP>

@@ -198,7 +198,9 @@ __device__ __forceinline__ u32x4v transposed(const char* tile, uint32_t row0, in
 // chunks, 16 bytes a lane, to consecutive places; lanes fetch the chunks that
 // belong there.  Reads past the descriptor's bytes give zeros: rows that do not
 // exist, and chunks past D (kNowhere).  The loads are outstanding until
-// `arrived`, which the compiler does not know: nothing may read the tile before.
+// `arrived`, which the compiler does not know: nothing may read the tile before.  Nor does
+// it know of the wait there: registers that it loads before a loop it waits for once more
+// at their first use within, and for the loads to LDS issued since.
 constexpr uint32_t kNowhere = 0x80000000u;
 
 template <int DP, int ROWS>

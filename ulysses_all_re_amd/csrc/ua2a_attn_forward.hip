@@ -9,15 +9,20 @@
 // lane's own work but for the other half's, and the weights go on to the
 // product with the values from the registers they are in.
 //
-// The matrix products and the exponentials bound it, about as much of either with
+// The matrix products and the exponentials take its time, about as much of either with
 // heads of 128: 40 heads over 75,600 tokens, a window of three frames of 3600 and
-// the first, take 21.3 ms, 970 TFLOP/s, where a large matrix product of the library
-// reaches 1162 on this card (matrix units busy 44 % of the time, the others 42).
+// the first, take 21.4 ms (22.4 on a slower card), 966 TFLOP/s, where a product of two
+// 8192 x 8192 matrices by the library reaches 1162 (matrix units busy 44 % of the time,
+// the others 42, waves waiting a third).  Part of that waiting is the next tile's loads:
+// the compiler knows nothing of the wait in `arrived`, takes the rows' operands for
+// outstanding still, and waits for all loads before the first product of each tile.
+// The other workgroup on the CU fills most of it; the variants below were timed with it.
 // Everything visible, 32 heads of 128 over 8192 tokens: 938 TFLOP/s; heads of 64, with
 // as many exponentials for half the products, 886; a window of 1024 of such, whose walks
-// are 18 tiles with a quarter of them masked, 564 to 670.  A cache's keys are decoded on
-// their way (1560 tokens of 12 heads over 7,800 positions: 600 TFLOP/s).  Tiles go straight from memory to LDS, in two buffers with a barrier a tile
-// (24.6 ms through registers, 22.5 so); a row's halves are joined in registers and
+// are 18 tiles with a quarter of them masked, 500 to 670.  A cache's keys are decoded on
+// their way (1560 tokens of 12 heads over 7,800 positions: 610 TFLOP/s).  Tiles go
+// straight from memory to LDS, in two buffers with a barrier a tile (24.6 ms through
+// registers, 22.5 so); a row's halves are joined in registers and
 // the wave at its products has priority (21.5).  Blocks of 32 keys worked on in turn,
 // one's products beside the other's exponentials, spill (43 ms; heads of 64 207 us
 // against 150); bounds of a mask as constants gain nothing (22.8).

@@ -204,8 +204,8 @@ int64_t size_floats(const AttnGeom& g) { return ceil_div(int64_t(g.units) * ceil
 // is small: as much as leaves two parts for each workgroup that the device holds
 // at once (512), but 512 rows at least, for a part's sums go through the
 // workspace (no more than 64 parts of a tile, and 256 MiB).  A
-// call of eight units of 6,124 keys at most, four rows a key, heads of 64, takes
-// 231-258 us, with one part for each workgroup 245-266.
+// call of eight units of 6,124 keys at most, four rows a key, heads of 64, took
+// 231-258 us, with one part for each workgroup 245-266 (the same lengths).
 void backward_shape(AttnGradArgs* a)
 {
     AttnGeom& g = a->g;
