@@ -6,7 +6,9 @@ import pytest
 import torch
 
 import ulysses_all_re_amd as ua
-from tests.test_gpu_attention import DEV, E4M3, E5M2, TYPES, as_args, gpu, ints, make_cache, note, values  # noqa: F401
+from tests import attn_reference as ref
+from tests.test_gpu_attention import (DEV, E4M3, E5M2, TYPES, as_args, gpu, inputs, ints, make_cache, note,  # noqa: F401
+                                      values)
 
 pytestmark = pytest.mark.gpu
 
@@ -286,3 +288,37 @@ def test_means_of_the_largest_values(t):
     for x in (torch.finfo(dtype).max, -torch.finfo(dtype).max, float("inf"), float("-inf")):
         v = torch.full(plan.out_shape(0), x, dtype=dtype, device=DEV)
         assert torch.equal(plan.window_attention(q, k, v, **as_args(window)).out, v), x
+
+
+# (w, B, S, H, D), key heads, window, counts
+PARTS = [((1, 1, 3000, 1, 64), 1, (None, 0, 0, 1), None), ((1, 2, 2500, 2, 128), 1, (None, None, 0, 1), [1700, 2500]),
+         ((2, 1, 2000, 4, 32), 4, (64, 0, 5, 1), None), ((1, 1, 5000, 8, 32), 8, (1, 1, 200, 50), [4321]),
+         ((2, 2, 700, 12, 96), 4, (300, 20, 150, 1), [1, 1399])]
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp16"])
+@pytest.mark.parametrize("shape,kv,window,counts", PARTS, ids=lambda v: str(v).replace(" ", ""))
+def test_gradients_of_rows_of_every_size(shape, kv, window, counts, t):
+    """Rows' gradients from 1e-4 to 10 in one call, walked in parts, with shared key heads,
+    sinks and padding: each row's dq beside its own rounding, dk and dv within the
+    definition's bounds, and the same bits again."""
+    dtype = TYPES[t]
+    w, B, S, H, D = shape
+    plan = ua.Plan(*shape, dtype, device=DEV)
+    q, k, v = inputs(shape, kv, dtype, 6, 1.0)
+    rows = 10.0 ** (torch.arange(S * w, device=DEV) * 7 % 6 - 4.0)
+    dout = (values(q.shape, torch.float32, 44) * rows.view(1, 1, -1, 1, 1)).to(dtype)
+    n = None if counts is None else ints(counts)
+    r = plan.window_attention(q, k, v, counts=n, lse=True, **as_args(window))
+    got = plan.window_attention_backward(dout, q, k, v, r.out, r.lse, counts=n, **as_args(window))
+    ref.check_backward(got, dout, q, k, v, r.out, r.lse, window, D ** -0.5, counts, f"{shape}")
+    again = plan.window_attention_backward(dout, q, k, v, r.out, r.lse, counts=n, **as_args(window))
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    for (rank, b, h, m), row in ref.rows_of(q, k, v, window, D ** -0.5, counts):
+        if m < 100:
+            continue
+        (dq, _, _), _ = ref.backward(row, r.out[rank, b, :m, h], dout[rank, b, :m, h], r.lse[rank, b, h, :m], dtype)
+        for size in range(6):
+            of = rows[:m] == rows[size]
+            off, own = (float((y.double() - dq)[of].norm()) for y in (got.dq[rank, b, :m, h], dq.to(dtype)))
+            assert off <= 1.2 * own, (rank, b, h, float(rows[size]), off, own)
